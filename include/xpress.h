@@ -287,6 +287,137 @@ xpress_status xpress_jacobi_step_graph(const xpress_weights* w, const xpress_bf1
 xpress_status xpress_graph_launch(void* graph, xpress_stream stream);
 xpress_status xpress_graph_destroy(void* graph);
 
+/* ---------------------------------------------------------------------------------------------
+ * The target's side of a draft step: a paged K/V cache, attention of the drafted blocks over it,
+ * and the verification of the drafts. One turn of a batch is
+ *   xpress_jacobi_step                  drafts B-1 tokens a request;
+ *   xpress_cache_extend                 room for the block's B tokens (anchor and drafts);
+ *   xpress_cache_append, xpress_block_attention   once a layer of the target;
+ *   xpress_verify_draft                 which drafts stand, and the next token;
+ *   xpress_cache_trim                   gives back the refused drafts' tokens.
+ * The conventions above hold (device pointers, stream order, nothing allocated, host-side argument
+ * errors, N == 0 is a no-op). Page tables, lengths and counts live on the device and are read when
+ * the kernels run, so a captured turn follows them from replay to replay.
+ * ------------------------------------------------------------------------------------------- */
+
+/* Element types of the tensors below that are passed as void*. */
+#define XPRESS_BF16 0u
+#define XPRESS_F16 1u
+#define XPRESS_F32 2u
+
+/* A paged cache: a pool of pages of `page` tokens, and `rows` sequences. Sequence r holds len[r]
+ * tokens; its token t is line t % page of page table[r*table_ld + t/page] (the same page id in
+ * every layer). Entries of a row past its last page are -1. ref[p] is the number of rows that hold
+ * page p (0: the page is free). The caller owns every buffer and starts with ref = 0, len = 0 and
+ * table = -1; the calls below keep them so.
+ * Limits: n_layers >= 1; 1 <= n_pages <= 2^24; page in {16, 32, 64, 128, 256}; 1 <= Hkv <= 256; D
+ * in {64, 128, 256}; 1 <= rows <= 2^20; 1 <= table_ld <= 2^20; dtype XPRESS_BF16 or XPRESS_F16; k
+ * and v 16-byte aligned, table, len and ref 4-byte aligned.
+ * Lists of rows (`seq`, `src`, `dst`) are int32 on the device. seq NULL means rows 0..N-1. A row
+ * outside [0, rows) is skipped. A row twice in one list is the caller's error (the metadata is
+ * then unspecified; nothing outside the buffers is touched). A page id outside [0, n_pages) in
+ * the used part of a table is too: it is clamped where it is read and never counted. */
+typedef struct {
+  int32_t n_layers, n_pages, page, Hkv, D;
+  uint32_t dtype;
+  int32_t rows, table_ld;
+  void* k;        /* [n_layers, n_pages, Hkv, page, D] */
+  void* v;        /* [n_layers, n_pages, Hkv, page, D] */
+  int32_t* table; /* [rows, table_ld] */
+  int32_t* len;   /* [rows] */
+  int32_t* ref;   /* [n_pages] */
+} xpress_cache;
+
+/* Bytes of workspace of xpress_cache_extend for up to n_max rows, and of xpress_cache_compact. */
+xpress_status xpress_cache_workspace_size(const xpress_cache* c, int32_t n_max, size_t* bytes);
+
+/* Fork: row dst[i] becomes a copy of row src[i] for i < n, sharing all its pages (their counts go
+ * up; no token is copied: xpress_cache_extend copies a shared last page when it is written next).
+ * What dst[i] held before is released. src and dst have no row in common; src may repeat. */
+xpress_status xpress_cache_fork(const xpress_cache* c, const int32_t* src, const int32_t* dst,
+                                int32_t n, xpress_stream stream);
+
+/* Extension: row seq[i] grows by add[i] tokens (add NULL: by add_all; a negative count is 0) for
+ * i < N. A row whose last page is partly filled and has ref > 1 when the call starts gets a page
+ * of its own for it first, with a copy of the old one (all layers, K and V); then pages for the
+ * new tokens. Pages are taken in ascending id order among those with ref = 0 when the call
+ * starts, rows in list order. *lacking (device, written): 0, or the number of pages that are
+ * missing, or -1 where a row would pass table_ld pages; in both latter cases nothing is changed,
+ * and the caller must not write the tokens it asked room for. */
+xpress_status xpress_cache_extend(const xpress_cache* c, const int32_t* seq, int32_t N,
+                                  const int32_t* add, int32_t add_all, int32_t* lacking, void* ws,
+                                  size_t ws_bytes, xpress_stream stream);
+
+/* Writes K and V of one layer for the last B tokens of each row: token b of list entry i goes to
+ * position len[seq[i]] - B + b (skipped where that is negative). k_new, v_new: token i*B + b at
+ * element (i*B + b)*ld_new, [Hkv, D] dense, the cache's dtype, 16-byte aligned, ld_new a multiple
+ * of 8 and at least Hkv*D (so slices of a fused projection's output can be passed). */
+xpress_status xpress_cache_append(const xpress_cache* c, int32_t layer, const void* k_new,
+                                  const void* v_new, int64_t ld_new, const int32_t* seq, int32_t N,
+                                  int32_t B, xpress_stream stream);
+
+/* Freeing: row seq[i] loses its last drop[i] tokens (clamped to [0, len]; drop NULL: all of them);
+ * pages that hold none of its tokens any more leave its table and their counts go down. */
+xpress_status xpress_cache_trim(const xpress_cache* c, const int32_t* seq, int32_t N,
+                                const int32_t* drop, xpress_stream stream);
+
+/* Compaction: with L = number of pages with ref > 0, the live pages with ids >= L (ascending) move
+ * to the free ids < L (ascending), in every layer; counts and the tables of all rows follow.
+ * *live (device, written) = L: pages L.. are free afterwards. */
+xpress_status xpress_cache_compact(const xpress_cache* c, int32_t* live, void* ws, size_t ws_bytes,
+                                   xpress_stream stream);
+
+/* Attention of a block of B query tokens a request over one layer of the cache, for a batch whose
+ * rows begin with the same `shared` tokens (0: none):
+ *   out[i, b, h] = sum_t softmax_t(scale * q[i, b, h] . k[t, h / (Hq/Hkv)]) v[t, h / (Hq/Hkv)]
+ * over the tokens t = 0 .. len[seq[i]] - B + b of row seq[i] (the block's own tokens are the
+ * row's last B, so the mask is causal inside the block; B = 1 is plain decoding). The first
+ * `shared` tokens are read once for all query rows, through the first request's table: the caller
+ * vouches that every row's first min(shared, len) tokens are the same. The result is that of
+ * attending over each row alone. A query that sees no token gives 0 (and lse = -inf).
+ * q: token i*B + b at element (i*B + b)*q_ld, [Hq, D] dense; out likewise with out_ld; both of the
+ * cache's dtype, 16-byte aligned, strides multiples of 8. lse: [N*B, Hq] fp32, nullable, the
+ * natural log of the sum of exp(scale * q.k). Hq a multiple of Hkv; B >= 1; N*B*Hq < 2^31;
+ * 0 < scale <= 1e6; 0 <= shared <= table_ld*page. Scores below -1e30 / scale count as masked.
+ * Values in masked places (beyond a row's end, in later tokens of the block) do not reach the
+ * result, whatever they are. */
+xpress_status xpress_attention_workspace_size(const xpress_cache* c, int32_t n_max, int32_t B,
+                                              int32_t Hq, size_t* bytes);
+xpress_status xpress_block_attention(const xpress_cache* c, int32_t layer, const void* q,
+                                     int64_t q_ld, const int32_t* seq, int32_t N, int32_t B,
+                                     int32_t Hq, float scale, int32_t shared, void* out,
+                                     int64_t out_ld, float* lse, void* ws, size_t ws_bytes,
+                                     xpress_stream stream);
+
+/* Verification of drafted blocks. Row i*B + s of logits is the target's distribution for slot s+1
+ * of block i, p_s = softmax(x / temperature[i]). Draft d = blk[i, s+1] stands iff
+ *   u[i, s] * q_s(d) < p_s(d),
+ * for s = 0, 1, .. up to the first refusal or to draft_len[i] drafts (draft_len NULL: B-1; clamped
+ * to [0, B-1]). accepted[i] = a of them stand; out[i, s] = blk[i, s+1] for s < a; out[i, a] is one
+ * more token, and the slots after it are -1. That token is the lowest id v whose running sum of
+ * weights (ids ascending) passes u[i, B-1] times the sum of all, with the weights
+ *   max(p_a - q_a, 0) when the draft of slot a+1 was refused (where they are all 0: p_a);
+ *   p_a when no draft was left to test.
+ * q: the drafts' own probabilities, row i*(B-1) + s for slot s+1; NULL for drafts that were not
+ * drawn (argmax, as xpress_jacobi_step's): q_s is then 1 at the draft and 0 elsewhere.
+ * temperature[i] = 0 (or temperature NULL): greedy, a draft stands iff it is the row's argmax
+ * (lowest id on ties) and the token is the argmax of row a; u and q are not used. Negative or NaN
+ * temperatures count as 0.
+ * A logit of -inf or NaN has no weight; at +inf the ids that hold it share all of it. In a row
+ * without any weight the draft is refused and the token is -1. Drafts outside [0, V) are refused.
+ * drop[i] (nullable) = B-1-a, what xpress_cache_trim takes after the block's B tokens were
+ * appended. u: [N, B] fp32 in [0, 1) (nullable if temperature is NULL). blk: [N, B] int64;
+ * out: [N, B] int64; accepted, drop: [N] int32; logits and q: XPRESS_BF16, _F16 or _F32 with row
+ * strides ld >= V and q_ld >= V in elements, any alignment of the rows to their own elements.
+ * 1 <= B <= 64; 1 <= V < 2^31. Deterministic: the same inputs give the same tokens. */
+xpress_status xpress_verify_workspace_size(int32_t n_max, int32_t B, int64_t V, size_t* bytes);
+xpress_status xpress_verify_draft(const void* logits, uint32_t logits_dtype, int64_t ld,
+                                  const int64_t* blk, const int32_t* draft_len, const void* q,
+                                  uint32_t q_dtype, int64_t q_ld, const float* temperature,
+                                  const float* u, int32_t N, int32_t B, int64_t V, int64_t* out,
+                                  int32_t* accepted, int32_t* drop, void* ws, size_t ws_bytes,
+                                  xpress_stream stream);
+
 /* Message of the last non-OK status returned on the calling thread ("" if none). */
 const char* xpress_last_error(void);
 

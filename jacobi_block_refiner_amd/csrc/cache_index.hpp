@@ -1,0 +1,46 @@
+// Index arithmetic of the paged cache, shared by its kernels and the attention that reads it.
+// Plain integer functions (no device built-ins), so they compile for the host too.
+#pragma once
+
+#include <stdint.h>
+
+#if defined(__HIPCC__)
+#define XP_HD __host__ __device__ __forceinline__
+#else
+#define XP_HD inline
+#endif
+
+namespace xpress {
+
+// Pages that hold n tokens (n >= 0).
+XP_HD int pages_of(int64_t n, int page_shift) {
+  return (int)((n + ((int64_t)1 << page_shift) - 1) >> page_shift);
+}
+
+// A row's token count as the kernels use it: inside what its table can hold, whatever the buffer
+// says.
+XP_HD int clamp_len(int len, int64_t table_ld, int page_shift) {
+  const int64_t most = table_ld << page_shift;
+  const int64_t v = len < 0 ? 0 : len;
+  return (int)(v < most ? v : most);
+}
+
+// A page id as the kernels use it for an address: inside the pool.
+XP_HD int clamp_page(int id, int n_pages) {
+  return id < 0 ? 0 : (id < n_pages ? id : n_pages - 1);
+}
+XP_HD bool page_ok(int id, int n_pages) { return id >= 0 && id < n_pages; }
+
+// Element offset of line `line` of page `id`, head `h`, inside one layer of K or V. 64 bits: a
+// layer of 2^16 pages of 64 tokens, 8 heads of 128 already holds 2^32 elements.
+XP_HD int64_t line_offset(int id, int h, int line, int Hkv, int page_shift, int D) {
+  return ((((int64_t)id * Hkv + h) << page_shift) + line) * D;
+}
+
+// Tokens in the sight of query b of a block of B that ends its row of `len` tokens.
+XP_HD int in_sight(int len, int B, int b) {
+  const int64_t v = (int64_t)len - B + b + 1;
+  return v < 0 ? 0 : (int)v;
+}
+
+}  // namespace xpress

@@ -1,0 +1,361 @@
+// Pages of the K/V cache (gfx950): fork, extension with copy on write, append, freeing and
+// compaction. The metadata (tables, lengths, counts) is integer work of a few KB; the copies are
+// plain 16-byte streams.
+#include "serve.hpp"
+#include "cache_index.hpp"
+
+#include <limits.h>
+
+namespace xpress {
+
+namespace {
+
+constexpr int kPlan = 1024;  // threads of the single workgroup that plans an allocation
+
+int shift_of(int page) { return __builtin_ctz((unsigned)page); }
+
+// What the kernels need of an xpress_cache.
+struct Pages {
+  int32_t *table, *len, *ref;
+  int rows, ld, n_pages, shift;
+};
+
+Pages pages(const xpress_cache& c) {
+  return Pages{c.table, c.len, c.ref, c.rows, c.table_ld, c.n_pages, shift_of(c.page)};
+}
+
+__device__ __forceinline__ int row_of(const int32_t* seq, int i, int rows) {
+  const int r = seq ? seq[i] : i;
+  return (unsigned)r < (unsigned)rows ? r : -1;
+}
+
+// Exclusive prefix sum over the workgroup's kPlan threads; *total gets the sum.
+__device__ int block_scan(int v, int* total) {
+  __shared__ int s_part[kPlan / 64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  int x = v;
+#pragma unroll
+  for (int d = 1; d < 64; d *= 2) {
+    const int y = __shfl_up(x, d);
+    if (lane >= d) x += y;
+  }
+  __syncthreads();  // the previous call's s_part has been read
+  if (lane == 63) s_part[w] = x;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kPlan / 64; ++i) {
+    const int p = s_part[i];
+    before += i < w ? p : 0;
+    all += p;
+  }
+  *total = all;
+  return before + x - v;
+}
+
+__global__ __launch_bounds__(256) void fork_kernel(Pages P, const int32_t* src, const int32_t* dst) {
+  const int from = row_of(src, blockIdx.x, P.rows), to = row_of(dst, blockIdx.x, P.rows);
+  if (from < 0 || to < 0 || from == to) return;
+  const int old_len = clamp_len(P.len[to], P.ld, P.shift);
+  const int new_len = clamp_len(P.len[from], P.ld, P.shift);
+  const int old_pages = pages_of(old_len, P.shift), new_pages = pages_of(new_len, P.shift);
+  __syncthreads();  // every thread has read both lengths
+  const int32_t* a = P.table + (int64_t)from * P.ld;
+  int32_t* b = P.table + (int64_t)to * P.ld;
+  for (int j = threadIdx.x; j < P.ld; j += blockDim.x) {
+    const int old = b[j], id = a[j];
+    if (j < old_pages && page_ok(old, P.n_pages)) atomicSub(&P.ref[old], 1);
+    if (j < new_pages && page_ok(id, P.n_pages)) atomicAdd(&P.ref[id], 1);
+    b[j] = id;
+  }
+  if (threadIdx.x == 0) P.len[to] = new_len;
+}
+
+__global__ __launch_bounds__(256) void trim_kernel(Pages P, const int32_t* seq,
+                                                   const int32_t* drop) {
+  const int r = row_of(seq, blockIdx.x, P.rows);
+  if (r < 0) return;
+  const int len = clamp_len(P.len[r], P.ld, P.shift);
+  const int d = drop ? min(max(drop[blockIdx.x], 0), len) : len;
+  __syncthreads();  // every thread has read the length
+  int32_t* t = P.table + (int64_t)r * P.ld;
+  const int keep = pages_of(len - d, P.shift), had = pages_of(len, P.shift);
+  for (int j = keep + threadIdx.x; j < had; j += blockDim.x) {
+    const int id = t[j];
+    if (page_ok(id, P.n_pages)) atomicSub(&P.ref[id], 1);
+    t[j] = -1;
+  }
+  if (threadIdx.x == 0) P.len[r] = len - d;
+}
+
+// What a row asks for: whether its partly filled last page is shared (cow), and its pages.
+struct Need {
+  int len, after, first, count;  // new pages go to table entries first .. first+count-1
+  bool cow;
+};
+__device__ Need need_of(const Pages& P, const int32_t* seq, const int32_t* add, int add_all, int i,
+                        int* r_out) {
+  Need n{0, 0, 0, 0, false};
+  const int r = row_of(seq, i, P.rows);
+  *r_out = r;
+  if (r < 0) return n;
+  n.len = clamp_len(P.len[r], P.ld, P.shift);
+  const int64_t after = (int64_t)n.len + max(add ? add[i] : add_all, 0);
+  if (after > ((int64_t)P.ld << P.shift)) {
+    n.count = -1;
+    return n;
+  }
+  n.after = (int)after;
+  n.first = pages_of(n.len, P.shift);
+  if (after > n.len && (n.len & ((1 << P.shift) - 1))) {
+    const int id = P.table[(int64_t)r * P.ld + n.first - 1];
+    n.cow = page_ok(id, P.n_pages) && P.ref[id] > 1;
+  }
+  n.first -= n.cow;
+  n.count = pages_of(after, P.shift) - n.first;
+  return n;
+}
+
+// Scratch of an extension: how many copies there are at most (0 where nothing is changed); by list
+// entry the copy's source (-1: none) and target, the first table entry and the number of the new
+// pages and their offset in the list of free pages; that list.
+struct ExtendScratch {
+  int32_t *ncopy, *from, *to, *first, *count, *offset, *free_ids;
+};
+constexpr int kExtendPerRow = 5;
+__host__ __device__ inline ExtendScratch extend_scratch(void* ws, int N) {
+  int32_t* p = static_cast<int32_t*>(ws);
+  const int64_t n = N;
+  return ExtendScratch{p,         p + 4,         p + 4 + n,     p + 4 + 2 * n, p + 4 + 3 * n,
+                       p + 4 + 4 * n, p + 4 + 5 * n};
+}
+
+// One workgroup: the rows' needs in list order (prefix sums), the first `total` free pages in id
+// order, then the tables. The whole plan is made before anything is written.
+__global__ __launch_bounds__(kPlan) void extend_kernel(Pages P, const int32_t* seq, int N,
+                                                       const int32_t* add, int add_all,
+                                                       int32_t* lacking, void* ws) {
+  const ExtendScratch S = extend_scratch(ws, N);
+  const int t = threadIdx.x;
+  __shared__ int s_over;
+  if (t == 0) s_over = 0;
+  __syncthreads();
+  int64_t total = 0;
+  for (int i0 = 0; i0 < N; i0 += kPlan) {
+    const int i = i0 + t;
+    int r, all;
+    const Need n = i < N ? need_of(P, seq, add, add_all, i, &r) : Need{0, 0, 0, 0, false};
+    if (n.count < 0) s_over = 1;
+    const int at = block_scan(max(n.count, 0), &all);
+    if (i < N) {
+      S.offset[i] = (int)min(total + at, (int64_t)P.n_pages);
+      S.first[i] = n.first;
+      S.count[i] = n.count;
+      S.from[i] = n.cow ? P.table[(int64_t)r * P.ld + n.first] : -1;
+    }
+    total += all;
+  }
+  __syncthreads();
+  int found = 0;
+  const int want = (int)min(total, (int64_t)P.n_pages);
+  if (!s_over)
+    for (int p0 = 0; p0 < P.n_pages && found < want; p0 += kPlan) {
+      const int p = p0 + t;
+      int all;
+      const bool is_free = p < P.n_pages && P.ref[p] == 0;
+      const int k = found + block_scan(is_free, &all);
+      if (is_free && k < want) S.free_ids[k] = p;
+      found += all;
+    }
+  const bool no = s_over || found < total;
+  if (t == 0) {
+    *lacking = s_over ? -1 : found < total ? (int)(total - found) : 0;
+    *S.ncopy = no ? 0 : N;
+  }
+  if (no) return;
+  __syncthreads();
+  for (int i0 = 0; i0 < N; i0 += kPlan) {
+    const int i = i0 + t;
+    if (i >= N) continue;
+    const int r = row_of(seq, i, P.rows);
+    if (r < 0) continue;
+    const int old = S.from[i], first = S.first[i], count = S.count[i];
+    int32_t* row = P.table + (int64_t)r * P.ld;
+    for (int j = 0; j < count; ++j) {
+      const int id = S.free_ids[S.offset[i] + j];
+      row[first + j] = id;
+      P.ref[id] = 1;
+    }
+    if (old >= 0) {
+      atomicSub(&P.ref[old], 1);
+      S.to[i] = row[first];
+    }
+    const int64_t after = (int64_t)clamp_len(P.len[r], P.ld, P.shift) + max(add ? add[i] : add_all, 0);
+    P.len[r] = clamp_len((int)min(after, (int64_t)INT_MAX), P.ld, P.shift);
+  }
+}
+
+// Copies pages from[i] -> to[i], i < *count, in every layer of K and V. One workgroup per (page,
+// layer and side) at a time; `chunks` 16-byte pieces per page.
+__global__ __launch_bounds__(256) void copy_pages_kernel(const int32_t* __restrict__ count,
+                                                         const int32_t* __restrict__ from,
+                                                         const int32_t* __restrict__ to,
+                                                         uint4* k, uint4* v, int n_layers,
+                                                         int64_t n_pages, int64_t chunks) {
+  const int64_t items = (int64_t)*count * n_layers * 2;
+  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
+    const int i = (int)(it / (n_layers * 2)), side = (int)(it % (n_layers * 2));
+    const int a = from[i];
+    if (a < 0) continue;
+    uint4* pool = (side & 1 ? v : k) + (int64_t)(side >> 1) * n_pages * chunks;
+    const uint4* x = pool + a * chunks;
+    uint4* y = pool + to[i] * chunks;
+    for (int64_t j = threadIdx.x; j < chunks; j += blockDim.x) y[j] = x[j];
+  }
+}
+
+__global__ __launch_bounds__(256) void append_kernel(Pages P, uint16_t* k, uint16_t* v,
+                                                     const uint16_t* __restrict__ k_new,
+                                                     const uint16_t* __restrict__ v_new,
+                                                     int64_t ld_new, const int32_t* seq, int N,
+                                                     int B, int Hkv, int D) {
+  const int per = Hkv * D / 8;  // 16-byte pieces of a token
+  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
+  if (i >= (int64_t)N * B * per) return;
+  const int64_t token = i / per;
+  const int piece = (int)(i % per), e = (int)(token / B), b = (int)(token % B);
+  const int r = row_of(seq, e, P.rows);
+  if (r < 0) return;
+  const int pos = in_sight(clamp_len(P.len[r], P.ld, P.shift), B, b) - 1;
+  if (pos < 0) return;
+  const int id = P.table[(int64_t)r * P.ld + (pos >> P.shift)];
+  if (!page_ok(id, P.n_pages)) return;
+  const int h = piece * 8 / D, d = piece * 8 % D;
+  const int64_t to = line_offset(id, h, pos & ((1 << P.shift) - 1), Hkv, P.shift, D) + d;
+  const uint16_t* x = (blockIdx.y ? v_new : k_new) + token * ld_new + piece * 8;
+  *reinterpret_cast<uint4*>((blockIdx.y ? v : k) + to) = *reinterpret_cast<const uint4*>(x);
+}
+
+// Scratch of a compaction: the number of moves, the moves, and where each page goes.
+struct CompactScratch {
+  int32_t *nmove, *from, *to, *place;
+};
+__host__ __device__ inline CompactScratch compact_scratch(void* ws, int n_pages) {
+  int32_t* p = static_cast<int32_t*>(ws);
+  return CompactScratch{p, p + 4, p + 4 + n_pages, p + 4 + 2 * (int64_t)n_pages};
+}
+
+__global__ __launch_bounds__(kPlan) void compact_plan_kernel(Pages P, int32_t* live, void* ws) {
+  const CompactScratch S = compact_scratch(ws, P.n_pages);
+  const int t = threadIdx.x;
+  int L = 0;
+  for (int p0 = 0; p0 < P.n_pages; p0 += kPlan) {
+    int all;
+    block_scan(p0 + t < P.n_pages && P.ref[p0 + t] > 0, &all);
+    L += all;
+  }
+  int nfrom = 0, nto = 0;
+  for (int p0 = 0; p0 < P.n_pages; p0 += kPlan) {
+    const int p = p0 + t;
+    const bool alive = p < P.n_pages && P.ref[p] > 0;
+    const bool out = alive && p >= L, in = p < P.n_pages && !alive && p < L;
+    int all;
+    const int a = nfrom + block_scan(out, &all);
+    nfrom += all;
+    const int b = nto + block_scan(in, &all);
+    nto += all;
+    if (out) S.from[a] = p;
+    if (in) S.to[b] = p;
+  }
+  __syncthreads();
+  for (int i = t; i < nfrom; i += kPlan) {
+    const int a = S.from[i], b = S.to[i];
+    S.place[a] = b;
+    P.ref[b] = P.ref[a];
+    P.ref[a] = 0;
+  }
+  if (t == 0) {
+    *live = L;
+    *S.nmove = nfrom;
+  }
+}
+
+__global__ __launch_bounds__(256) void compact_tables_kernel(Pages P, const int32_t* live,
+                                                             void* ws) {
+  const CompactScratch S = compact_scratch(ws, P.n_pages);
+  const int r = blockIdx.x, L = *live;
+  const int n = pages_of(clamp_len(P.len[r], P.ld, P.shift), P.shift);
+  int32_t* t = P.table + (int64_t)r * P.ld;
+  for (int j = threadIdx.x; j < n; j += blockDim.x) {
+    const int id = t[j];
+    if (page_ok(id, P.n_pages) && id >= L) t[j] = S.place[id];
+  }
+}
+
+hipError_t launch_copy(const xpress_cache& c, const int32_t* count, const int32_t* from,
+                       const int32_t* to, int64_t most, hipStream_t s) {
+  const int64_t chunks = (int64_t)c.Hkv * c.page * c.D * 2 / 16;
+  const int64_t items = most * c.n_layers * 2;
+  hipLaunchKernelGGL(copy_pages_kernel, dim3((unsigned)(items < 2048 ? items : 2048)), dim3(256),
+                     0, s, count, from, to, static_cast<uint4*>(c.k), static_cast<uint4*>(c.v),
+                     c.n_layers, (int64_t)c.n_pages, chunks);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t cache_scratch_bytes(const xpress_cache& c, int n_max) {
+  const size_t extend = 4 * (4 + kExtendPerRow * (size_t)n_max + c.n_pages);
+  const size_t compact = 4 * (4 + 3 * (size_t)c.n_pages);
+  return extend > compact ? extend : compact;
+}
+
+hipError_t launch_cache_fork(const xpress_cache& c, const int32_t* src, const int32_t* dst, int n,
+                             hipStream_t s) {
+  hipLaunchKernelGGL(fork_kernel, dim3(n), dim3(256), 0, s, pages(c), src, dst);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_extend(const xpress_cache& c, const int32_t* seq, int N,
+                               const int32_t* add, int add_all, int32_t* lacking, void* ws,
+                               hipStream_t s) {
+  hipLaunchKernelGGL(extend_kernel, dim3(1), dim3(kPlan), 0, s, pages(c), seq, N, add, add_all,
+                     lacking, ws);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const ExtendScratch S = extend_scratch(ws, N);
+  return launch_copy(c, S.ncopy, S.from, S.to, N, s);
+}
+
+hipError_t launch_cache_append(const xpress_cache& c, int layer, const void* k_new,
+                               const void* v_new, int64_t ld_new, const int32_t* seq, int N, int B,
+                               hipStream_t s) {
+  const int64_t n = (int64_t)N * B * (c.Hkv * c.D / 8);
+  const int64_t layer_elems = (int64_t)c.n_pages * c.Hkv * c.page * c.D;
+  hipLaunchKernelGGL(append_kernel, dim3((unsigned)((n + 255) / 256), 2), dim3(256), 0, s,
+                     pages(c), static_cast<uint16_t*>(c.k) + layer * layer_elems,
+                     static_cast<uint16_t*>(c.v) + layer * layer_elems,
+                     static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new),
+                     ld_new, seq, N, B, c.Hkv, c.D);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_trim(const xpress_cache& c, const int32_t* seq, int N, const int32_t* drop,
+                             hipStream_t s) {
+  hipLaunchKernelGGL(trim_kernel, dim3(N), dim3(256), 0, s, pages(c), seq, drop);
+  return hipGetLastError();
+}
+
+hipError_t launch_cache_compact(const xpress_cache& c, int32_t* live, void* ws, hipStream_t s) {
+  hipLaunchKernelGGL(compact_plan_kernel, dim3(1), dim3(kPlan), 0, s, pages(c), live, ws);
+  hipError_t e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(compact_tables_kernel, dim3(c.rows), dim3(256), 0, s, pages(c),
+                     static_cast<const int32_t*>(live), ws);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  const CompactScratch S = compact_scratch(ws, c.n_pages);
+  return launch_copy(c, S.nmove, S.from, S.to, (c.n_pages + 1) / 2, s);
+}
+
+}  // namespace xpress

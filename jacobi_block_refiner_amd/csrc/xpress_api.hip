@@ -8,9 +8,14 @@
 #include <mutex>
 #include <string>
 
+#include "api_common.hpp"
 #include "launch.hpp"
 
 namespace {
+
+using xpress::aligned16;
+using xpress::fail;
+using xpress::up256;
 
 // Scratch is sized for the widest supported MLP (M = 1024) and hidden size, so
 // xpress_workspace_size does not depend on M or H.
@@ -19,45 +24,8 @@ constexpr int kMaxH = 16384;
 
 thread_local std::string g_err;
 
-xpress_status fail(xpress_status st, const char* fmt, ...) {
-  char buf[512];
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(buf, sizeof buf, fmt, ap);
-  va_end(ap);
-  g_err = buf;
-  return st;
-}
-
-xpress_status hip_check(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(XPRESS_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  return XPRESS_OK;
-}
-
-#define XP_TRY(expr, what)                                   \
-  do {                                                       \
-    xpress_status st_ = hip_check((expr), (what));           \
-    if (st_ != XPRESS_OK) return st_;                        \
-  } while (0)
-
-bool aligned16(const void* p) { return ((uintptr_t)p & 15u) == 0; }
-
 // The readout's base copies address 16 rows from one scalar pointer with 32-bit lane offsets.
 constexpr int64_t kMaxBaseLd = (int64_t)1 << 27;
-
-size_t up256(size_t x) { return (x + 255) & ~(size_t)255; }
-
-xpress_status check_ptr(const void* p, const char* name) {
-  if (p == nullptr) return fail(XPRESS_ERR_ARG, "%s is NULL", name);
-  if (!aligned16(p)) return fail(XPRESS_ERR_ARG, "%s is not 16-byte aligned", name);
-  return XPRESS_OK;
-}
-
-#define XP_PTR(p)                                        \
-  do {                                                   \
-    xpress_status st_ = check_ptr((p), #p);              \
-    if (st_ != XPRESS_OK) return st_;                    \
-  } while (0)
 
 xpress_status check_dims(int B, int r, int64_t V) {
   if (B < 2 || B > 16) return fail(XPRESS_ERR_ARG, "B=%d outside [2, 16]", B);
@@ -201,6 +169,31 @@ xpress_status scratch_ptr(void** out) {
 }
 
 }  // namespace
+
+namespace xpress {
+
+xpress_status fail(xpress_status st, const char* fmt, ...) {
+  char buf[512];
+  va_list ap;
+  va_start(ap, fmt);
+  vsnprintf(buf, sizeof buf, fmt, ap);
+  va_end(ap);
+  g_err = buf;
+  return st;
+}
+
+xpress_status hip_check(hipError_t e, const char* what) {
+  if (e != hipSuccess) return fail(XPRESS_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
+  return XPRESS_OK;
+}
+
+xpress_status check_ptr(const void* p, const char* name) {
+  if (p == nullptr) return fail(XPRESS_ERR_ARG, "%s is NULL", name);
+  if (!aligned16(p)) return fail(XPRESS_ERR_ARG, "%s is not 16-byte aligned", name);
+  return XPRESS_OK;
+}
+
+}  // namespace xpress
 
 extern "C" {
 

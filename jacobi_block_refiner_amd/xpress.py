@@ -40,6 +40,16 @@ class _Weights(ctypes.Structure):
     ]
 
 
+class _Cache(ctypes.Structure):
+    _fields_ = [
+        ("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32),
+        ("Hkv", ctypes.c_int32), ("D", ctypes.c_int32), ("dtype", ctypes.c_uint32),
+        ("rows", ctypes.c_int32), ("table_ld", ctypes.c_int32),
+        ("k", ctypes.c_void_p), ("v", ctypes.c_void_p),
+        ("table", ctypes.c_void_p), ("len", ctypes.c_void_p), ("ref", ctypes.c_void_p),
+    ]
+
+
 _lib = None
 
 
@@ -58,7 +68,8 @@ def lib() -> ctypes.CDLL:
                 f"{LIB_PATH} is missing: build it with jacobi_block_refiner_amd.build.build()")
         L = ctypes.CDLL(str(LIB_PATH))
         P, i32, i64, sz = ctypes.c_void_p, ctypes.c_int32, ctypes.c_int64, ctypes.c_size_t
-        W = ctypes.POINTER(_Weights)
+        f32, u32 = ctypes.c_float, ctypes.c_uint32
+        W, C = ctypes.POINTER(_Weights), ctypes.POINTER(_Cache)
         sig = {
             "xpress_workspace_size": [i32, i32, i32, i64, i32, i32, ctypes.POINTER(sz)],
             "xpress_fold_mixer": [P, i32, i32, P, P],
@@ -81,6 +92,18 @@ def lib() -> ctypes.CDLL:
                                          P, sz, ctypes.POINTER(ctypes.c_void_p)],
             "xpress_graph_launch": [P, P],
             "xpress_graph_destroy": [P],
+            "xpress_cache_workspace_size": [C, i32, ctypes.POINTER(sz)],
+            "xpress_cache_fork": [C, P, P, i32, P],
+            "xpress_cache_extend": [C, P, i32, P, i32, P, P, sz, P],
+            "xpress_cache_append": [C, i32, P, P, i64, P, i32, i32, P],
+            "xpress_cache_trim": [C, P, i32, P, P],
+            "xpress_cache_compact": [C, P, P, sz, P],
+            "xpress_attention_workspace_size": [C, i32, i32, i32, ctypes.POINTER(sz)],
+            "xpress_block_attention": [C, i32, P, i64, P, i32, i32, i32, f32, i32, P, i64, P, P,
+                                       sz, P],
+            "xpress_verify_workspace_size": [i32, i32, i64, ctypes.POINTER(sz)],
+            "xpress_verify_draft": [P, u32, i64, P, P, P, u32, i64, P, P, i32, i32, i64, P, P, P,
+                                    P, sz, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -379,3 +402,199 @@ class StepGraph:
             self.close()
         except Exception:
             pass
+
+
+# ------------------------------------------------------------- the target's side of a draft step
+
+BF16, F16, F32 = 0, 1, 2
+_DTYPES = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
+
+
+def _list(t, n: int, dtype, name: str):
+    """A device list of at least n elements of one type, as a pointer; None passes as NULL."""
+    if t is None:
+        return None
+    if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+        raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor")
+    if t.numel() < n:
+        raise ValueError(f"{name} holds {t.numel()} elements, the call needs {n}")
+    return t.data_ptr()
+
+
+def _tokens(t, n: int, width: int, dtype, name: str) -> int:
+    """A [n, width] view with unit column stride; its row stride in elements."""
+    if t.dtype != dtype or not t.is_cuda:
+        raise TypeError(f"{name} must be a CUDA {dtype} tensor")
+    if t.dim() != 2 or t.shape[0] < n or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} is {tuple(t.shape)}; the call needs [{n}, {width}] rows with unit "
+                         "column stride")
+    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+
+
+def _ws(ws):
+    if not ws.is_cuda or not ws.is_contiguous():
+        raise TypeError("ws must be a contiguous CUDA tensor")
+    return ws.data_ptr(), ws.numel() * ws.element_size()
+
+
+@dataclass
+class Cache:
+    """A paged K/V cache (``xpress_cache``): pools of pages, one table row a sequence, tokens a
+    sequence and holders a page. The caller owns the tensors; the struct is built once."""
+
+    k: torch.Tensor  # [n_layers, n_pages, Hkv, page, D] bf16 or fp16
+    v: torch.Tensor
+    table: torch.Tensor  # [rows, table_ld] int32, -1 past a row's pages
+    length: torch.Tensor  # [rows] int32
+    ref: torch.Tensor  # [n_pages] int32
+
+    def __post_init__(self):
+        if self.k.dim() != 5 or self.v.shape != self.k.shape:
+            raise ValueError("k and v must be [n_layers, n_pages, Hkv, page, D]")
+        if self.table.dim() != 2 or self.length.shape != self.table.shape[:1]:
+            raise ValueError("table must be [rows, table_ld] and length [rows]")
+        if self.ref.shape != self.k.shape[1:2]:
+            raise ValueError("ref must be [n_pages]")
+        if self.k.dtype not in (torch.bfloat16, torch.float16):
+            raise TypeError("k must be bfloat16 or float16")
+        for name, dtype in (("k", self.k.dtype), ("v", self.k.dtype), ("table", torch.int32),
+                            ("length", torch.int32), ("ref", torch.int32)):
+            t = getattr(self, name)
+            if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
+                raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor")
+        n_layers, n_pages, Hkv, page, D = self.k.shape
+        rows, ld = self.table.shape
+        self._struct = _Cache(n_layers, n_pages, page, Hkv, D, _DTYPES[self.k.dtype], rows, ld,
+                              self.k.data_ptr(), self.v.data_ptr(), self.table.data_ptr(),
+                              self.length.data_ptr(), self.ref.data_ptr())
+        self._ref = ctypes.byref(self._struct)
+
+    @classmethod
+    def empty(cls, n_layers: int, n_pages: int, Hkv: int, page: int, D: int, rows: int,
+              table_ld: int, dtype=torch.bfloat16, device="cuda") -> "Cache":
+        """An empty cache: every page free, every row of length 0. The pools are not filled."""
+        shape = (n_layers, n_pages, Hkv, page, D)
+        return cls(k=torch.empty(shape, dtype=dtype, device=device),
+                   v=torch.empty(shape, dtype=dtype, device=device),
+                   table=torch.full((rows, table_ld), -1, dtype=torch.int32, device=device),
+                   length=torch.zeros(rows, dtype=torch.int32, device=device),
+                   ref=torch.zeros(n_pages, dtype=torch.int32, device=device))
+
+    def _rows(self, seq, N, name="seq") -> int:
+        if N is None:
+            N = self.table.shape[0] if seq is None else seq.numel()
+        return N
+
+
+def cache_workspace(cache: Cache, n_max: int) -> torch.Tensor:
+    """Workspace of ``cache_extend`` for up to n_max rows and of ``cache_compact``."""
+    out = ctypes.c_size_t()
+    _check(lib().xpress_cache_workspace_size(cache._ref, n_max, ctypes.byref(out)))
+    return torch.empty(max(out.value, 256), dtype=torch.uint8, device=cache.k.device)
+
+
+def cache_fork(cache: Cache, src: torch.Tensor, dst: torch.Tensor) -> None:
+    """Row dst[i] becomes a copy of row src[i], sharing its pages."""
+    n = dst.numel()
+    _check(lib().xpress_cache_fork(cache._ref, _list(src, n, torch.int32, "src"),
+                                   _list(dst, n, torch.int32, "dst"), n, _stream()))
+
+
+def cache_extend(cache: Cache, add, *, lacking: torch.Tensor, ws: torch.Tensor, seq=None,
+                 N: int | None = None) -> torch.Tensor:
+    """Room for add tokens (an int, or an int32 tensor of one count a row) at the end of each row;
+    a shared last page is copied first. lacking (int32): 0, or why nothing was changed."""
+    N = cache._rows(seq, N)
+    each = add if isinstance(add, torch.Tensor) else None
+    ws_ptr, ws_bytes = _ws(ws)
+    _check(lib().xpress_cache_extend(cache._ref, _list(seq, N, torch.int32, "seq"), N,
+                                     _list(each, N, torch.int32, "add"),
+                                     0 if each is not None else int(add),
+                                     _list(lacking, 1, torch.int32, "lacking"), ws_ptr, ws_bytes,
+                                     _stream()))
+    return lacking
+
+
+def cache_append(cache: Cache, layer: int, k_new: torch.Tensor, v_new: torch.Tensor, *, B: int,
+                 seq=None, N: int | None = None) -> None:
+    """K and V of one layer for the last B tokens of each row; k_new, v_new: [N*B, Hkv*D] views
+    with the same row stride."""
+    N = cache._rows(seq, N)
+    width = cache.k.shape[2] * cache.k.shape[4]
+    ld = _tokens(k_new, N * B, width, cache.k.dtype, "k_new")
+    if _tokens(v_new, N * B, width, cache.k.dtype, "v_new") != ld:
+        raise ValueError("k_new and v_new must have the same row stride")
+    _check(lib().xpress_cache_append(cache._ref, layer, k_new.data_ptr(), v_new.data_ptr(), ld,
+                                     _list(seq, N, torch.int32, "seq"), N, B, _stream()))
+
+
+def cache_trim(cache: Cache, drop=None, *, seq=None, N: int | None = None) -> None:
+    """Row seq[i] loses its last drop[i] tokens (drop None: all of them)."""
+    N = cache._rows(seq, N)
+    _check(lib().xpress_cache_trim(cache._ref, _list(seq, N, torch.int32, "seq"), N,
+                                   _list(drop, N, torch.int32, "drop"), _stream()))
+
+
+def cache_compact(cache: Cache, *, live: torch.Tensor, ws: torch.Tensor) -> torch.Tensor:
+    """Moves the live pages to the front of the pools; live (int32) gets their number."""
+    ws_ptr, ws_bytes = _ws(ws)
+    _check(lib().xpress_cache_compact(cache._ref, _list(live, 1, torch.int32, "live"), ws_ptr,
+                                      ws_bytes, _stream()))
+    return live
+
+
+def attention_workspace(cache: Cache, n_max: int, B: int, Hq: int) -> torch.Tensor:
+    out = ctypes.c_size_t()
+    _check(lib().xpress_attention_workspace_size(cache._ref, n_max, B, Hq, ctypes.byref(out)))
+    return torch.empty(max(out.value, 256), dtype=torch.uint8, device=cache.k.device)
+
+
+def block_attention(cache: Cache, layer: int, q: torch.Tensor, *, B: int, Hq: int,
+                    out: torch.Tensor, ws: torch.Tensor, shared: int = 0,
+                    scale: float | None = None, seq=None, N: int | None = None,
+                    lse: torch.Tensor | None = None) -> torch.Tensor:
+    """Attention of the last B tokens of each row over one layer; q and out: [N*B, Hq*D] views.
+    The first ``shared`` tokens, common to all rows, are read once. scale defaults to D**-0.5."""
+    N = cache._rows(seq, N)
+    D = cache.k.shape[4]
+    q_ld = _tokens(q, N * B, Hq * D, cache.k.dtype, "q")
+    out_ld = _tokens(out, N * B, Hq * D, cache.k.dtype, "out")
+    ws_ptr, ws_bytes = _ws(ws)
+    _check(lib().xpress_block_attention(
+        cache._ref, layer, q.data_ptr(), q_ld, _list(seq, N, torch.int32, "seq"), N, B, Hq,
+        D ** -0.5 if scale is None else scale, shared, out.data_ptr(), out_ld,
+        _list(lse, N * B * Hq, torch.float32, "lse"), ws_ptr, ws_bytes, _stream()))
+    return out
+
+
+def verify_workspace(n_max: int, B: int, V: int, device="cuda") -> torch.Tensor:
+    out = ctypes.c_size_t()
+    _check(lib().xpress_verify_workspace_size(n_max, B, V, ctypes.byref(out)))
+    return torch.empty(max(out.value, 256), dtype=torch.uint8, device=device)
+
+
+def verify_draft(logits: torch.Tensor, blk: torch.Tensor, *, out: torch.Tensor,
+                 accepted: torch.Tensor, ws: torch.Tensor, u=None, temperature=None,
+                 draft_len=None, q=None, drop=None) -> torch.Tensor:
+    """Which drafts of blk [N, B] stand against the target's logits [N*B, V], and the token after
+    them; q [N*(B-1), V]: the drafts' probabilities (None: drafts chosen by argmax)."""
+    N, B = blk.shape
+    V = logits.shape[-1]
+    if logits.dtype not in _DTYPES:
+        raise TypeError("logits must be bfloat16, float16 or float32")
+    ld = _tokens(logits, N * B, V, logits.dtype, "logits")
+    q_ptr, q_type, q_ld = None, BF16, V
+    if q is not None:
+        if q.dtype not in _DTYPES:
+            raise TypeError("q must be bfloat16, float16 or float32")
+        q_ld = _tokens(q, N * (B - 1), V, q.dtype, "q")
+        q_ptr, q_type = q.data_ptr(), _DTYPES[q.dtype]
+    ws_ptr, ws_bytes = _ws(ws)
+    i64, i32, f32 = torch.int64, torch.int32, torch.float32
+    _check(lib().xpress_verify_draft(
+        logits.data_ptr(), _DTYPES[logits.dtype], ld, _list(blk, N * B, i64, "blk"),
+        _list(draft_len, N, i32, "draft_len"), q_ptr, q_type, q_ld,
+        _list(temperature, N, f32, "temperature"), _list(u, N * B, f32, "u"), N, B, V,
+        _list(out, N * B, i64, "out"), _list(accepted, N, i32, "accepted"),
+        _list(drop, N, i32, "drop"), ws_ptr, ws_bytes, _stream()))
+    return out

@@ -1,0 +1,283 @@
+"""Block attention over the paged cache against attention from its definition in 64 bits."""
+import math
+
+import numpy as np
+import pytest
+import torch
+
+from jacobi_block_refiner_amd import xpress
+from tests.gpu_helpers import log
+from tests.serve_oracle import attention, attention_bounds
+
+pytestmark = [pytest.mark.gpu, pytest.mark.timeout(120)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    xpress.lib()
+    torch.cuda.set_device(0)
+
+
+class Case:
+    """Rows of `lengths` tokens whose first `shared` are the same, on pages drawn at random; the
+    lines past a row's end, and pages nobody holds, are NaN."""
+
+    def __init__(self, lengths, shared, B, Hkv, G, D, page, dtype=torch.bfloat16, seed=0, q_scale=1.0,
+                 n_layers=1, layer=0, pad=8):
+        rng = np.random.default_rng(seed)
+        g = torch.Generator().manual_seed(seed)
+        self.lengths, self.shared, self.B, self.Hq, self.page = lengths, shared, B, Hkv * G, page
+        self.D, self.dtype, self.layer = D, dtype, layer
+        need = [-(-n // page) for n in lengths]
+        ld = max(max(need), -(-shared // page), 1) + 1
+        first = shared // page
+        perm = rng.permutation(sum(need) + first + 3)
+        n_pages = len(perm)
+        common, used = perm[:first], first
+        self.table = np.full((len(lengths), ld), -1, np.int32)
+        pools = torch.full((2, n_pages, Hkv, page, D), math.nan)
+        prefix = torch.randn(2, Hkv, max(shared, 1), D, generator=g)
+        for r, n in enumerate(lengths):
+            for j in range(need[r]):
+                if j < first:
+                    p = common[j]
+                else:
+                    p, used = perm[used], used + 1
+                self.table[r, j] = p
+                lines = min(page, n - j * page)
+                if j >= first or r == max(range(len(lengths)), key=lambda x: lengths[x]):
+                    pools[:, p, :, :lines] = torch.randn(2, Hkv, lines, D, generator=g)
+                both = max(0, min(lines, shared - j * page))
+                if both:
+                    pools[:, p, :, :both] = prefix[:, :, j * page:j * page + both]
+        pools = pools.to(dtype)
+        full = torch.full((n_layers, n_pages, Hkv, page, D), 3.0).to(dtype)
+        self.k, self.v = full.clone(), full.clone()
+        self.k[layer], self.v[layer] = pools[0], pools[1]
+        # q and out are slices of wider rows
+        self.wide = (torch.randn(len(lengths) * B, self.Hq * D + pad, generator=g) * q_scale).to(dtype)
+        self.q = self.wide[:, :self.Hq * D]
+        self.pad = pad
+
+    def cache(self):
+        return xpress.Cache(k=self.k.cuda(), v=self.v.cuda(),
+                            table=torch.from_numpy(self.table).cuda(),
+                            length=torch.tensor(self.lengths, dtype=torch.int32, device="cuda"),
+                            ref=torch.zeros(self.k.shape[1], dtype=torch.int32, device="cuda"))
+
+    def run(self, cache, shared=None, seq=None, rows=None, scale=None, lse=True, q=None, ws=None):
+        rows = list(range(len(self.lengths))) if rows is None else rows
+        N = len(rows)
+        q = self.wide.cuda()[:N * self.B, :self.Hq * self.D] if q is None else q
+        hold = torch.full((N * self.B, self.Hq * self.D + self.pad), 5.0, dtype=self.dtype,
+                          device="cuda")
+        out = hold[:, :self.Hq * self.D]
+        l = torch.full((N * self.B, self.Hq), 7.0, device="cuda") if lse else None
+        ws = xpress.attention_workspace(cache, N, self.B, self.Hq) if ws is None else ws
+        xpress.block_attention(cache, self.layer, q, B=self.B, Hq=self.Hq, N=N, seq=seq, out=out,
+                               lse=l, shared=self.shared if shared is None else shared, ws=ws,
+                               scale=scale)
+        torch.cuda.synchronize()
+        assert bool((hold[:, self.Hq * self.D:] == 5.0).all())  # nothing past a row's end
+        return out.cpu().view(N * self.B, self.Hq, self.D), None if l is None else l.cpu()
+
+    def check(self, got, rows=None, scale=None, what=""):
+        rows = list(range(len(self.lengths))) if rows is None else rows
+        scale = self.D ** -0.5 if scale is None else scale
+        out, lse, mass, size = attention(self.k[self.layer], self.v[self.layer], self.table,
+                                         self.lengths, self.page, self.q[:len(rows) * self.B],
+                                         rows, self.B, self.Hq, scale)
+        bound, lse_bound = attention_bounds(out, mass, size, max(self.lengths), self.D, self.dtype)
+        err = (got[0].double() - out).abs()
+        worst = float((err / bound).max())
+        log(f"  {what}: worst error {worst:.3f} of the bound")
+        assert not bool(got[0].isnan().any()), what
+        assert bool((err <= bound).all()), (what, worst)
+        if got[1] is not None:
+            empty = lse == -math.inf
+            assert bool((got[1][empty] == -math.inf).all()), what
+            off = (got[1].double() - lse).abs()[~empty]
+            assert bool((off <= (lse_bound + lse.abs() * 2.0 ** -22)[~empty]).all()), (
+                what, float(off.max()))
+
+
+CASES = [
+    # lengths, shared, B, Hkv, G, D, page
+    dict(lengths=[1], shared=0, B=1, Hkv=1, G=1, D=64, page=16),
+    dict(lengths=[5, 0, 3, 64, 65], shared=0, B=4, Hkv=2, G=3, D=64, page=16),
+    dict(lengths=[100, 37, 129], shared=32, B=16, Hkv=2, G=4, D=128, page=32),
+    dict(lengths=[300, 0, 290, 288, 401], shared=277, B=7, Hkv=1, G=5, D=128, page=64),
+    dict(lengths=[64, 64, 64], shared=64, B=1, Hkv=2, G=1, D=64, page=64),
+    dict(lengths=[700, 650], shared=600, B=16, Hkv=1, G=8, D=256, page=128),
+    dict(lengths=[500, 3, 17], shared=450, B=5, Hkv=1, G=2, D=64, page=256),  # rows end in the prefix
+    dict(lengths=[1025], shared=0, B=16, Hkv=2, G=7, D=128, page=16),
+    dict(lengths=[260] * 9, shared=256, B=2, Hkv=3, G=1, D=64, page=32),
+    dict(lengths=[90, 91, 92, 93], shared=80, B=33, Hkv=1, G=9, D=64, page=16),  # 297 rows a request
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("i", range(len(CASES)))
+def test_against_the_definition(i, dtype):
+    log(f"attention case {i} {CASES[i]} {dtype}")
+    x = Case(**CASES[i], dtype=dtype, seed=i)
+    c = x.cache()
+    x.check(x.run(c), what="shared")
+    # the same rows attended alone
+    x.check(x.run(c, shared=0), what="not shared")
+    if x.shared > 1:
+        x.check(x.run(c, shared=x.shared - 1), what="shared, one less")
+
+
+def test_rows_in_any_order_and_rows_outside():
+    x = Case(lengths=[80, 33, 0, 47, 95], shared=32, B=3, Hkv=2, G=2, D=128, page=16, seed=3)
+    c = x.cache()
+    order = [4, 1, 3]
+    seq = torch.tensor(order, dtype=torch.int32, device="cuda")
+    x.check(x.run(c, seq=seq, rows=order), rows=order, what="a list")
+    seq = torch.tensor([4, -1, 9], dtype=torch.int32, device="cuda")
+    out, lse = x.run(c, seq=seq, rows=[4, 0, 0])
+    assert bool((out[3:] == 0).all()) and bool((lse[3:] == -math.inf).all())
+    x.check((out[:3], lse[:3]), rows=[4], what="rows outside are empty")
+
+
+def test_large_scores_and_other_scales():
+    """Scores of some hundreds: one key takes all the weight in most rows; running maxima grow along
+    the row."""
+    x = Case(lengths=[400, 333], shared=256, B=4, Hkv=1, G=4, D=128, page=32, seed=4, q_scale=16.0)
+    x.check(x.run(x.cache()), what="large")
+    x.check(x.run(x.cache(), scale=0.01), scale=0.01, what="scale 0.01")
+    # keys that grow along the row: the maximum moves in every tile
+    y = Case(lengths=[600], shared=0, B=2, Hkv=1, G=2, D=64, page=16, seed=5)
+    for j in range(600):
+        p = y.table[0, j // 16]
+        y.k[0, p, :, j % 16] = (y.q[0, :64].float() * (j / 100.0)).to(y.dtype)
+    y.check(y.run(y.cache(), scale=0.125), what="growing")
+    y.q.neg_()
+    y.check(y.run(y.cache(), scale=0.125), what="falling")
+
+
+@pytest.mark.parametrize("D", [64, 128, 256])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_values_of_later_tokens_do_not_reach_earlier_queries(D, bad):
+    """K and V of the block's last token are infinite or NaN: queries before it are as if it were
+    not there, the last query is not finite."""
+    x = Case(lengths=[75, 40, 64], shared=32, B=6, Hkv=2, G=3, D=D, page=16, seed=6)
+    x.pad = 8
+    good = x.run(x.cache())
+    x.check(good, what="before")
+    for r, n in enumerate(x.lengths):
+        p = x.table[r, (n - 1) // 16]
+        x.v[0, p, :, (n - 1) % 16] = bad
+        x.k[0, p, :, (n - 1) % 16, : D // 2] = bad
+    got = x.run(x.cache())
+    early = [t for t in range(18) if t % 6 != 5]
+    assert not bool(got[0][early].isnan().any())
+    scale = D ** -0.5
+    out, lse, mass, size = attention(
+        torch.nan_to_num(x.k[0], 0, 0, 0), torch.nan_to_num(x.v[0], 0, 0, 0), x.table, x.lengths, 16,
+        x.q, range(3), 6, x.Hq, scale)
+    bound, _ = attention_bounds(out, mass, size, 75, D, x.dtype)
+    assert bool(((got[0].double() - out).abs() <= bound)[early].all())
+    if math.isnan(bad):
+        assert bool(got[0][5::6].isnan().all())
+
+
+def test_page_ids_outside_the_pool_stay_inside_it():
+    """Ids outside the pool are the caller's error: the affected request's result is unspecified, the
+    others' is right."""
+    x = Case(lengths=[80, 90], shared=0, B=2, Hkv=1, G=2, D=64, page=16, seed=7)
+    c = x.cache()
+    c.table[0, 1], c.table[0, 2] = -9, 1 << 30
+    out, lse = x.run(c)
+    x.q = x.q[2:]
+    x.check((out[2:], lse[2:]), rows=[1], what="the other row")
+
+
+def test_lengths_past_the_table_are_clamped():
+    x = Case(lengths=[80, 96], shared=0, B=2, Hkv=1, G=1, D=64, page=16, seed=8)
+    c = x.cache()
+    c.table = c.table[:, :6].contiguous()
+    c = xpress.Cache(k=c.k, v=c.v, table=c.table, length=c.length, ref=c.ref)
+    c.length[1] = 1 << 30  # the table holds 96
+    x.check(x.run(c), what="clamped")
+
+
+@pytest.mark.parametrize("layer", [0, 2])
+def test_layers_streams_and_workspaces(layer):
+    """Another stream, another layer, a workspace of another call's, twice the same bits."""
+    x = Case(lengths=[500, 480, 0], shared=400, B=16, Hkv=2, G=4, D=128, page=64, seed=9,
+             n_layers=3, layer=layer)
+    c = x.cache()
+    ws = xpress.attention_workspace(c, 3, 16, 8)
+    ws.fill_(0xFF)  # NaN everywhere: nothing is read that was not written
+    a = x.run(c, ws=ws)
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        b = x.run(c, ws=ws)
+    torch.cuda.current_stream().wait_stream(s)
+    x.check(a, what="first")
+    assert torch.equal(a[0], b[0]) and torch.equal(a[1], b[1])
+    x.check(x.run(c, lse=False, ws=ws), what="no lse")
+
+
+def test_long_row_in_a_big_pool():
+    """Pages past element 2^32 of a layer."""
+    n_pages, Hkv, page, D = 70000, 8, 64, 128
+    c = xpress.Cache.empty(1, n_pages, Hkv, page, D, rows=2, table_ld=40)
+    log("attention past 32 bits")
+    g = torch.Generator().manual_seed(1)
+    ids = n_pages - 1 - torch.randperm(60, generator=g)
+    lengths = [30 * 64 - 5, 30 * 64 - 60]
+    kv = torch.randn(2, 60, Hkv, page, D, generator=g).to(torch.bfloat16)
+    c.k[0, ids.cuda()], c.v[0, ids.cuda()] = kv[0].cuda(), kv[1].cuda()
+    table = torch.full((2, 40), -1, dtype=torch.int32)
+    table[0, :30], table[1, :30] = ids[:30], ids[30:]
+    small = np.full((2, 40), -1, np.int64)
+    small[0, :30], small[1, :30] = np.arange(30), np.arange(30, 60)
+    c.table.copy_(table)
+    c.length.copy_(torch.tensor(lengths, dtype=torch.int32))
+    q = torch.randn(4, 8 * D, generator=g).to(torch.bfloat16)
+    out = torch.empty(4, 8 * D, dtype=torch.bfloat16, device="cuda")
+    xpress.block_attention(c, 0, q.cuda(), B=2, Hq=8, out=out,
+                           ws=xpress.attention_workspace(c, 2, 2, 8))
+    want, _, mass, size = attention(kv[0], kv[1], small, lengths, page, q, [0, 1], 2, 8, D ** -0.5)
+    bound, _ = attention_bounds(want, mass, size, 1920, D, torch.bfloat16)
+    assert bool(((out.cpu().double().view(4, 8, D) - want).abs() <= bound).all())
+    del c
+    torch.cuda.empty_cache()
+
+
+def test_a_captured_call_follows_the_lengths():
+    """Replays of a captured call read lengths and tables as they are then; eager work in between."""
+    x = Case(lengths=[200, 180, 190], shared=128, B=4, Hkv=2, G=2, D=128, page=32, seed=11)
+    c = x.cache()
+    q = x.wide.cuda()[:, :x.Hq * x.D]
+    out = torch.empty(12, x.Hq * x.D, dtype=x.dtype, device="cuda")
+    lse = torch.empty(12, x.Hq, device="cuda")
+    ws = xpress.attention_workspace(c, 3, 4, x.Hq)
+
+    def call():
+        xpress.block_attention(c, 0, q, B=4, Hq=x.Hq, out=out, lse=lse, shared=128, ws=ws)
+
+    s = torch.cuda.Stream()
+    s.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(s):
+        call()
+    torch.cuda.current_stream().wait_stream(s)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        call()
+    for lengths in ([200, 180, 190], [150, 0, 131], [199, 180, 2], [200, 180, 190]):
+        x.lengths = lengths
+        c.length.copy_(torch.tensor(lengths, dtype=torch.int32))
+        out.fill_(3.0)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = (out.cpu().view(12, x.Hq, x.D), lse.cpu())
+        x.check(got, what=f"replay {lengths}")
+        eager = x.run(c, ws=ws)
+        assert torch.equal(got[0], eager[0]) and torch.equal(got[1], eager[1])

@@ -1,0 +1,233 @@
+"""The paged cache's calls on the GPU against the host oracle, bit for bit after every call."""
+import numpy as np
+import pytest
+import torch
+
+from jacobi_block_refiner_amd import xpress
+from tests.gpu_helpers import log
+from tests.serve_oracle import CacheOracle
+
+pytestmark = [pytest.mark.gpu, pytest.mark.timeout(120)]
+
+
+@pytest.fixture(scope="module", autouse=True)
+def _gpu():
+    assert torch.cuda.is_available(), "GPU tests need a GPU"
+    xpress.lib()
+    torch.cuda.set_device(0)
+
+
+def device_cache(o: CacheOracle) -> xpress.Cache:
+    return xpress.Cache(k=o.k.cuda(), v=o.v.cuda(), table=torch.from_numpy(o.table).cuda(),
+                        length=torch.from_numpy(o.length).cuda(),
+                        ref=torch.from_numpy(o.ref).cuda())
+
+
+def i32(x):
+    return torch.tensor(np.asarray(x), dtype=torch.int32, device="cuda")
+
+
+def same(c: xpress.Cache, o: CacheOracle, what: str):
+    torch.cuda.synchronize()
+    assert np.array_equal(c.length.cpu().numpy(), o.length), what
+    assert np.array_equal(c.table.cpu().numpy(), o.table), what
+    assert np.array_equal(c.ref.cpu().numpy(), o.ref), what
+    assert torch.equal(c.k.cpu().view(torch.int16), o.k.view(torch.int16)), what
+    assert torch.equal(c.v.cpu().view(torch.int16), o.v.view(torch.int16)), what
+    # the counts are what the tables say
+    held = [o.table[r, :o.pages(o.length[r])] for r in range(len(o.length))]
+    count = np.bincount(np.concatenate(held).astype(np.int64), minlength=len(o.ref))
+    assert np.array_equal(count, o.ref), what
+
+
+SHAPES = [  # layers, pages, Hkv, page, D, rows, ld, dtype
+    (1, 40, 1, 16, 64, 6, 9, torch.bfloat16),
+    (3, 75, 2, 32, 128, 9, 11, torch.float16),
+    (2, 33, 5, 16, 256, 5, 14, torch.bfloat16),
+    (1, 21, 3, 256, 64, 4, 5, torch.float16),
+    (2, 1500, 1, 16, 64, 40, 70, torch.bfloat16),  # more pages than the planning workgroup's threads
+]
+
+
+@pytest.mark.parametrize("shape", SHAPES, ids=lambda s: f"p{s[1]}x{s[3]}D{s[4]}")
+@pytest.mark.parametrize("seed", [0, 1])
+def test_random_turns(shape, seed):
+    layers, n_pages, Hkv, page, D, rows, ld, dtype = shape
+    rng = np.random.default_rng(seed)
+    o = CacheOracle(layers, n_pages, Hkv, page, D, rows, ld, dtype, seed)
+    c = device_cache(o)
+    ws = xpress.cache_workspace(c, rows)
+    lacking = torch.full((1,), 7, dtype=torch.int32, device="cuda")
+    seen = {"cow": 0, "lack": 0, "over": 0, "moved": 0}
+    log(f"cache turns {shape} seed {seed}")
+    for turn in range(14):
+        sub = rng.permutation(rows)[: rng.integers(1, rows + 1)]
+        kind = rng.integers(0, 6)
+        if kind == 0 and rows > 1:
+            half = rows // 2
+            perm = rng.permutation(rows)
+            n = rng.integers(1, half + 1)
+            src, dst = rng.choice(perm[:half], n), perm[half:][:n]
+            o.fork(src, dst)
+            xpress.cache_fork(c, i32(src), i32(dst))
+            same(c, o, f"turn {turn} fork")
+        elif kind == 1:
+            drop = rng.integers(-2, 3 * page, len(sub)) if rng.random() < 0.8 else None
+            o.trim(sub, drop)
+            xpress.cache_trim(c, None if drop is None else i32(drop), seq=i32(sub))
+            same(c, o, f"turn {turn} trim")
+        elif kind == 2:
+            live = torch.zeros(1, dtype=torch.int32, device="cuda")
+            before = o.table.copy()
+            want = o.compact()
+            seen["moved"] += int((before != o.table).sum())
+            xpress.cache_compact(c, live=live, ws=ws)
+            same(c, o, f"turn {turn} compact")
+            assert int(live.item()) == want
+        # every turn also grows some rows and writes their last tokens
+        each = rng.integers(-1, 2 * page + 3, len(sub))
+        if rng.random() < 0.3:
+            each[:] = int(rng.integers(0, 17))
+            got = xpress.cache_extend(c, int(each[0]), lacking=lacking, ws=ws, seq=i32(sub))
+        else:
+            got = xpress.cache_extend(c, i32(each), lacking=lacking, ws=ws, seq=i32(sub))
+        refs = o.ref.copy()
+        want = o.extend(sub, each)
+        same(c, o, f"turn {turn} extend")
+        assert int(got.item()) == want
+        seen["lack"] += want > 0
+        seen["over"] += want < 0
+        seen["cow"] += int((o.ref < refs).sum())
+        B = int(rng.integers(1, 20))
+        wide = torch.randn(len(sub) * B, 2 * Hkv * D + 8).to(dtype)
+        k_new, v_new = wide[:, :Hkv * D], wide[:, Hkv * D:2 * Hkv * D]
+        layer = int(rng.integers(layers))
+        # rows that share a page are not written through it
+        alone = [r for r in sub if all(
+            o.ref[o.table[r, p // page]] == 1
+            for p in range(max(int(o.length[r]) - B, 0), int(o.length[r])))]
+        if not alone:
+            continue
+        at = np.concatenate([np.arange(B) + B * int(np.nonzero(sub == r)[0][0]) for r in alone])
+        k_new, v_new = wide[at][:, :Hkv * D], wide[at][:, Hkv * D:2 * Hkv * D]
+        o.append(layer, k_new.reshape(-1, Hkv, D), v_new.reshape(-1, Hkv, D), alone, B)
+        dev = wide[at].cuda()
+        xpress.cache_append(c, layer, dev[:, :Hkv * D], dev[:, Hkv * D:2 * Hkv * D], B=B,
+                            seq=i32(alone))
+        same(c, o, f"turn {turn} append")
+    log(f"  seen {seen}")
+
+
+def test_copy_on_write_of_a_shared_partial_page():
+    """Two rows of one prompt both grow: each gets a page of its own with the prompt's tokens, and
+    the page that nobody holds any more is free."""
+    o = CacheOracle(2, 12, 2, 16, 64, 3, 6, torch.bfloat16)
+    c = device_cache(o)
+    ws = xpress.cache_workspace(c, 3)
+    lacking = i32([9])
+    for want, add in (([0], [21]),):
+        assert o.extend(want, add) == 0
+        xpress.cache_extend(c, i32(add), lacking=lacking, ws=ws, seq=i32(want))
+    o.fork([0], [1])
+    xpress.cache_fork(c, i32([0]), i32([1]))
+    same(c, o, "fork")
+    assert o.ref[1] == 2
+    assert o.extend([1, 0], [1, 2]) == 0
+    xpress.cache_extend(c, i32([1, 2]), lacking=lacking, ws=ws, seq=i32([1, 0]))
+    same(c, o, "extend")
+    assert o.ref[1] == 0 and int(lacking.item()) == 0
+    assert o.table[0, 1] == 3 and o.table[1, 1] == 2
+
+
+def test_nothing_changes_when_pages_are_missing_or_a_row_is_full():
+    o = CacheOracle(1, 5, 1, 16, 64, 3, 4, torch.bfloat16)
+    c = device_cache(o)
+    ws = xpress.cache_workspace(c, 3)
+    lacking = i32([9])
+    for add, want in (([40, 30, 16], 1), ([80, 80, 0], -1), ([64, 16, 16], 1),
+                      ([64, 16, 0], 0), ([1, 0, 0], -1), ([0, 0, 1], 1)):
+        got = int(xpress.cache_extend(c, i32(add), lacking=lacking, ws=ws).item())
+        assert got == o.extend(range(3), add) == want, add
+        same(c, o, str(add))
+
+
+def test_rows_and_pages_outside_the_cache_are_skipped():
+    """List entries outside [0, rows) do nothing; page ids outside the pool are neither counted nor
+    written."""
+    o = CacheOracle(1, 8, 1, 16, 64, 4, 4, torch.bfloat16)
+    c = device_cache(o)
+    ws = xpress.cache_workspace(c, 4)
+    lacking = i32([9])
+    xpress.cache_extend(c, i32([5, 5, 20]), lacking=lacking, ws=ws, seq=i32([-1, 4, 2]))
+    assert o.extend([2], [20]) == 0
+    same(c, o, "extend")
+    xpress.cache_trim(c, i32([3, 3]), seq=i32([1 << 30, 2]))
+    o.trim([2], [3])
+    same(c, o, "trim")
+    xpress.cache_fork(c, i32([-5, 2]), i32([0, 77]))
+    same(c, o, "fork")
+    new = torch.randn(2, 64).to(torch.bfloat16)
+    xpress.cache_append(c, 0, new.cuda(), new.cuda(), B=1, seq=i32([9, 2]))
+    o.append(0, new[1:].reshape(1, 1, 64), new[1:].reshape(1, 1, 64), [2], 1)
+    same(c, o, "append")
+    bad = torch.from_numpy(o.table).cuda()
+    bad[2, 0], bad[2, 1] = 99, -7
+    c.table.copy_(bad)
+    xpress.cache_append(c, 0, new.cuda(), new.cuda(), B=2, seq=i32([2]))
+    xpress.cache_trim(c, seq=i32([2]))
+    torch.cuda.synchronize()
+    assert torch.equal(c.k.cpu().view(torch.int16), o.k.view(torch.int16))
+    assert np.array_equal(c.ref.cpu().numpy(), o.ref)
+    assert int(c.length[2].item()) == 0 and bool((c.table[2] == -1).all())
+
+
+def test_list_of_a_row_twice_stays_inside_the_buffers():
+    """A row twice in one list is the caller's error: the result is unspecified, but every page id
+    and length stays in range and other rows keep theirs."""
+    o = CacheOracle(1, 32, 1, 16, 64, 4, 6, torch.bfloat16)
+    c = device_cache(o)
+    ws = xpress.cache_workspace(c, 4)
+    lacking = i32([9])
+    xpress.cache_extend(c, i32([30]), lacking=lacking, ws=ws, seq=i32([1]))
+    keep = c.table[1].clone()
+    xpress.cache_extend(c, 90, lacking=lacking, ws=ws, seq=i32([0, 0, 0]))
+    torch.cuda.synchronize()
+    t = c.table.cpu().numpy()
+    assert t.min() >= -1 and t.max() < 32
+    assert torch.equal(c.table[1], keep)
+    assert 0 <= int(c.length[0].item()) <= 6 * 16
+
+
+@pytest.mark.parametrize("page,Hkv,D", [(64, 8, 128)])
+def test_offsets_past_32_bits(page, Hkv, D):
+    """A layer of 4.6e9 elements (9.2 GB a side): pages at its end are written, copied and moved."""
+    n_pages = 70000
+    assert n_pages * page * Hkv * D > 1 << 32
+    c = xpress.Cache.empty(1, n_pages, Hkv, page, D, rows=3, table_ld=4)
+    log("cache past 32 bits")
+    ws = xpress.cache_workspace(c, 3)
+    lacking, live = i32([9]), i32([9])
+    c.ref.fill_(1)
+    c.ref[n_pages - 4:] = 0  # the only free pages are the last ones
+    xpress.cache_extend(c, i32([page + 9, 0, 0]), lacking=lacking, ws=ws)
+    assert int(lacking.item()) == 0
+    assert c.table[0].tolist() == [n_pages - 4, n_pages - 3, -1, -1]
+    new = torch.randn(page + 9, 2 * Hkv * D, device="cuda").to(torch.bfloat16)
+    xpress.cache_append(c, 0, new[:, :Hkv * D], new[:, Hkv * D:], B=page + 9, N=1)
+    kk = new[:, :Hkv * D].view(-1, Hkv, D).transpose(0, 1)
+    vv = new[:, Hkv * D:].view(-1, Hkv, D).transpose(0, 1)
+    assert torch.equal(c.k[0, n_pages - 4], kk[:, :page])
+    assert torch.equal(c.v[0, n_pages - 3, :, :9], vv[:, page:])
+    xpress.cache_fork(c, i32([0]), i32([1]))
+    xpress.cache_extend(c, i32([1]), lacking=lacking, ws=ws, seq=i32([1]))
+    assert int(lacking.item()) == 0
+    assert c.table[1].tolist() == [n_pages - 4, n_pages - 2, -1, -1]
+    assert torch.equal(c.v[0, n_pages - 2, :, :9], vv[:, page:])
+    c.ref[:n_pages - 4] = 0
+    xpress.cache_compact(c, live=live, ws=ws)
+    assert int(live.item()) == 3
+    assert c.table[0].tolist() == [0, 1, -1, -1] and c.table[1].tolist() == [0, 2, -1, -1]
+    assert torch.equal(c.k[0, 0], kk[:, :page]) and torch.equal(c.v[0, 2, :, :9], vv[:, page:])
+    assert c.ref[:4].tolist() == [2, 1, 1, 0] and int(c.ref.sum().item()) == 4
+    del c, ws
+    torch.cuda.empty_cache()
