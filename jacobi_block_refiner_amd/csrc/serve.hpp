@@ -24,6 +24,7 @@ hipError_t launch_cache_trim(const xpress_cache& c, const int32_t* seq, int N, c
 hipError_t launch_cache_compact(const xpress_cache& c, int32_t* live, void* ws, hipStream_t s);
 
 size_t attention_scratch_bytes(const xpress_cache& c, int N, int B, int Hq);
+int64_t attention_items(const xpress_cache& c, int N, int B, int Hq, int shared);  // workgroups
 hipError_t launch_block_attention(const xpress_cache& c, int layer, const void* q, int64_t q_ld,
                                   const int32_t* seq, int N, int B, int Hq, float scale,
                                   int shared, void* out, int64_t out_ld, float* lse, void* ws,

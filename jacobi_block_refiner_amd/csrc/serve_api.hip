@@ -221,6 +221,9 @@ xpress_status xpress_block_attention(const xpress_cache* c, int32_t layer, const
     return fail(XPRESS_ERR_ARG, "shared=%d outside [0, table_ld*page=%lld]", shared,
                 (long long)c->table_ld * c->page);
   if (N == 0) return XPRESS_OK;
+  if (xpress::attention_items(*c, N, B, Hq, shared) >= (int64_t)1 << 31)
+    return fail(XPRESS_ERR_ARG, "N=%d, B=%d, Hq=%d over tables of %lld tokens is too large a launch",
+                N, B, Hq, (long long)c->table_ld * c->page);
   XP_PTR(q);
   XP_PTR(out);
   XP_WORDS_OR_NULL(lse);

@@ -94,6 +94,12 @@ __device__ __forceinline__ void lds_copy16(const void* gbase, uint32_t off, uint
                :: "s"(lds_base), "v"(off), "s"(gbase) : "memory");
 }
 
+// The same copy from a 64-bit address of each lane's own (pools of more than 4 GiB).
+__device__ __forceinline__ void lds_copy16_at(const void* from, uint32_t lds_base) {
+  asm volatile("s_mov_b32 m0, %0\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %1, off"
+               :: "s"(lds_base), "v"(from) : "memory");
+}
+
 // Skip test of the fixed-point early exit: pass p >= 1 is skipped once pass p-1 changed nothing.
 // flags == nullptr disables it.
 __device__ __forceinline__ bool pass_skipped(const int32_t* flags, int pass) {
