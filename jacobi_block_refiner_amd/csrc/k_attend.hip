@@ -18,6 +18,9 @@ namespace xpress {
 namespace {
 
 typedef _Float16 f16x8 __attribute__((ext_vector_type(8)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
+typedef float f32x2 __attribute__((ext_vector_type(2)));
 typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
@@ -39,14 +42,12 @@ struct Args {
   float2* pml; // [slots, N*B, Hq]: maximum (log2 units), sum
 };
 
-template <bool F16> __device__ __forceinline__ uint16_t round_to(float x) {
-  return F16 ? __builtin_bit_cast(uint16_t, (_Float16)x) : __builtin_bit_cast(uint16_t, (__bf16)x);
-}
-
 // Two weights rounded to the type (to nearest even) in one register: the matrix core takes them as
 // bf16 or fp16. Relative error half a step each, against the 32-bit sum of the unrounded weights.
 template <bool F16> __device__ __forceinline__ uint32_t pack2(float a, float b) {
-  return (uint32_t)round_to<F16>(a) | (uint32_t)round_to<F16>(b) << 16;
+  const f32x2 x = {a, b};
+  return F16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(x, f16x2))
+             : __builtin_bit_cast(uint32_t, __builtin_convertvector(x, bf16x2));
 }
 
 template <bool F16>
@@ -216,123 +217,136 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(Args A) {
 #pragma unroll
   for (int dt = 0; dt < DT; ++dt) o[dt] = f32x16{};
 
-  if (nt > 0) copy_tile(0, 0);
-  if (nt > 1) copy_tile(1, 1);
+  // Start of a tile: its copies have landed in every wave, and tile t-1's stage is free again.
   int stage = 0;
-  for (int t = 0; t < nt; ++t) {
-    // this wave's copies of tile t have landed (those of tile t+1 may be in flight)
-    // and its reads of tile t-1 are done: vmcnt, lgkmcnt(0)
+  auto enter = [&](int t) {
+    // this wave's copies of tile t (those of tile t+1 may be in flight) and its reads of tile t-1:
+    // vmcnt, lgkmcnt(0)
     if (t + 1 < nt)
       __builtin_amdgcn_s_waitcnt(0x0070 | (2 * CW));
     else
       __builtin_amdgcn_s_waitcnt(0x0070);
     asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();  // so are every wave's
+    __builtin_amdgcn_s_barrier();
     asm volatile("" ::: "memory");
     if (t + 2 < nt) copy_tile(t + 2, stage == 0 ? 2 : stage - 1);
+  };
+  auto leave = [&] { stage = stage == NS - 1 ? 0 : stage + 1; };
+  f32x16 s[KH];
+  s16x8 pf[KK];
+  auto scores = [&] {
+#pragma unroll
+    for (int d = 0; d < DS; ++d)
+#pragma unroll
+      for (int kh = 0; kh < KH; ++kh)
+        s[kh] = mfma<F16>(k_frag(stage, kh, d), qf[d], d == 0 ? f32x16{} : s[kh]);
+  };
+  auto weights = [&] {
+    float top = s[0][0];
+#pragma unroll
+    for (int kh = 0; kh < KH; ++kh)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kh][i]);
+    const float2 tops = both_halves(top);
+    top = fmaxf(tops.x, tops.y);
+    // The sums are rescaled only when some row's maximum grew by more than 2^8 in weight: weights
+    // stay below 2^8, which 32-bit sums and the rounded weights' relative precision do not feel.
+    if (__any((top - m) * A.c > 8.f)) {
+      const float mn = fmaxf(m, top);
+      const float alpha = __builtin_amdgcn_exp2f((m - mn) * A.c);
+      l *= alpha;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) o[dt] *= alpha;
+      m = mn;
+    }
+    const float mc = -m * A.c;
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = __builtin_amdgcn_exp2f(fmaf(s[kk / 2][8 * (kk % 2) + 2 * j], A.c, mc));
+        const float b = __builtin_amdgcn_exp2f(fmaf(s[kk / 2][8 * (kk % 2) + 2 * j + 1], A.c, mc));
+        l += a + b;
+        w[j] = pack2<F16>(a, b);
+      }
+      pf[kk] = __builtin_bit_cast(s16x8, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+  };
+
+  if (nt > 0) copy_tile(0, 0);
+  if (nt > 1) copy_tile(1, 1);
+  int t = 0;
+  // tiles that every row of the wave sees whole
+  for (; t < nt && kbeg + t * KT + KT <= vmin; ++t) {
+    enter(t);
+    scores();
+    weights();
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) o[dt] = mfma<F16>(v_frag(stage, kk, dt), pf[kk], o[dt]);
+    leave();
+  }
+  // the others
+  for (; t < nt; ++t) {
+    enter(t);
     const int t0 = kbeg + t * KT;
     if (t0 < vmax) {
-      f32x16 s[KH];
-#pragma unroll
-      for (int kh = 0; kh < KH; ++kh) {
-        s[kh] = f32x16{};
-#pragma unroll
-        for (int d = 0; d < DS; ++d) s[kh] = mfma<F16>(k_frag(stage, kh, d), qf[d], s[kh]);
-      }
-      const bool masked = t0 + KT > vmin;
-      if (masked) {
-#pragma unroll
-        for (int kh = 0; kh < KH; ++kh)
-#pragma unroll
-          for (int i = 0; i < 16; ++i)
-            s[kh][i] = t0 + kh * 32 + 8 * (i / 4) + 4 * h + i % 4 < vis ? s[kh][i] : -INFINITY;
-      }
-      float top = s[0][0];
+      scores();
 #pragma unroll
       for (int kh = 0; kh < KH; ++kh)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kh][i]);
-      const float2 tops = both_halves(top);
-      top = fmaxf(tops.x, tops.y);
-      // The sums are rescaled only when some row's maximum grew by more than 2^8 in weight: weights
-      // stay below 2^8, which 32-bit sums and the rounded weights' relative precision do not feel.
-      if (__any((top - m) * A.c > 8.f)) {
-        const float mn = fmaxf(m, top);
-        const float alpha = __builtin_amdgcn_exp2f((m - mn) * A.c);
-        l *= alpha;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt) o[dt] *= alpha;
-        m = mn;
-      }
-      const float mc = -m * A.c;
-      s16x8 pf[KK];
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        uint32_t w[4];
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          const float a = __builtin_amdgcn_exp2f(fmaf(s[kk / 2][8 * (kk % 2) + 2 * j], A.c, mc));
-          const float b = __builtin_amdgcn_exp2f(fmaf(s[kk / 2][8 * (kk % 2) + 2 * j + 1], A.c, mc));
-          l += a + b;
-          w[j] = pack2<F16>(a, b);
-        }
-        pf[kk] = __builtin_bit_cast(s16x8, make_uint4(w[0], w[1], w[2], w[3]));
-      }
+        for (int i = 0; i < 16; ++i)
+          s[kh][i] = t0 + kh * 32 + 8 * (i / 4) + 4 * h + i % 4 < vis ? s[kh][i] : -INFINITY;
+      weights();
       // Values in masked places must not reach a row: 0 * inf would. Keys with a value that is not
       // finite are taken out of the product and added one by one to the rows that see them.
-      uint64_t bad = 0;
-      if (masked) {
-        const int key = lane % KT;
-        const uint4* row = s_tile + (stage * 2 * SIDE + SIDE) / 16 + key * CPR;
+      uint64_t bad;
+      {
+        const uint4* row = s_tile + (stage * 2 * SIDE + SIDE) / 16 + lane % KT * CPR;
         constexpr uint32_t E = F16 ? 0x7c00u : 0x7f80u;
         bool found = false;
-#pragma unroll
+#pragma unroll 4
         for (int x = 0; x < CPR; ++x) {
           const uint4 u = row[x];
           const uint32_t w[4] = {u.x, u.y, u.z, u.w};
 #pragma unroll
-          for (int y = 0; y < 4; ++y)
-            found |= (w[y] & E) == E || ((w[y] >> 16) & E) == E;
+          for (int y = 0; y < 4; ++y) found |= (w[y] & E) == E || ((w[y] >> 16) & E) == E;
         }
         bad = __ballot(found);
         if (KT < 64) bad &= (uint64_t(1) << (KT & 63)) - 1;
       }
-      if (bad == 0) {
 #pragma unroll
-        for (int kk = 0; kk < KK; ++kk)
+      for (int kk = 0; kk < KK; ++kk) {
+        s16x8 keep;
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt) o[dt] = mfma<F16>(v_frag(stage, kk, dt), pf[kk], o[dt]);
-      } else {
+        for (int j = 0; j < 8; ++j)
+          keep[j] = (bad >> (kk * 16 + 8 * (j / 4) + 4 * h + j % 4)) & 1 ? 0 : -1;
+#pragma unroll
+        for (int dt = 0; dt < DT; ++dt)
+          o[dt] = mfma<F16>(v_frag(stage, kk, dt) & keep, pf[kk], o[dt]);
+      }
+#pragma unroll 1
+      for (uint64_t left = bad; left; left &= left - 1) {
+        const int key = __builtin_ctzll(left);
+        const bool sees = t0 + key < vis;
 #pragma unroll
         for (int kk = 0; kk < KK; ++kk) {
+          if (key / 16 != kk) continue;
           s16x8 keep;
 #pragma unroll
-          for (int j = 0; j < 8; ++j)
-            keep[j] = (bad >> (kk * 16 + 8 * (j / 4) + 4 * h + j % 4)) & 1 ? 0 : -1;
+          for (int j = 0; j < 8; ++j) keep[j] = kk * 16 + 8 * (j / 4) + 4 * h + j % 4 == key ? -1 : 0;
 #pragma unroll
-          for (int dt = 0; dt < DT; ++dt)
-            o[dt] = mfma<F16>(v_frag(stage, kk, dt) & keep, pf[kk], o[dt]);
-        }
-        for (uint64_t left = bad; left; left &= left - 1) {
-          const int key = __builtin_ctzll(left);
-          const bool sees = t0 + key < vis;
+          for (int dt = 0; dt < DT; ++dt) {
+            const f32x16 one = mfma<F16>(v_frag(stage, kk, dt) & keep, pf[kk] & keep, f32x16{});
 #pragma unroll
-          for (int kk = 0; kk < KK; ++kk) {
-            if (key / 16 != kk) continue;
-            s16x8 keep;
-#pragma unroll
-            for (int j = 0; j < 8; ++j) keep[j] = kk * 16 + 8 * (j / 4) + 4 * h + j % 4 == key ? -1 : 0;
-#pragma unroll
-            for (int dt = 0; dt < DT; ++dt) {
-              const f32x16 one = mfma<F16>(v_frag(stage, kk, dt) & keep, pf[kk] & keep, f32x16{});
-#pragma unroll
-              for (int i = 0; i < 16; ++i) o[dt][i] += sees ? one[i] : 0.f;
-            }
+            for (int i = 0; i < 16; ++i) o[dt][i] += sees ? one[i] : 0.f;
           }
         }
       }
     }
-    stage = stage == NS - 1 ? 0 : stage + 1;
+    leave();
   }
 
   const float2 ls = both_halves(l);
