@@ -351,7 +351,8 @@ xpress_status xpress_cache_extend(const xpress_cache* c, const int32_t* seq, int
 /* Writes K and V of one layer for the last B tokens of each row: token b of list entry i goes to
  * position len[seq[i]] - B + b (skipped where that is negative). k_new, v_new: token i*B + b at
  * element (i*B + b)*ld_new, [Hkv, D] dense, the cache's dtype, 16-byte aligned, ld_new a multiple
- * of 8 and at least Hkv*D (so slices of a fused projection's output can be passed). */
+ * of 8 and at least Hkv*D (so slices of a fused projection's output can be passed).
+ * N*B*Hkv < 2^26. */
 xpress_status xpress_cache_append(const xpress_cache* c, int32_t layer, const void* k_new,
                                   const void* v_new, int64_t ld_new, const int32_t* seq, int32_t N,
                                   int32_t B, xpress_stream stream);
@@ -377,7 +378,7 @@ xpress_status xpress_cache_compact(const xpress_cache* c, int32_t* live, void* w
  * attending over each row alone. A query that sees no token gives 0 (and lse = -inf).
  * q: token i*B + b at element (i*B + b)*q_ld, [Hq, D] dense; out likewise with out_ld; both of the
  * cache's dtype, 16-byte aligned, strides multiples of 8. lse: [N*B, Hq] fp32, nullable, the
- * natural log of the sum of exp(scale * q.k). Hq a multiple of Hkv; B >= 1; N*B*Hq < 2^31;
+ * natural log of the sum of exp(scale * q.k). Hq a multiple of Hkv; B >= 1; N*B*Hq < 2^26;
  * 0 < scale <= 1e6; 0 <= shared <= table_ld*page. Scores below -1e30 / scale count as masked.
  * Values in masked places (beyond a row's end, in later tokens of the block) do not reach the
  * result, whatever they are. */
@@ -409,7 +410,7 @@ xpress_status xpress_block_attention(const xpress_cache* c, int32_t layer, const
  * appended. u: [N, B] fp32 in [0, 1) (nullable if temperature is NULL). blk: [N, B] int64;
  * out: [N, B] int64; accepted, drop: [N] int32; logits and q: XPRESS_BF16, _F16 or _F32 with row
  * strides ld >= V and q_ld >= V in elements, any alignment of the rows to their own elements.
- * 1 <= B <= 64; 1 <= V < 2^31. Deterministic: the same inputs give the same tokens. */
+ * 1 <= B <= 64; 1 <= V < 2^31; N*B*ceil((V+7)/8192) < 2^24. Deterministic: the same inputs give the same tokens. */
 xpress_status xpress_verify_workspace_size(int32_t n_max, int32_t B, int64_t V, size_t* bytes);
 xpress_status xpress_verify_draft(const void* logits, uint32_t logits_dtype, int64_t ld,
                                   const int64_t* blk, const int32_t* draft_len, const void* q,

@@ -31,6 +31,7 @@ hipError_t launch_block_attention(const xpress_cache& c, int layer, const void* 
                                   hipStream_t s);
 
 size_t verify_scratch_bytes(int N, int B, int64_t V);
+int64_t verify_items(int N, int B, int64_t V);  // workgroups
 hipError_t launch_verify_draft(const void* logits, uint32_t logits_dtype, int64_t ld,
                                const int64_t* blk, const int32_t* draft_len, const void* q,
                                uint32_t q_dtype, int64_t q_ld, const float* temperature,

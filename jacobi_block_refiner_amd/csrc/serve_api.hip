@@ -71,8 +71,8 @@ xpress_status check_attention(const xpress_cache* c, int32_t N, int32_t B, int32
   if (B < 1) return fail(XPRESS_ERR_ARG, "B=%d < 1", B);
   if (Hq < 1 || Hq % c->Hkv)
     return fail(XPRESS_ERR_ARG, "Hq=%d not a positive multiple of Hkv=%d", Hq, c->Hkv);
-  if ((int64_t)N * B >= (int64_t)1 << 31 || (int64_t)N * B * Hq >= (int64_t)1 << 31)
-    return fail(XPRESS_ERR_ARG, "N*B*Hq = %d*%d*%d is not below 2^31", N, B, Hq);
+  if ((int64_t)N * B >= (int64_t)1 << 26 || (int64_t)N * B * Hq >= (int64_t)1 << 26)
+    return fail(XPRESS_ERR_ARG, "N*B*Hq = %d*%d*%d is not below 2^26", N, B, Hq);
   return XPRESS_OK;
 }
 
@@ -81,8 +81,8 @@ xpress_status check_verify(int32_t N, int32_t B, int64_t V) {
   if (B < 1 || B > 64) return fail(XPRESS_ERR_ARG, "B=%d outside [1, 64]", B);
   if (V < 1 || V >= (int64_t)1 << 31)
     return fail(XPRESS_ERR_ARG, "V=%lld outside [1, 2^31)", (long long)V);
-  if ((int64_t)N * B >= (int64_t)1 << 31)
-    return fail(XPRESS_ERR_ARG, "N*B = %d*%d is not below 2^31", N, B);
+  if ((int64_t)N * B >= (int64_t)1 << 24 || xpress::verify_items(N, B, V) >= (int64_t)1 << 24)
+    return fail(XPRESS_ERR_ARG, "N=%d, B=%d, V=%lld is too large a launch", N, B, (long long)V);
   return XPRESS_OK;
 }
 
@@ -151,8 +151,8 @@ xpress_status xpress_cache_append(const xpress_cache* c, int32_t layer, const vo
   if (layer < 0 || layer >= c->n_layers)
     return fail(XPRESS_ERR_ARG, "layer=%d outside [0, %d)", layer, c->n_layers);
   if (B < 0) return fail(XPRESS_ERR_ARG, "B=%d < 0", B);
-  if ((int64_t)N * B * c->Hkv >= (int64_t)1 << 31)
-    return fail(XPRESS_ERR_ARG, "N*B*Hkv = %d*%d*%d is not below 2^31", N, B, c->Hkv);
+  if ((int64_t)N * B * c->Hkv >= (int64_t)1 << 26)
+    return fail(XPRESS_ERR_ARG, "N*B*Hkv = %d*%d*%d is not below 2^26", N, B, c->Hkv);
   if (ld_new < (int64_t)c->Hkv * c->D || ld_new % 8)
     return fail(XPRESS_ERR_ARG, "ld_new=%lld must be >= Hkv*D=%d and a multiple of 8",
                 (long long)ld_new, c->Hkv * c->D);
@@ -221,7 +221,7 @@ xpress_status xpress_block_attention(const xpress_cache* c, int32_t layer, const
     return fail(XPRESS_ERR_ARG, "shared=%d outside [0, table_ld*page=%lld]", shared,
                 (long long)c->table_ld * c->page);
   if (N == 0) return XPRESS_OK;
-  if (xpress::attention_items(*c, N, B, Hq, shared) >= (int64_t)1 << 31)
+  if (xpress::attention_items(*c, N, B, Hq, shared) >= (int64_t)1 << 23)
     return fail(XPRESS_ERR_ARG, "N=%d, B=%d, Hq=%d over tables of %lld tokens is too large a launch",
                 N, B, Hq, (long long)c->table_ld * c->page);
   XP_PTR(q);

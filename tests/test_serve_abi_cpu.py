@@ -81,7 +81,7 @@ def test_cache_calls_check_their_arguments():
     says(L().xpress_cache_append(c, 0, FAKE, FAKE, 1016, None, 4, 16, None), b"ld_new")
     says(L().xpress_cache_append(c, 0, FAKE, FAKE, 1028, None, 4, 16, None), b"ld_new")
     says(L().xpress_cache_append(c, 0, ODD8, FAKE, 1024, None, 4, 16, None), b"k_new")
-    says(L().xpress_cache_append(c, 0, FAKE, FAKE, 1024, None, 16, 1 << 28, None), b"2^31")
+    says(L().xpress_cache_append(c, 0, FAKE, FAKE, 1024, None, 16, 1 << 28, None), b"2^26")
     says(L().xpress_cache_trim(c, ODD2, 4, None, None), b"seq")
     says(L().xpress_cache_compact(c, None, FAKE, 1 << 30, None), b"live")
     says(L().xpress_cache_compact(c, FAKE, FAKE, 64, None), b"workspace", xpress.ERR_WORKSPACE)
@@ -95,7 +95,7 @@ def test_attention_checks_its_arguments():
 
     for args, text in ((dict(layer=2), b"layer"), (dict(N=-1), b"N=-1"), (dict(N=17), b"rows"),
                        (dict(B=0), b"B=0"), (dict(Hq=0), b"Hq"), (dict(Hq=12), b"Hq"),
-                       (dict(B=1 << 24), b"2^31"), (dict(q_ld=4088), b"q_ld"),
+                       (dict(B=1 << 24), b"2^26"), (dict(q_ld=4088), b"q_ld"),
                        (dict(q_ld=4100), b"q_ld"), (dict(out_ld=4100), b"out_ld"),
                        (dict(scale=0.0), b"scale"), (dict(scale=-1.0), b"scale"),
                        (dict(scale=float("nan")), b"scale"), (dict(scale=1e7), b"scale"),
