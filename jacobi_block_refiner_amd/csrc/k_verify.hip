@@ -2,13 +2,20 @@
 //
 // A row's weights are w(v) = 2^((x_v - m) c), c = log2(e) / T, m the row's maximum. Rows are cut into
 // chunks of kChunk ids; stats_kernel leaves each chunk's maximum, its id and the sum of its weights
-// (relative to the chunk's own maximum), and draw_kernel joins the chunks of a block's rows, tests
-// the drafts, and finds the token: first the chunk whose running sum passes u * total, then the id
-// inside it, the only part of the row that is read again.
+// (relative to the chunk's own maximum), and the last chunk of a row joins them and tests the row's
+// draft. For the one row of each block where a token is drawn, sums_kernel forms the chunks' sums
+// once more in 64 bits (left_kernel what the drafts' probabilities leave of them), and draw_kernel
+// finds the token: first the chunk whose running sum passes u * total, then the id inside it.
 //
-// Weights and sums are kept in 64 bits. A draw from V ids has borders 1/V apart: weights that are
-// off by 2^-24 would shift a border of a flat distribution of 151,936 ids by several percent of
-// their distance and change that share of the tokens; at 2e-12 it is one in 10^6.
+// Precision. A draw from V ids has borders 1/V apart: weights that are off by 2^-24 would shift a
+// border of a flat distribution of 151,936 ids by several percent of their distance and change that
+// share of the tokens; at 2e-12 it is one in 10^6. A test u q S < w has one border and takes 32-bit
+// weights; where the two sides are within 1e-5 of each other the row is summed anew in 64 bits.
+// (64 bits for all rows: 74 against MEASURED_STATS us at 512 rows of 151,936 ids.)
+//
+// Rows after a block's first refusal do not matter. Chunks go by slot, all blocks' first slots
+// first, and a chunk whose block is known to have been refused earlier returns at once. How many
+// do depends on timing; the result does not, since rows up to the first refusal are never left out.
 #include "serve.hpp"
 #include "xpress_common.hpp"
 
@@ -17,8 +24,8 @@ namespace xpress {
 namespace {
 
 constexpr int kThreads = 256;
+constexpr int kDraw = 1024;  // threads of draw_kernel: one workgroup a block, bound by latency
 constexpr int kChunk = 8192;  // ids of a chunk: 32 a thread
-constexpr int kMaxB = 64;
 
 template <class T> __device__ __forceinline__ float to_f32(T x);
 template <> __device__ __forceinline__ float to_f32(uint16_t x) { return bf16_to_f32(x); }
@@ -95,7 +102,11 @@ struct Args {
   int64_t* out;
   int32_t *accepted, *drop;
   Part* part;     // [N*B, chunks]
-  double* left;   // [N, chunks]: what is left of the refused row's chunks (with q)
+  Part* row;      // [N*B]: the rows' own
+  double* sums;   // [N, chunks]: the row of the draw (without a refused point draft)
+  double* left;   // [N, chunks]: what is left of it beside the drafts' probabilities
+  int32_t* done;  // [N*B]: chunks that are in
+  int32_t* stop;  // [N]: first refused slot so far (B: none)
 };
 
 // An element of q by its type code.
@@ -114,20 +125,48 @@ __device__ __forceinline__ double scale_of(const Args& A, int n) {
   return t > 0.f ? fmax(1.4426950408889634 / (double)t, 1e-300) : 0.0;
 }
 
+// Chunks travel between workgroups of different XCDs: stores and loads at the card's scope, which
+// neither leave a value in an L2 nor take one from it.
+__device__ __forceinline__ void put(Part* at, const Part& p) {
+  uint64_t* w = reinterpret_cast<uint64_t*>(at);
+  const uint64_t lo = (uint64_t)__double_as_longlong(p.sum);
+  const uint64_t hi = (uint64_t)__float_as_uint(p.m) | (uint64_t)(uint32_t)p.arg << 32;
+  __hip_atomic_store(w, lo, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  __hip_atomic_store(w + 1, hi, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+}
+__device__ __forceinline__ Part get(const Part* at) {
+  const uint64_t* w = reinterpret_cast<const uint64_t*>(at);
+  const uint64_t lo = __hip_atomic_load(w, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const uint64_t hi = __hip_atomic_load(w + 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  return Part{__longlong_as_double((int64_t)lo), __uint_as_float((uint32_t)hi), (int)(hi >> 32)};
+}
+
 __device__ __forceinline__ double wave_sum(double v) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) v += __shfl_xor(v, d);
   return v;
 }
 
-// One chunk of one row. Bound by HBM: 16 KiB of bf16 a workgroup, eight workgroups a CU; the 18
-// operations of 64 bits a weight are about as long as its two bytes' way from HBM.
+template <int NT> __device__ double block_sum(double v) {
+  __shared__ double s_sum[NT / 64];
+  v = wave_sum(v);
+  __syncthreads();
+  if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = v;
+  __syncthreads();
+  double t = 0;
+#pragma unroll
+  for (int i = 0; i < NT / 64; ++i) t += s_sum[i];
+  return t;  // the same in every thread
+}
+
+// One chunk of one row. Bound by HBM: 16 KiB of bf16 a workgroup, eight workgroups a CU.
 template <class T>
 __global__ __launch_bounds__(kThreads) void stats_kernel(Args A) {
   constexpr int E = Row<T>::E, K = kChunk / kThreads / E;
   const int c = blockIdx.x % A.chunks, y = blockIdx.x / A.chunks, t = threadIdx.x;
-  const int n = y % A.N, s = y / A.N;
-  if (s > limit_of(A, n)) return;
+  const int n = y % A.N, s = y / A.N, limit = limit_of(A, n);
+  if (s > limit || s > __hip_atomic_load(A.stop + n, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT))
+    return;
   const int64_t r = (int64_t)n * A.B + s;
   const Row<T> row(static_cast<const T*>(A.logits) + r * A.ld, A.V);
   float x[K][E];
@@ -141,7 +180,7 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(Args A) {
 #pragma unroll
   for (int d = 32; d; d >>= 1) m = fmaxf(m, __shfl_xor(m, d));
   const double scale = scale_of(A, n);
-  double sum = 0;
+  float sum = 0;
   int arg = INT_MAX;
   if (scale == 0.0) {
 #pragma unroll
@@ -158,16 +197,22 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(Args A) {
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum += x[k][e] == m ? 1.0 : 0.0;
+        for (int e = 0; e < E; ++e) sum += x[k][e] == m ? 1.f : 0.f;
     } else {
+      // (x - m first: near the maximum, where the weight is, the product then has no large terms
+      // that cancel; the maximum with -1e30 turns NaN and -inf into no weight)
+      const float c32 = (float)fmin(scale, 1e37);
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < E; ++e) sum += pow2(((double)x[k][e] - (double)m) * scale);
+        for (int e = 0; e < E; ++e)
+          sum += __builtin_amdgcn_exp2f(fmaxf((x[k][e] - m) * c32, -1e30f));
     }
-    sum = wave_sum(sum);
+#pragma unroll
+    for (int d = 32; d; d >>= 1) sum += __shfl_xor(sum, d);
   }
   __shared__ Part s_part[kThreads / 64];
+  __shared__ int s_last, s_again;
   if ((t & 63) == 0) s_part[t >> 6] = Part{sum, m, arg};
   __syncthreads();
   if (t == 0) {
@@ -181,102 +226,124 @@ __global__ __launch_bounds__(kThreads) void stats_kernel(Args A) {
       if (scale != 0.0) p.sum += o.sum * weight(o.m, p.m, scale);
       if (o.m == p.m) p.arg = min(p.arg, o.arg);
     }
-    A.part[r * A.chunks + c] = p;
+    put(A.part + r * A.chunks + c, p);
+    // The chunk is in memory before it is counted: its stores go through the caches to the card's
+    // point of coherence, and the wait is for their acknowledgement. (A release at the card's scope
+    // also writes back the whole L2 of the XCD and an acquire empties it, once a chunk: 278 against
+    // 74 us at 512 rows of 151,936 ids.)
+    asm volatile("" ::: "memory");
+    __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
+    asm volatile("" ::: "memory");
+    s_last = __hip_atomic_fetch_add(A.done + r, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT) ==
+             A.chunks - 1;
+    s_again = 0;
+  }
+  __syncthreads();
+  if (!s_last) return;
+  // the row's last chunk: join them, test the draft
+  const Part* part = A.part + r * A.chunks;
+  Part w{0, -INFINITY, INT_MAX};
+  bool ok = false;
+  int64_t d = -1;
+  double test = 0, drafted = 0;  // u q, and the draft's weight
+  if (t < 64) {
+    if (s < limit) {
+      d = A.blk[r + 1];
+      if (d < 0 || d >= A.V) d = -1;
+      if (scale != 0.0 && d >= 0) {
+        const double qd = A.q ? q_at(A, ((int64_t)n * (A.B - 1) + s) * A.q_ld + d) : 1.0;
+        test = (double)A.u[r] * qd;
+      }
+    }
+    for (int i = t; i < A.chunks; i += 64) {
+      const Part o = get(part + i);
+      if (o.arg != INT_MAX) argmax_merge(w.m, w.arg, o.m, o.arg);
+    }
+#pragma unroll
+    for (int x = 32; x; x >>= 1) argmax_merge(w.m, w.arg, __shfl_xor(w.m, x), __shfl_xor(w.arg, x));
+    if (scale == 0.0) {
+      ok = w.arg != INT_MAX && d == w.arg;
+    } else if (w.arg != INT_MAX && d >= 0) {
+      for (int i = t; i < A.chunks; i += 64) {
+        const Part o = get(part + i);
+        if (o.arg != INT_MAX) w.sum += o.sum * weight(o.m, w.m, scale);
+      }
+      w.sum = wave_sum(w.sum);
+      drafted = weight(to_f32<T>(row.x[d]), w.m, scale);
+      ok = test * w.sum < drafted;
+      if (t == 0) s_again = fabs(test * w.sum - drafted) <= 1e-5 * drafted;
+    }
+    if (t == 0) s_part[0] = w;
+  }
+  __syncthreads();
+  if (s_again) {
+    const float top = s_part[0].m;
+    double all = 0;
+    for (int v = t; v < A.V; v += kThreads) all += weight(to_f32<T>(row.x[v]), top, scale);
+    all = block_sum<kThreads>(all);
+    ok = test * all < drafted;
+  }
+  if (t == 0) {
+    A.row[r] = w;
+    if (s < limit && !ok) atomicMin(A.stop + n, s);
   }
 }
 
-// What a block's rows say, in every thread of the workgroup.
+// What a block's rows say.
 struct Verdict {
-  int a;          // drafts that stand
-  bool refused;   // the draft of slot a + 1 was tested and refused
-  float m;        // row a's maximum, its id (INT_MAX: no weight), and the sum of its weights
-  int arg;
-  double sum;
+  int a;         // drafts that stand
+  bool refused;  // the draft of slot a + 1 was tested and refused
+  Part row;      // row a's maximum, its id (INT_MAX: no weight), and the sum of its weights
 };
 
-template <class T>
-__device__ Verdict decide(const Args& A, int n, double scale) {
-  __shared__ Part s_row[kMaxB];
-  __shared__ int s_ok[kMaxB];
-  const int lane = threadIdx.x & 63, limit = limit_of(A, n);
-  for (int s = threadIdx.x >> 6; s <= limit; s += kThreads / 64) {
-    const int64_t r = (int64_t)n * A.B + s;
-    const Part* part = A.part + r * A.chunks;
-    float m = -INFINITY;
-    int arg = INT_MAX;
-    for (int c = lane; c < A.chunks; c += 64) {
-      const Part p = part[c];
-      if (p.arg != INT_MAX) argmax_merge(m, arg, p.m, p.arg);
-    }
-#pragma unroll
-    for (int d = 32; d; d >>= 1) argmax_merge(m, arg, __shfl_xor(m, d), __shfl_xor(arg, d));
-    double sum = 0;
-    if (scale != 0.0 && arg != INT_MAX) {
-      for (int c = lane; c < A.chunks; c += 64) {
-        const Part p = part[c];
-        if (p.arg != INT_MAX) sum += p.sum * weight(p.m, m, scale);
-      }
-      sum = wave_sum(sum);
-    }
-    bool ok = false;
-    if (s < limit && arg != INT_MAX) {
-      const int64_t d = A.blk[r + 1];
-      if (scale == 0.0) {
-        ok = d == arg;
-      } else if (d >= 0 && d < A.V) {
-        const float x = to_f32<T>(static_cast<const T*>(A.logits)[r * A.ld + d]);
-        const double qd = A.q ? q_at(A, ((int64_t)n * (A.B - 1) + s) * A.q_ld + d) : 1.0;
-        ok = (double)A.u[r] * qd * sum < weight(x, m, scale);
-      }
-    }
-    if (lane == 0) {
-      s_row[s] = Part{sum, m, arg};
-      s_ok[s] = ok;
-    }
-  }
-  __syncthreads();
+__device__ __forceinline__ Verdict verdict_of(const Args& A, int n) {
+  const int limit = limit_of(A, n), stop = A.stop[n];
   Verdict v;
-  v.a = 0;
-  while (v.a < limit && s_ok[v.a]) ++v.a;
-  v.refused = v.a < limit;
-  v.m = s_row[v.a].m;
-  v.arg = s_row[v.a].arg;
-  v.sum = s_row[v.a].sum;
+  v.refused = stop < limit;
+  v.a = min(stop, limit);
+  v.row = A.row[(int64_t)n * A.B + v.a];
   return v;
 }
 
-// The row of the draw: weights p = 2^((x - m) c); with `residual` what the refused draft d leaves
-// of them, max(p / sum - q, 0), or p without d for a point draft.
+__global__ __launch_bounds__(kThreads) void clear_kernel(int32_t* done, int rows, int32_t* stop,
+                                                         int N, int B) {
+  const int i = blockIdx.x * kThreads + threadIdx.x;
+  if (i < rows) done[i] = 0;
+  if (i < N) stop[i] = B;
+}
+
+// The row of the draw: weights p = 2^((x - m) c); where the draft d was refused, what it leaves of
+// them: p without d, or (`drawn`) max(p / sum - q, 0).
 template <class T> struct Weights {
   const Args& A;
   const T* x;
   float m;
   double scale, sum;
-  bool residual;
+  bool drawn;
   int64_t d, q_row;
 };
 
+// With the target's own weights, without a refused point draft.
 template <class T>
 __device__ Weights<T> weights_of(const Args& A, int n, const Verdict& v, double scale) {
   const int64_t r = (int64_t)n * A.B + v.a;
-  return Weights<T>{A, static_cast<const T*>(A.logits) + r * A.ld, v.m, scale, v.sum, v.refused,
-                    v.refused ? A.blk[r + 1] : -1, ((int64_t)n * (A.B - 1) + v.a) * A.q_ld};
+  return Weights<T>{A, static_cast<const T*>(A.logits) + r * A.ld, v.row.m, scale, 0, false,
+                    v.refused && !A.q ? A.blk[r + 1] : -1, ((int64_t)n * (A.B - 1) + v.a) * A.q_ld};
 }
 
 // The weights that this thread's ids of chunk c keep, in `w`: pieces a thread apart (coalesced),
 // or with `in_order` one after the other, so that threads hold ascending ranges of ids. All loads
 // are in flight before the first weight is formed. Returns the first piece.
-template <class T, bool in_order>
+template <class T, int NT, bool in_order>
 __device__ __forceinline__ int64_t chunk_weights(const Row<T>& row, const Weights<T>& left, int c,
-                                                 double (&w)[kChunk / kThreads]) {
-  constexpr int E = Row<T>::E, K = kChunk / kThreads / E;
+                                                 double (&w)[kChunk / NT]) {
+  constexpr int E = Row<T>::E, K = kChunk / NT / E;
   const int64_t j0 = (int64_t)c * (kChunk / E) + threadIdx.x * (in_order ? K : 1);
-  constexpr int step = in_order ? 1 : kThreads;
+  constexpr int step = in_order ? 1 : NT;
   float x[K][E], q[K][E];
 #pragma unroll
   for (int k = 0; k < K; ++k) row.load(j0 + k * step, x[k]);
-  const bool drawn = left.residual && left.A.q;
-  if (drawn) {
+  if (left.drawn) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -291,29 +358,16 @@ __device__ __forceinline__ int64_t chunk_weights(const Row<T>& row, const Weight
     for (int e = 0; e < E; ++e) {
       const double p = weight(x[k][e], left.m, left.scale);
       const int64_t v = (j0 + k * step) * E - row.off + e;
-      w[k * E + e] = drawn                            ? fmax(p / left.sum - (double)q[k][e], 0.0)
-                     : left.residual && v == left.d ? 0.0
-                                                    : p;
+      w[k * E + e] = left.drawn    ? fmax(p / left.sum - (double)q[k][e], 0.0)
+                     : v == left.d ? 0.0
+                                   : p;
     }
   return j0;
 }
 
-// Sum over the workgroup, the same in every thread.
-__device__ double block_sum(double v) {
-  __shared__ double s_sum[kThreads / 64];
-  v = wave_sum(v);
-  __syncthreads();
-  if ((threadIdx.x & 63) == 0) s_sum[threadIdx.x >> 6] = v;
-  __syncthreads();
-  double t = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) t += s_sum[i];
-  return t;
-}
-
 // Sum of the values of the threads before this one.
-__device__ double block_before(double v) {
-  __shared__ double s_wave[kThreads / 64];
+template <int NT> __device__ double block_before(double v) {
+  __shared__ double s_wave[NT / 64];
   const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
   double x = v;
 #pragma unroll
@@ -326,118 +380,134 @@ __device__ double block_before(double v) {
   __syncthreads();
   double before = 0;
 #pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) before += i < w ? s_wave[i] : 0.0;
+  for (int i = 0; i < NT / 64; ++i) before += i < w ? s_wave[i] : 0.0;
   const double up = __shfl_up(x, 1);
   return before + (lane ? up : 0.0);
 }
 
-// With the drafts' probabilities: what is left of each chunk of the refused row.
+// The row of the draw in 64 bits: each chunk's sum.
+template <class T>
+__global__ __launch_bounds__(kThreads) void sums_kernel(Args A) {
+  const int n = blockIdx.x / A.chunks, c = blockIdx.x % A.chunks;
+  const double scale = scale_of(A, n);
+  if (scale == 0.0) return;
+  const Verdict v = verdict_of(A, n);
+  if (v.row.arg == INT_MAX) return;
+  const Weights<T> left = weights_of<T>(A, n, v, scale);
+  double w[kChunk / kThreads], sum = 0;
+  chunk_weights<T, kThreads, false>(Row<T>(left.x, A.V), left, c, w);
+#pragma unroll
+  for (int i = 0; i < kChunk / kThreads; ++i) sum += w[i];
+  sum = block_sum<kThreads>(sum);
+  if (threadIdx.x == 0) A.sums[(int64_t)n * A.chunks + c] = sum;
+}
+
+template <int NT> __device__ double total_of(const double* sums, int chunks) {
+  double mine = 0;
+  for (int c = threadIdx.x; c < chunks; c += NT) mine += sums[c];
+  return block_sum<NT>(mine);
+}
+
+// With the drafts' probabilities: what they leave of each chunk of a refused row.
 template <class T>
 __global__ __launch_bounds__(kThreads) void left_kernel(Args A) {
   const int n = blockIdx.x / A.chunks, c = blockIdx.x % A.chunks;
   const double scale = scale_of(A, n);
   if (scale == 0.0) return;
-  const Verdict v = decide<T>(A, n, scale);
-  if (!v.refused || v.arg == INT_MAX) return;
-  const Weights<T> left = weights_of<T>(A, n, v, scale);
+  const Verdict v = verdict_of(A, n);
+  if (!v.refused || v.row.arg == INT_MAX) return;
+  Weights<T> left = weights_of<T>(A, n, v, scale);
+  left.drawn = true;
+  left.sum = total_of<kThreads>(A.sums + (int64_t)n * A.chunks, A.chunks);
   double w[kChunk / kThreads], sum = 0;
-  chunk_weights<T, false>(Row<T>(left.x, A.V), left, c, w);
+  chunk_weights<T, kThreads, false>(Row<T>(left.x, A.V), left, c, w);
 #pragma unroll
   for (int i = 0; i < kChunk / kThreads; ++i) sum += w[i];
-  sum = block_sum(sum);
+  sum = block_sum<kThreads>(sum);
   if (threadIdx.x == 0) A.left[(int64_t)n * A.chunks + c] = sum;
+}
+
+// The lowest id whose running sum passes u * total.
+template <class T>
+__device__ int draw_token(const Args& A, int n, const Verdict& v, double scale) {
+  const int t = threadIdx.x;
+  Weights<T> left = weights_of<T>(A, n, v, scale);
+  const double* sums = A.sums + (int64_t)n * A.chunks;
+  double total = total_of<kDraw>(sums, A.chunks);
+  if (total == 0) return (int)left.d;  // nothing beside the point draft: it holds all the weight
+  if (v.refused && A.q) {
+    const double* rest = A.left + (int64_t)n * A.chunks;
+    const double what = total_of<kDraw>(rest, A.chunks);
+    if (what > 0) {  // else nothing is left: the target itself
+      left.drawn = true;
+      left.sum = total;
+      sums = rest;
+      total = what;
+    }
+  }
+  const double goal = (double)A.u[(int64_t)n * A.B + A.B - 1] * total;
+  const int per = (A.chunks + kDraw - 1) / kDraw;
+  const int c0 = min(t * per, A.chunks), c1 = min(c0 + per, A.chunks);
+  double mine = 0;
+  for (int c = c0; c < c1; ++c) mine += sums[c];
+  __shared__ int s_chunk, s_last, s_token, s_end;
+  __shared__ double s_before;
+  if (t == 0) {
+    s_chunk = s_token = INT_MAX;
+    s_last = s_end = -1;
+  }
+  double run = block_before<kDraw>(mine);  // (its barriers order the lines above)
+  double before = run;
+  int hit = INT_MAX, last = -1;
+  for (int c = c0; c < c1; ++c) {
+    const double w = sums[c];
+    if (w > 0) {
+      last = c;
+      if (hit == INT_MAX && run + w > goal) {
+        hit = c;
+        before = run;
+      }
+    }
+    run += w;
+  }
+  if (hit != INT_MAX) atomicMin(&s_chunk, hit);
+  if (last >= 0) atomicMax(&s_last, last);
+  __syncthreads();
+  const bool rounded = s_chunk == INT_MAX;  // the sums' last roundings: take the last weight
+  const int chunk = rounded ? s_last : s_chunk;
+  if (!rounded && hit == chunk) s_before = before;
+  constexpr int K = kChunk / kDraw;
+  double w[K];
+  const Row<T> row(left.x, A.V);
+  const int64_t v0 = chunk_weights<T, kDraw, true>(row, left, chunk, w) * Row<T>::E - row.off;
+  mine = 0;
+#pragma unroll
+  for (int i = 0; i < K; ++i) mine += w[i];
+  run = block_before<kDraw>(mine);
+  run += rounded ? 0.0 : s_before;
+  int end = -1, first = INT_MAX;
+#pragma unroll
+  for (int i = 0; i < K; ++i) {
+    run += w[i];
+    if (w[i] > 0) {
+      end = (int)(v0 + i);
+      if (!rounded && first == INT_MAX && run > goal) first = end;
+    }
+  }
+  if (first != INT_MAX) atomicMin(&s_token, first);
+  if (end >= 0) atomicMax(&s_end, end);
+  __syncthreads();
+  return s_token == INT_MAX ? s_end : s_token;
 }
 
 // The verdict on one block, and its token.
 template <class T>
-__global__ __launch_bounds__(kThreads) void draw_kernel(Args A) {
+__global__ __launch_bounds__(kDraw) void draw_kernel(Args A) {
   const int n = blockIdx.x, t = threadIdx.x;
   const double scale = scale_of(A, n);
-  const Verdict v = decide<T>(A, n, scale);
-  int token = -1;
-  if (v.arg != INT_MAX && scale == 0.0) token = v.arg;
-  if (v.arg != INT_MAX && scale != 0.0) {
-    Weights<T> left = weights_of<T>(A, n, v, scale);
-    const Row<T> row(left.x, A.V);
-    const Part* part = A.part + ((int64_t)n * A.B + v.a) * A.chunks;
-    // a point draft's chunk is summed anew without it (a difference of sums would lose what is
-    // left beside a draft that holds nearly all the weight)
-    int point_chunk = -1;
-    double point_sum = 0;
-    if (v.refused && !A.q && left.d >= 0 && left.d < A.V) {
-      point_chunk = (int)((left.d + row.off) / kChunk);
-      double w[kChunk / kThreads];
-      chunk_weights<T, false>(row, left, point_chunk, w);
-#pragma unroll
-      for (int i = 0; i < kChunk / kThreads; ++i) point_sum += w[i];
-      point_sum = block_sum(point_sum);
-    }
-    auto chunk_sum = [&](int c) {
-      if (left.residual && A.q) return A.left[(int64_t)n * A.chunks + c];
-      if (left.residual && c == point_chunk) return point_sum;
-      return part[c].arg == INT_MAX ? 0.0 : part[c].sum * weight(part[c].m, v.m, scale);
-    };
-    const int per = (A.chunks + kThreads - 1) / kThreads;
-    const int c0 = min(t * per, A.chunks), c1 = min(c0 + per, A.chunks);
-    double mine = 0, total = 0;
-    for (int round = 0; round < 2; ++round) {
-      mine = 0;
-      for (int c = c0; c < c1; ++c) mine += chunk_sum(c);
-      total = block_sum(mine);
-      if (!left.residual || total > 0) break;
-      left.residual = false;  // nothing is left: the target itself
-    }
-    const double goal = (double)A.u[(int64_t)n * A.B + A.B - 1] * total;
-    __shared__ int s_chunk, s_last, s_token, s_end;
-    __shared__ double s_before;
-    if (t == 0) {
-      s_chunk = INT_MAX;
-      s_last = s_end = -1;
-      s_token = INT_MAX;
-    }
-    double run = block_before(mine);  // (its barriers order the lines above)
-    double before = run;
-    int hit = INT_MAX, last = -1;
-    for (int c = c0; c < c1; ++c) {
-      const double w = chunk_sum(c);
-      if (w > 0) {
-        last = c;
-        if (hit == INT_MAX && run + w > goal) {
-          hit = c;
-          before = run;
-        }
-      }
-      run += w;
-    }
-    if (hit != INT_MAX) atomicMin(&s_chunk, hit);
-    if (last >= 0) atomicMax(&s_last, last);
-    __syncthreads();
-    const bool rounded = s_chunk == INT_MAX;  // the sums' last roundings: take the last weight
-    const int chunk = rounded ? s_last : s_chunk;
-    if (!rounded && hit == chunk) s_before = before;
-    __syncthreads();
-    constexpr int K = kChunk / kThreads;
-    double w[K];
-    const int64_t v0 = chunk_weights<T, true>(row, left, chunk, w) * Row<T>::E - row.off;
-    mine = 0;
-#pragma unroll
-    for (int i = 0; i < K; ++i) mine += w[i];
-    run = block_before(mine) + (rounded ? 0.0 : s_before);
-    int end = -1, first = INT_MAX;
-#pragma unroll
-    for (int i = 0; i < K; ++i) {
-      run += w[i];
-      if (w[i] > 0) {
-        end = (int)(v0 + i);
-        if (!rounded && first == INT_MAX && run > goal) first = end;
-      }
-    }
-    if (first != INT_MAX) atomicMin(&s_token, first);
-    if (end >= 0) atomicMax(&s_end, end);
-    __syncthreads();
-    token = s_token == INT_MAX ? s_end : s_token;
-  }
-  for (int s = t; s < A.B; s += kThreads)
+  const Verdict v = verdict_of(A, n);
+  const int token = v.row.arg == INT_MAX ? -1 : scale == 0.0 ? v.row.arg : draw_token<T>(A, n, v, scale);
+  for (int s = t; s < A.B; s += kDraw)
     A.out[(int64_t)n * A.B + s] = s < v.a ? A.blk[(int64_t)n * A.B + s + 1] : s == v.a ? token : -1;
   if (t == 0) {
     A.accepted[n] = v.a;
@@ -446,15 +516,25 @@ __global__ __launch_bounds__(kThreads) void draw_kernel(Args A) {
 }
 
 template <class T> hipError_t launch_t(const Args& A, hipStream_t s) {
-  hipLaunchKernelGGL(stats_kernel<T>, dim3((unsigned)A.chunks * A.N * A.B), dim3(kThreads), 0, s, A);
+  const int rows = A.N * A.B;
+  hipLaunchKernelGGL(clear_kernel, dim3((rows + kThreads - 1) / kThreads), dim3(kThreads), 0, s,
+                     A.done, rows, A.stop, A.N, A.B);
   hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
+  hipLaunchKernelGGL(stats_kernel<T>, dim3((unsigned)A.chunks * A.N * A.B), dim3(kThreads), 0, s, A);
+  e = hipGetLastError();
+  if (e != hipSuccess) return e;
+  if (A.temperature != nullptr) {
+    hipLaunchKernelGGL(sums_kernel<T>, dim3((unsigned)A.chunks * A.N), dim3(kThreads), 0, s, A);
+    e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
   if (A.q != nullptr && A.temperature != nullptr) {
     hipLaunchKernelGGL(left_kernel<T>, dim3((unsigned)A.chunks * A.N), dim3(kThreads), 0, s, A);
     e = hipGetLastError();
     if (e != hipSuccess) return e;
   }
-  hipLaunchKernelGGL(draw_kernel<T>, dim3(A.N), dim3(kThreads), 0, s, A);
+  hipLaunchKernelGGL(draw_kernel<T>, dim3(A.N), dim3(kDraw), 0, s, A);
   return hipGetLastError();
 }
 
@@ -465,7 +545,8 @@ int chunks_of(int64_t V) { return (int)((V + 7 + kChunk - 1) / kChunk); }
 int64_t verify_items(int N, int B, int64_t V) { return (int64_t)N * B * chunks_of(V); }
 
 size_t verify_scratch_bytes(int N, int B, int64_t V) {
-  return (size_t)N * chunks_of(V) * (B * sizeof(Part) + sizeof(double));
+  return (size_t)N * chunks_of(V) * (B * sizeof(Part) + 2 * sizeof(double)) +
+         (size_t)N * B * (sizeof(Part) + sizeof(int32_t)) + (size_t)N * sizeof(int32_t);
 }
 
 hipError_t launch_verify_draft(const void* logits, uint32_t logits_dtype, int64_t ld,
@@ -474,9 +555,13 @@ hipError_t launch_verify_draft(const void* logits, uint32_t logits_dtype, int64_
                                const float* u, int N, int B, int64_t V, int64_t* out,
                                int32_t* accepted, int32_t* drop, void* ws, hipStream_t s) {
   Args A{logits, ld, q_ld, blk, draft_len, q, q_dtype, temperature, u, N, B, (int)V, chunks_of(V),
-         out, accepted, drop, nullptr, nullptr};
+         out, accepted, drop, nullptr, nullptr, nullptr, nullptr, nullptr, nullptr};
   A.part = static_cast<Part*>(ws);
-  A.left = reinterpret_cast<double*>(A.part + (size_t)N * B * A.chunks);
+  A.row = A.part + (size_t)N * B * A.chunks;
+  A.sums = reinterpret_cast<double*>(A.row + (size_t)N * B);
+  A.left = A.sums + (size_t)N * A.chunks;
+  A.done = reinterpret_cast<int32_t*>(A.left + (size_t)N * A.chunks);
+  A.stop = A.done + (size_t)N * B;
   return logits_dtype == XPRESS_BF16  ? launch_t<uint16_t>(A, s)
          : logits_dtype == XPRESS_F16 ? launch_t<_Float16>(A, s)
                                       : launch_t<float>(A, s);
