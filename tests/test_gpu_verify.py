@@ -92,6 +92,26 @@ def test_drawn_drafts(N, B, V, pad, q_dtype):
         assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0]), seed
 
 
+@pytest.mark.parametrize("q_dtype", [None, torch.float32], ids=["point", "drawn"])
+@pytest.mark.parametrize("V", [97, 8200, 20011])
+def test_many_draws(q_dtype, V):
+    """Many blocks, a refusal in most, weights of exactly nothing between the others (masked ids, and
+    ids where the drafts' probability is the larger): every token is the definition's."""
+    N, B = 60000 // V + 40, 2
+    rng, x, blk, u, _, _ = draw(N, B, V, 77, agree=0.2)
+    x[:, rng.random(V) < 0.4] = -math.inf
+    t = strided(x, torch.float32, 1)
+    q = None
+    if q_dtype is not None:
+        noisy = x.reshape(N, B, V)[:, 0] + 0.5 * rng.standard_normal((N, V)).astype(np.float32)
+        q = strided(torch.softmax(torch.as_tensor(noisy), -1).numpy(), q_dtype, 3)
+    temperature = rng.choice([0.7, 1.0], N).astype(np.float32)
+    want = verify(f64(t), blk, None, None if q is None else f64(q), temperature, u)
+    got = run(t, blk, q=q, u=u, temperature=temperature)
+    assert (want[1] == 0).sum() > N / 10
+    assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0])
+
+
 def test_greedy_without_lists():
     """No temperature: argmax, lowest id on ties (also of -0 and +0)."""
     x = np.zeros((8, 900), np.float32) - 1
