@@ -1,12 +1,16 @@
 // Attention of drafted blocks over the paged cache (gfx950).
 //
 // Per kv head h the query rows of a batch are the N*B*G vectors q[token, h*G + g]. The keys fall in
-// two parts: the `shared` first tokens, which are the same for every request, and each request's
-// own. Work items are (head, tile of 32*NW query rows, range of keys): tiles over all requests'
-// rows for the shared part (its K and V are read once per tile of 256 rows instead of once per
-// request), tiles over one request's rows for its own part. Each item runs the softmax in one pass
-// over its keys with a running maximum and sum; where a row has more than one item, they leave
-// (sum of weighted values, maximum, sum) in the workspace and merge_kernel joins them.
+// two parts: the first tokens, which are the same for every request, and each request's own. Work
+// items are (head, tile of query rows, range of keys): tiles over all requests' rows for the shared
+// part (its K and V are read once per tile of 128 or 256 rows instead of once per request), tiles
+// over one request's rows for its own part. Each item runs the softmax in one pass over its keys with
+// a running maximum and sum; where a row has more than one item, they leave (sum of weighted values,
+// maximum, sum) in the workspace and merge_kernel joins them.
+//
+// The shared part is cut to whole tiles of 64 keys; what is left of it goes with the requests' own.
+// A request whose queries do not all see the whole shared part (a short or an empty row) takes all
+// its keys as its own. So no shared item has a mask.
 #include "serve.hpp"
 #include "cache_index.hpp"
 #include "xpress_common.hpp"
@@ -25,7 +29,8 @@ typedef short s16x4 __attribute__((ext_vector_type(4)));
 typedef short s16x8 __attribute__((ext_vector_type(8)));
 typedef uint32_t u32x2v __attribute__((ext_vector_type(2)));
 
-constexpr int kIds = 2048;  // table entries an item keeps in LDS: bounds its range of keys
+constexpr int kNarrow = 4, kWide = 8;  // waves (of 32 query rows) of an item
+constexpr int kIds = 1024;  // table entries an item keeps in LDS: bounds its range of keys
 
 struct Args {
   const uint16_t *q, *k, *v;  // k, v of the layer
@@ -36,11 +41,17 @@ struct Args {
   float c;  // scale * log2(e)
   // shared items: tiles of rows x splits of keys; own items the same per request
   int tiles_sh, s_sh, chunk_sh, tiles_own, s_own;
+  int slots_sh;  // slots of the shared part (items of this launch or of one before it)
+  int step_own;  // own ranges are multiples of it
   uint16_t* out;
   float* lse;
   float* po;   // [slots, N*B, Hq, D]
   float2* pml; // [slots, N*B, Hq]: maximum (log2 units), sum
 };
+
+template <bool F16> __device__ __forceinline__ float value(short x) {
+  return F16 ? (float)__builtin_bit_cast(_Float16, x) : bf16_to_f32((uint16_t)x);
+}
 
 // Two weights rounded to the type (to nearest even) in one register: the matrix core takes them as
 // bf16 or fp16. Relative error half a step each, against the 32-bit sum of the unrounded weights.
@@ -67,12 +78,19 @@ __device__ __forceinline__ float2 both_halves(float x) {
   return make_float2(__uint_as_float(r.x), __uint_as_float(r.y));
 }
 
+// Keys of one split of a request's n own keys.
+__device__ __forceinline__ int own_chunk(int n, int s_own, int step) {
+  return ((n + s_own - 1) / s_own + step - 1) / step * step;
+}
+// First of a request's own keys: 0 where some query of it does not see the whole shared part.
+__device__ __forceinline__ int own_begin(int len, int B, int shared) {
+  return in_sight(len, B, 0) >= shared ? shared : 0;
+}
 // Range of a request's own keys that split s of s_own covers.
-__device__ __forceinline__ int2 own_range(int len, int shared, int s, int s_own, int step) {
-  const int n = max(len - shared, 0);
-  const int chunk = ((n + s_own - 1) / s_own + step - 1) / step * step;
+__device__ __forceinline__ int2 own_range(int len, int first, int s, int s_own, int step) {
+  const int n = len - first, chunk = own_chunk(n, s_own, step);
   const int64_t a = (int64_t)s * chunk;
-  return make_int2(shared + (int)min(a, (int64_t)n), shared + (int)min(a + chunk, (int64_t)n));
+  return make_int2(first + (int)min(a, (int64_t)n), first + (int)min(a + chunk, (int64_t)n));
 }
 
 __device__ __forceinline__ int list_row(const Args& A, int i) {
@@ -84,37 +102,324 @@ __device__ __forceinline__ int list_len(const Args& A, int i) {
   return r < 0 ? 0 : clamp_len(A.len[r], A.ld, A.shift);
 }
 
-// One work item. Scores are formed transposed, S^T = K Q^T (32 keys x 32 queries a tile of the
-// matrix core), so a lane holds scores of one query only: maxima and sums stay in the lane up to
-// one exchange with the lane 32 further. The weights P^T leave the accumulator in the order in which
-// the second product O^T = V^T P^T takes its right operand, once V^T's keys are taken in the same
-// order: lane half h, element j of a step of 16 keys is key 8*(j/4) + 4*h + j%4. V^T comes from the
-// row-major V tile with transposing LDS reads of 4 keys x 16 channels.
+// A wave's 32 queries against tiles of KT keys in LDS. Scores are formed transposed, S^T = K Q^T (32
+// keys x 32 queries a tile of the matrix core), so a lane holds scores of one query only: maxima and
+// sums stay in the lane up to one exchange with the lane 32 further. The weights P^T leave the
+// accumulator in the order in which the second product O^T = V^T P^T takes its right operand, once
+// V^T's keys are taken in the same order: lane half h, element j of a step of 16 keys is key
+// 8*(j/4) + 4*h + j%4. V^T comes from the row-major V tile with transposing LDS reads of 4 keys x 16
+// channels. 16-byte pieces of a K or V row are placed with an XOR of the key's low bits, so that both
+// kinds of reads are free of bank conflicts.
+template <bool F16, int D, int KT> struct Core {
+  static constexpr int CPR = D / 8;           // 16-byte pieces of a row
+  static constexpr int KPC = 64 / CPR;        // keys of a 1 KiB copy
+  static constexpr int SIDE = KT * CPR * 16;  // bytes of a K or V tile
+  static constexpr int KH = KT / 32, KK = KT / 16, DT = D / 32, DS = D / 16;
+
+  char* lds;
+  int lane, h, col;
+  float c;
+  s16x8 qf[DS];
+  f32x16 s[KH], o[DT];
+  s16x8 pf[KK];
+  float m, l;
+
+  __device__ static int k_swizzle(int key) { return D == 64 ? (key >> 1) & 7 : key & 15; }
+  __device__ static int v_swizzle(int key) {
+    return D == 64 ? ((key >> 1) & 1) << 2 | ((key >> 2) & 3) : (key & 3) << 2 | ((key >> 2) & 3);
+  }
+
+  __device__ __forceinline__ void begin(void* tiles, const uint16_t* q, float scale) {
+    lds = static_cast<char*>(tiles);
+    lane = threadIdx.x & 63;
+    h = lane >> 5;
+    col = lane & 31;
+    c = scale;
+#pragma unroll
+    for (int x = 0; x < DS; ++x) qf[x] = *reinterpret_cast<const s16x8*>(q + 16 * x + 8 * h);
+#pragma unroll
+    for (int dt = 0; dt < DT; ++dt) o[dt] = f32x16{};
+    m = -1e30f;
+    l = 0.f;
+  }
+
+  // Scores of the K tile at byte kb.
+  __device__ __forceinline__ void scores(int kb) {
+    const int fk = k_swizzle(col);
+#pragma unroll
+    for (int d = 0; d < DS; ++d)
+#pragma unroll
+      for (int kh = 0; kh < KH; ++kh) {
+        const s16x8 k = *reinterpret_cast<const s16x8*>(lds + kb + (kh * 32 + col) * D * 2 +
+                                                        (((2 * d + h) ^ fk) * 16));
+        s[kh] = mfma<F16>(k, qf[d], d == 0 ? f32x16{} : s[kh]);
+      }
+  }
+
+  // Keys t0.. of which this lane's query sees those below vis.
+  __device__ __forceinline__ void mask(int t0, int vis) {
+#pragma unroll
+    for (int kh = 0; kh < KH; ++kh)
+#pragma unroll
+      for (int i = 0; i < 16; ++i)
+        s[kh][i] = t0 + kh * 32 + 8 * (i / 4) + 4 * h + i % 4 < vis ? s[kh][i] : -INFINITY;
+  }
+
+  // Takes the tile's maximum in. The sums are rescaled only when some row's maximum grew by more than
+  // 2^8 in weight: weights stay below 2^8, which 32-bit sums and the rounded weights' relative
+  // precision do not feel.
+  __device__ __forceinline__ void rise() {
+    float top = s[0][0];
+#pragma unroll
+    for (int kh = 0; kh < KH; ++kh)
+#pragma unroll
+      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kh][i]);
+    const float2 tops = both_halves(top);
+    top = fmaxf(tops.x, tops.y);
+    if (__any((top - m) * c > 8.f)) {
+      const float mn = fmaxf(m, top);
+      const float alpha = __builtin_amdgcn_exp2f((m - mn) * c);
+      l *= alpha;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) o[dt] *= alpha;
+      m = mn;
+    }
+  }
+
+  __device__ __forceinline__ void weights() {
+    const float mc = -m * c;
+    float sum[4] = {l, 0.f, 0.f, 0.f};
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk) {
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = __builtin_amdgcn_exp2f(fmaf(s[kk / 2][8 * (kk % 2) + 2 * j], c, mc));
+        const float b = __builtin_amdgcn_exp2f(fmaf(s[kk / 2][8 * (kk % 2) + 2 * j + 1], c, mc));
+        sum[j] += a + b;
+        w[j] = pack2<F16>(a, b);
+      }
+      pf[kk] = __builtin_bit_cast(s16x8, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+    l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
+  }
+
+  // Adds the weights times the V tile at byte vb.
+  __device__ __forceinline__ void values(int vb) {
+    const int i16 = lane & 15, vkey = 4 * h + (i16 >> 2);         // key of the transposing read
+    const int vpiece = ((lane >> 4) & 1) * 2 + ((i16 >> 1) & 1);  // 16-byte piece of 32 channels
+#pragma unroll
+    for (int kk = 0; kk < KK; ++kk)
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt) {
+        s16x4 part[2];
+#pragma unroll
+        for (int x = 0; x < 2; ++x) {
+          const int key = kk * 16 + 8 * x + vkey;
+          part[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+              (__attribute__((address_space(3))) s16x4*)(lds + vb + key * D * 2 +
+                                                         (((dt * 4 + vpiece) ^ v_swizzle(key)) * 16) +
+                                                         (i16 & 1) * 8));
+        }
+        o[dt] = mfma<F16>(__builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7), pf[kk],
+                          o[dt]);
+      }
+  }
+
+  // Whether the V tile holds a value that is not finite.
+  __device__ __forceinline__ bool wild(int vb) const {
+    constexpr uint32_t E = F16 ? 0x7c00u : 0x7f80u;
+    bool found = false;
+#pragma unroll 4
+    for (int x = lane; x < KT * CPR; x += 64) {
+      const uint4 u = *reinterpret_cast<const uint4*>(lds + vb + x * 16);
+      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+      for (int y = 0; y < 4; ++y) found |= (w[y] & E) == E || ((w[y] >> 16) & E) == E;
+    }
+    return __any(found);
+  }
+
+  // A tile some of whose keys some rows do not see. Values in masked places must not reach a row,
+  // and 0 * inf would: where such a tile holds a value that is not finite it goes key by key
+  // (slowly), each row taking the keys that it sees.
+  __device__ __forceinline__ void masked_tile(int kb, int vb, int t0, int vis) {
+    scores(kb);
+    mask(t0, vis);
+    rise();
+    if (!wild(vb)) {
+      weights();
+      values(vb);
+      return;
+    }
+    const float mc = -m * c;
+#pragma unroll 1
+    for (int key = 0; key < KT; ++key) {
+      float dot = 0.f;
+#pragma unroll
+      for (int d = 0; d < DS; ++d) {
+        const s16x8 k = *reinterpret_cast<const s16x8*>(lds + kb + key * D * 2 +
+                                                        (((2 * d + h) ^ k_swizzle(key)) * 16));
+        s16x8 q = qf[d];
+        asm volatile("" : "+v"(q));  // (or its conversions stay in registers all along)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) dot = fmaf(value<F16>(k[j]), value<F16>(q[j]), dot);
+      }
+      const float2 dots = both_halves(dot);
+      const bool sees = t0 + key < vis;
+      const float p = sees ? __builtin_amdgcn_exp2f(fmaf(dots.x + dots.y, c, mc)) : 0.f;
+      l += h == 0 ? p : 0.f;
+#pragma unroll
+      for (int dt = 0; dt < DT; ++dt)
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int piece = dt * 4 + i;
+          const s16x4 x = *reinterpret_cast<const s16x4*>(
+              lds + vb + key * D * 2 + ((piece ^ v_swizzle(key)) * 16) + h * 8);
+#pragma unroll
+          for (int y = 0; y < 4; ++y) {
+            const float at = o[dt][4 * i + y];
+            o[dt][4 * i + y] = sees ? fmaf(p, value<F16>(x[y]), at) : at;
+          }
+        }
+    }
+  }
+};
+
+// Where an item's K and V come from: a range of one row's tokens, its table entries in LDS. A lane
+// copies 16 bytes of one key's line at a time; keys past the range copy the last one (their weights
+// are masked, or nothing reads them). Page ids are read a tile ahead: the chain from LDS to an address
+// took a thousand cycles of every tile when it stood before each copy.
+template <int D, int KT, int NW> struct Source {
+  using C = Core<false, D, KT>;
+  static constexpr int CW = KT / C::KPC / NW;  // copies of K (and of V) a wave issues per tile
+  static_assert(CW * C::KPC * NW == KT, "copies divide evenly");
+  const uint16_t *k, *v;  // of the head
+  const int* ids;
+  int kbeg, kend, shift, key0;
+  uint32_t base, page_elems;  // LDS address of this wave's first copy; elements of a page
+  int64_t off[CW], off_before[CW];
+  int id[CW], line[CW];
+
+  __device__ __forceinline__ void begin(const Args& A, int hk, const int* ids_, int kbeg_, int kend_,
+                                        uint32_t lds) {
+    const int lane = threadIdx.x & 63;
+    const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+    ids = ids_;
+    kbeg = kbeg_;
+    kend = kend_;
+    shift = A.shift;
+    key0 = wave * C::KPC + lane / C::CPR;
+    base = lds + wave * 1024;
+    page_elems = (uint32_t)(A.Hkv * D) << A.shift;
+    const int64_t head = (int64_t)hk * D << A.shift;
+    k = A.k + head;
+    v = A.v + head;
+    ask(0);
+  }
+  // Page ids and lines of tile t's keys are under way.
+  __device__ __forceinline__ void ask(int t) {
+#pragma unroll
+    for (int i = 0; i < CW; ++i) {
+      const int pos = min(kbeg + t * KT + key0 + i * NW * C::KPC, kend - 1);
+      id[i] = ids[(pos >> shift) - (kbeg >> shift)];
+      line[i] = pos & ((1 << shift) - 1);
+    }
+  }
+  // Turns to the tile asked for, and asks for tile `next`.
+  __device__ __forceinline__ void turn(int next) {
+#pragma unroll
+    for (int i = 0; i < CW; ++i) {
+      off_before[i] = off[i];
+      off[i] = (int64_t)((uint64_t)(uint32_t)id[i] * page_elems) + line[i] * D;
+    }
+    ask(next);
+  }
+  __device__ __forceinline__ void copy_k(int to) const {
+    const int piece = threadIdx.x % C::CPR;
+#pragma unroll
+    for (int i = 0; i < CW; ++i)
+      lds_copy16_at(k + off[i] + (piece ^ C::k_swizzle(key0 + i * NW * C::KPC)) * 8,
+                    base + to + i * NW * 1024);
+  }
+  // V of the tile turned to, or of the one before it.
+  template <bool BEFORE> __device__ __forceinline__ void copy_v(int to) const {
+    const int piece = threadIdx.x % C::CPR;
+#pragma unroll
+    for (int i = 0; i < CW; ++i)
+      lds_copy16_at(v + (BEFORE ? off_before[i] : off[i]) +
+                        (piece ^ C::v_swizzle(key0 + i * NW * C::KPC)) * 8,
+                    base + to + i * NW * 1024);
+  }
+};
+
+// Waits until at most N of this wave's copies are under way and all its LDS reads are done, then for
+// the other waves.
+template <int N> __device__ __forceinline__ void meet() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0x0070 | (N & 15) | ((N >> 4) << 14));  // vmcnt(N), lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+// Waits for this wave's LDS reads, then for the other waves.
+__device__ __forceinline__ void meet_reads() {
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt(0xC07F);  // lgkmcnt(0)
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+}
+
+// Order of a wide item's products (N/2 of each kind) and their LDS reads: eight reads ahead of the
+// first product, and every read about eight products ahead of its own, so that none waits for LDS.
+// (Left to itself the compiler reads two fragments, waits for both and multiplies: 1450-1850 cycles
+// a tile where the products alone take 1024.)
+template <int N> __device__ __forceinline__ void feed() {
+  __builtin_amdgcn_sched_group_barrier(0x100, 8, 0);  // LDS reads
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);  // matrix core
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < N / 4; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 2, 0);
+  }
+#pragma unroll
+  for (int i = 0; i < N / 2; ++i) {
+    __builtin_amdgcn_sched_group_barrier(0x008, 1, 0);
+    __builtin_amdgcn_sched_group_barrier(0x100, 1, 0);
+  }
+}
+
+// One work item: NW waves of 32 query rows each; K and V tiles of KT keys go from HBM straight into an
+// LDS ring of three or four stages.
 //
-// K and V tiles of KT keys go from HBM straight into an LDS ring of three stages, two tiles in
-// flight while one is used; one barrier a tile. 16-byte pieces of a row are placed with an XOR of
-// the key's low bits, so that both kinds of reads are free of bank conflicts.
+// Narrow (NW = 4, two or three workgroups a CU): for items that wait for HBM. Tiles are taken one
+// after the other with one barrier each; the workgroups of a CU fill each other's waits.
+//
+// Wide (NW = 8, one workgroup a CU): shared items that the matrix core bounds. The two waves of a SIMD
+// are half a tile apart: while one multiplies (scores of tile t, values of tile t-1) the other forms
+// weights, and after each such half they meet and change roles. A tile needs about as many cycles of
+// the matrix core as of the vector unit; with both waves in step, each unit waited for the other.
 template <bool F16, int D, int NW, int KT>
-__global__ __launch_bounds__(NW * 64) void attend_kernel(Args A) {
-  constexpr int CPR = D / 8;               // 16-byte pieces of a row
-  constexpr int KPC = 64 / CPR;            // keys of a 1 KiB copy
-  constexpr int CW = KT / KPC / NW;        // copies of K (and of V) a wave issues per tile
-  constexpr int NS = 3;
-  constexpr int SIDE = KT * CPR * 16;      // bytes of a K or V tile
-  constexpr int KH = KT / 32, KK = KT / 16, DT = D / 32, DS = D / 16;
-  static_assert(CW * KPC * NW == KT, "copies divide evenly");
-  __shared__ uint4 s_tile[NS * 2 * SIDE / 16];
+__global__ __launch_bounds__(NW * 64, NW == kWide || D == 128 ? 2 : D == 256 ? 1 : 3) void attend_kernel(
+    Args A) {
+  using C = Core<F16, D, KT>;
+  using S = Source<D, KT, NW>;
+  constexpr bool WIDE = NW == kWide;
+  constexpr int NS = WIDE ? 4 : 3, STAGE = 2 * C::SIDE, CW = S::CW;
+  __shared__ uint4 s_tile[NS * STAGE / 16];
   __shared__ int s_ids[kIds];
 
-  const int lane = threadIdx.x & 63;
+  const int lane = threadIdx.x & 63, h = lane >> 5, col = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int h = lane >> 5, col = lane & 31;
 
   // the item
   int id = blockIdx.x;
   const int n_sh = A.Hkv * A.tiles_sh * A.s_sh;
-  const bool is_shared = id < n_sh;
-  int hk, tile, slot, req, kbeg, kend, nrows, trow;
+  const bool is_shared = WIDE || id < n_sh;
+  int hk, tile, slot, req, kbeg, kend, nrows;
   if (is_shared) {
     hk = id % A.Hkv;
     id /= A.Hkv;
@@ -132,256 +437,170 @@ __global__ __launch_bounds__(NW * 64) void attend_kernel(Args A) {
     id /= A.s_own;
     tile = id % A.tiles_own;
     req = id / A.tiles_own;
-    slot = A.s_sh + s;
-    const int2 r = own_range(list_len(A, req), A.shared, s, A.s_own, KT);
+    slot = A.slots_sh + s;
+    const int len = list_len(A, req);
+    const int2 r = own_range(len, own_begin(len, A.B, A.shared), s, A.s_own, A.step_own);
     kbeg = r.x;
     kend = r.y;
     nrows = A.B * A.G;
   }
-  const bool direct = A.s_sh + A.s_own == 1;
+  const bool direct = A.slots_sh + A.s_own == 1;
   if (kend <= kbeg && !direct) return;
-  trow = max(list_row(A, req), 0);
 
-  // this lane's query
+  // this lane's query; `blind`: it sees nothing here (what it computes is dropped)
   const int rl = (tile * NW + wave) * 32 + col;
   const bool valid = rl < nrows;
   const int token = (is_shared ? 0 : req * A.B) + min(rl, nrows - 1) / A.G;
   const int hq = hk * A.G + min(rl, nrows - 1) % A.G;
-  const int sight = min(in_sight(list_len(A, token / A.B), A.B, token % A.B), kend);
-  const int vis = valid ? sight : INT_MAX;
-  int vmin = vis, vmax = valid ? sight : 0;
-  for (int x = 16; x; x >>= 1) {
-    vmin = min(vmin, __shfl_xor(vmin, x));
-    vmax = max(vmax, __shfl_xor(vmax, x));
-  }
-  vmin = __builtin_amdgcn_readfirstlane(vmin);
-  vmax = __builtin_amdgcn_readfirstlane(vmax);
-
-  s16x8 qf[DS];
+  const int len = list_len(A, token / A.B);
+  const int sight = min(in_sight(len, A.B, token % A.B), kend);
+  const bool blind =
+      !valid || sight <= kbeg || (is_shared && own_begin(len, A.B, A.shared) < A.shared);
+  C w;
+  w.begin(s_tile, A.q + token * A.q_ld + (int64_t)hq * D, A.c);
   {
-    const uint16_t* qp = A.q + token * A.q_ld + (int64_t)hq * D + 8 * h;
-#pragma unroll
-    for (int s = 0; s < DS; ++s) qf[s] = *reinterpret_cast<const s16x8*>(qp + 16 * s);
-  }
-
-  const int pfirst = kbeg >> A.shift;
-  {
-    const int n = kend > kbeg ? ((kend - 1) >> A.shift) - pfirst + 1 : 0;
-    const int32_t* t = A.table + (int64_t)trow * A.ld + pfirst;
+    const int first = kbeg >> A.shift, n = kend > kbeg ? ((kend - 1) >> A.shift) - first + 1 : 0;
+    const int32_t* t = A.table + (int64_t)max(list_row(A, req), 0) * A.ld + first;
     for (int j = threadIdx.x; j < n; j += NW * 64) s_ids[j] = clamp_page(t[j], A.n_pages);
   }
   __syncthreads();
-
-  const uint32_t sbase = (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint4*)s_tile;
   const int nt = (kend - kbeg + KT - 1) / KT;
-  // lane's piece of each copy: its key's line, and which 16 bytes of it (keys past the range read
-  // the last one: their weights are masked)
-  auto copy_tile = [&](int t, int stage) {
-#pragma unroll
-    for (int c = 0; c < CW; ++c) {
-      const int ci = wave + NW * c, key = ci * KPC + lane / CPR, piece = lane % CPR;
-      const int pos = min(kbeg + t * KT + key, kend - 1);
-      const int page_id = s_ids[(pos >> A.shift) - pfirst];
-      const int64_t off = line_offset(page_id, hk, pos & ((1 << A.shift) - 1), A.Hkv, A.shift, D);
-      const int fk = D == 64 ? (key >> 1) & 7 : key & 15;
-      const int fv = D == 64 ? ((key >> 1) & 1) << 2 | ((key >> 2) & 3) : (key & 3) << 2 | ((key >> 2) & 3);
-      const uint32_t to = sbase + stage * 2 * SIDE + ci * 1024;
-      lds_copy16_at(A.k + off + ((piece ^ fk) * 8), to);
-      lds_copy16_at(A.v + off + ((piece ^ fv) * 8), to + SIDE);
+  S src;
+  if (nt > 0)
+    src.begin(A, hk, s_ids, kbeg, kend,
+              (uint32_t)(uintptr_t)(__attribute__((address_space(3))) uint4*)s_tile);
+  if constexpr (WIDE) {
+    // Copies by group: group t is K(t+3) and V(t+2), issued in half-step 2t or 2t+1, when the last
+    // readers of their stages (those of tile t-1 in half-step 2t-1) are done. From half-step 2t+1 on
+    // the groups up to t-2 are in, so K(t+1) and V(t). (Tiles past the end are read by no one.)
+    auto step = [](int& at, int first) { at = at == first + (NS - 1) * STAGE ? first : at + STAGE; };
+    int kto = 0, vto = C::SIDE;
+    auto group = [&](int t) {
+      src.turn(t + 4);
+      src.copy_k(kto);
+      step(kto, 0);
+      src.template copy_v<true>(vto);
+      step(vto, C::SIDE);
+    };
+    src.turn(1);
+    src.copy_k(kto);
+    step(kto, 0);
+    group(-2);
+    group(-1);
+    const bool second = wave >= 4;
+    meet<4 * CW>();
+    if (second) {
+      group(0);
+      meet<4 * CW>();
     }
-  };
-
-  // LDS byte offsets of this lane's fragment reads inside a stage
-  const int fk = D == 64 ? (col >> 1) & 7 : col & 15;
-  const int i16 = lane & 15, vkey = 4 * h + (i16 >> 2);           // key of the transposing read
-  const int vpiece = ((lane >> 4) & 1) * 2 + ((i16 >> 1) & 1);    // 16-byte piece inside 32 channels
-  auto k_frag = [&](int stage, int kh, int s) {
-    const int byte = stage * 2 * SIDE + (kh * 32 + col) * D * 2 + (((2 * s + h) ^ fk) * 16);
-    return *reinterpret_cast<const s16x8*>(reinterpret_cast<const char*>(s_tile) + byte);
-  };
-  auto v_frag = [&](int stage, int kk, int dt) {
-    s16x4 part[2];
-#pragma unroll
-    for (int x = 0; x < 2; ++x) {
-      const int key = kk * 16 + 8 * x + vkey;
-      const int fv = D == 64 ? ((key >> 1) & 1) << 2 | ((key >> 2) & 3) : (key & 3) << 2 | ((key >> 2) & 3);
-      const int byte = stage * 2 * SIDE + SIDE + key * D * 2 + (((dt * 4 + vpiece) ^ fv) * 16) + (i16 & 1) * 8;
-      part[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-          (__attribute__((address_space(3))) s16x4*)(reinterpret_cast<char*>(s_tile) + byte));
+    int kb = 0, vb = (NS - 1) * STAGE + C::SIDE;  // K(t), V(t-1)
+    auto half = [&](int t) {  // what follows the products of tile t: weights, and the two meetings
+      if (second)
+        meet_reads();
+      else
+        meet<2 * CW>();
+      group(t + second);
+      w.rise();
+      w.weights();
+      if (second)
+        meet<4 * CW>();
+      else
+        meet_reads();
+      step(kb, 0);
+      step(vb, C::SIDE);
+    };
+    w.scores(kb);
+    half(0);
+    for (int t = 1; t < nt; ++t) {
+      w.scores(kb);
+      w.values(vb);
+      feed<C::KH * C::DS + C::KK * C::DT>();
+      half(t);
     }
-    return __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
-  };
-
-  float m = -1e30f, l = 0.f;
-  f32x16 o[DT];
+    w.values(vb);
+    if (!second) meet_reads();
+    meet<0>();
+  } else {
+    const int vis = blind ? INT_MAX : sight;
+    int vmin = vis, vmax = blind ? 0 : sight;
 #pragma unroll
-  for (int dt = 0; dt < DT; ++dt) o[dt] = f32x16{};
-
-  // Start of a tile: its copies have landed in every wave, and tile t-1's stage is free again.
-  int stage = 0;
-  auto enter = [&](int t) {
-    // this wave's copies of tile t (those of tile t+1 may be in flight) and its reads of tile t-1:
-    // vmcnt, lgkmcnt(0)
-    if (t + 1 < nt)
-      __builtin_amdgcn_s_waitcnt(0x0070 | (2 * CW));
-    else
-      __builtin_amdgcn_s_waitcnt(0x0070);
-    asm volatile("" ::: "memory");
-    __builtin_amdgcn_s_barrier();
-    asm volatile("" ::: "memory");
-    if (t + 2 < nt) copy_tile(t + 2, stage == 0 ? 2 : stage - 1);
-  };
-  auto leave = [&] { stage = stage == NS - 1 ? 0 : stage + 1; };
-  f32x16 s[KH];
-  s16x8 pf[KK];
-  auto scores = [&] {
-#pragma unroll
-    for (int d = 0; d < DS; ++d)
-#pragma unroll
-      for (int kh = 0; kh < KH; ++kh)
-        s[kh] = mfma<F16>(k_frag(stage, kh, d), qf[d], d == 0 ? f32x16{} : s[kh]);
-  };
-  auto weights = [&] {
-    float top = s[0][0];
-#pragma unroll
-    for (int kh = 0; kh < KH; ++kh)
-#pragma unroll
-      for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kh][i]);
-    const float2 tops = both_halves(top);
-    top = fmaxf(tops.x, tops.y);
-    // The sums are rescaled only when some row's maximum grew by more than 2^8 in weight: weights
-    // stay below 2^8, which 32-bit sums and the rounded weights' relative precision do not feel.
-    if (__any((top - m) * A.c > 8.f)) {
-      const float mn = fmaxf(m, top);
-      const float alpha = __builtin_amdgcn_exp2f((m - mn) * A.c);
-      l *= alpha;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) o[dt] *= alpha;
-      m = mn;
+    for (int x = 16; x; x >>= 1) {
+      vmin = min(vmin, __shfl_xor(vmin, x));
+      vmax = max(vmax, __shfl_xor(vmax, x));
     }
-    const float mc = -m * A.c;
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk) {
-      uint32_t w[4];
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const float a = __builtin_amdgcn_exp2f(fmaf(s[kk / 2][8 * (kk % 2) + 2 * j], A.c, mc));
-        const float b = __builtin_amdgcn_exp2f(fmaf(s[kk / 2][8 * (kk % 2) + 2 * j + 1], A.c, mc));
-        l += a + b;
-        w[j] = pack2<F16>(a, b);
-      }
-      pf[kk] = __builtin_bit_cast(s16x8, make_uint4(w[0], w[1], w[2], w[3]));
+    vmax = __builtin_amdgcn_readfirstlane(vmax);
+    vmin = __builtin_amdgcn_readfirstlane(vmin);
+    int t = 0, at = 0, to = 0;
+    auto copy_both = [&](int next) {
+      src.turn(next);
+      src.copy_k(to);
+      src.template copy_v<false>(to + C::SIDE);
+      to = to == 2 * STAGE ? 0 : to + STAGE;
+    };
+    auto enter = [&] {
+      if (t + 1 < nt)
+        meet<2 * CW>();
+      else
+        meet<0>();
+      if (t + 2 < nt) copy_both(t + 3);
+    };
+    auto leave = [&] {
+      at = at == 2 * STAGE ? 0 : at + STAGE;
+      ++t;
+    };
+    if (nt > 0) copy_both(1);
+    if (nt > 1) copy_both(2);
+    // tiles that every row of the wave sees whole, then those that some see in part
+    const int whole = vmax == 0 ? 0 : (vmin - kbeg) / KT;
+    while (t < nt && t < whole) {
+      enter();
+      w.scores(at);
+      w.rise();
+      w.weights();
+      w.values(at + C::SIDE);
+      leave();
     }
-  };
-
-  if (nt > 0) copy_tile(0, 0);
-  if (nt > 1) copy_tile(1, 1);
-  int t = 0;
-  // tiles that every row of the wave sees whole
-  for (; t < nt && kbeg + t * KT + KT <= vmin; ++t) {
-    enter(t);
-    scores();
-    weights();
-#pragma unroll
-    for (int kk = 0; kk < KK; ++kk)
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt) o[dt] = mfma<F16>(v_frag(stage, kk, dt), pf[kk], o[dt]);
-    leave();
-  }
-  // the others
-  for (; t < nt; ++t) {
-    enter(t);
-    const int t0 = kbeg + t * KT;
-    if (t0 < vmax) {
-      scores();
-#pragma unroll
-      for (int kh = 0; kh < KH; ++kh)
-#pragma unroll
-        for (int i = 0; i < 16; ++i)
-          s[kh][i] = t0 + kh * 32 + 8 * (i / 4) + 4 * h + i % 4 < vis ? s[kh][i] : -INFINITY;
-      weights();
-      // Values in masked places must not reach a row: 0 * inf would. Keys with a value that is not
-      // finite are taken out of the product and added one by one to the rows that see them.
-      uint64_t bad;
-      {
-        const uint4* row = s_tile + (stage * 2 * SIDE + SIDE) / 16 + lane % KT * CPR;
-        constexpr uint32_t E = F16 ? 0x7c00u : 0x7f80u;
-        bool found = false;
-#pragma unroll 4
-        for (int x = 0; x < CPR; ++x) {
-          const uint4 u = row[x];
-          const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-          for (int y = 0; y < 4; ++y) found |= (w[y] & E) == E || ((w[y] >> 16) & E) == E;
-        }
-        bad = __ballot(found);
-        if (KT < 64) bad &= (uint64_t(1) << (KT & 63)) - 1;
-      }
-#pragma unroll
-      for (int kk = 0; kk < KK; ++kk) {
-        s16x8 keep;
-#pragma unroll
-        for (int j = 0; j < 8; ++j)
-          keep[j] = (bad >> (kk * 16 + 8 * (j / 4) + 4 * h + j % 4)) & 1 ? 0 : -1;
-#pragma unroll
-        for (int dt = 0; dt < DT; ++dt)
-          o[dt] = mfma<F16>(v_frag(stage, kk, dt) & keep, pf[kk], o[dt]);
-      }
-#pragma unroll 1
-      for (uint64_t left = bad; left; left &= left - 1) {
-        const int key = __builtin_ctzll(left);
-        const bool sees = t0 + key < vis;
-#pragma unroll
-        for (int kk = 0; kk < KK; ++kk) {
-          if (key / 16 != kk) continue;
-          s16x8 keep;
-#pragma unroll
-          for (int j = 0; j < 8; ++j) keep[j] = kk * 16 + 8 * (j / 4) + 4 * h + j % 4 == key ? -1 : 0;
-#pragma unroll
-          for (int dt = 0; dt < DT; ++dt) {
-            const f32x16 one = mfma<F16>(v_frag(stage, kk, dt) & keep, pf[kk] & keep, f32x16{});
-#pragma unroll
-            for (int i = 0; i < 16; ++i) o[dt][i] += sees ? one[i] : 0.f;
-          }
-        }
-      }
+    while (t < nt) {
+      enter();
+      const int t0 = kbeg + t * KT;
+      if (t0 < vmax) w.masked_tile(at, at + C::SIDE, t0, vis);
+      leave();
     }
-    leave();
   }
 
-  const float2 ls = both_halves(l);
-  l = ls.x + ls.y;
+  const float2 ls = both_halves(w.l);
+  const float l = blind ? 0.f : ls.x + ls.y;
   if (!valid) return;
   const int64_t row = (int64_t)token * A.Hq + hq;
   if (direct) {
-    const float inv = l == 0.f ? 0.f : 1.f / l;
+    const float inv = 1.f / l;
     uint16_t* op = A.out + token * A.out_ld + (int64_t)hq * D + 4 * h;
 #pragma unroll
-    for (int dt = 0; dt < DT; ++dt)
+    for (int dt = 0; dt < C::DT; ++dt)
 #pragma unroll
       for (int i = 0; i < 4; ++i) {
-        uint2 w;
-        w.x = pack2<F16>(o[dt][4 * i] * inv, o[dt][4 * i + 1] * inv);
-        w.y = pack2<F16>(o[dt][4 * i + 2] * inv, o[dt][4 * i + 3] * inv);
-        *reinterpret_cast<uint2*>(op + dt * 32 + 8 * i) = w;
+        uint2 u;
+        u.x = pack2<F16>(w.o[dt][4 * i] * inv, w.o[dt][4 * i + 1] * inv);
+        u.y = pack2<F16>(w.o[dt][4 * i + 2] * inv, w.o[dt][4 * i + 3] * inv);
+        *reinterpret_cast<uint2*>(op + dt * 32 + 8 * i) = l == 0.f ? make_uint2(0, 0) : u;
       }
     if (A.lse && h == 0)
-      A.lse[row] = l == 0.f ? -INFINITY : (m * A.c + log2f(l)) * 0.69314718056f;
+      A.lse[row] = l == 0.f ? -INFINITY : (w.m * A.c + log2f(l)) * 0.69314718056f;
     return;
   }
   const int64_t at = (int64_t)slot * A.N * A.B * A.Hq + row;
   float* op = A.po + at * D + 4 * h;
 #pragma unroll
-  for (int dt = 0; dt < DT; ++dt)
+  for (int dt = 0; dt < C::DT; ++dt)
 #pragma unroll
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<float4*>(op + dt * 32 + 8 * i) =
-          make_float4(o[dt][4 * i], o[dt][4 * i + 1], o[dt][4 * i + 2], o[dt][4 * i + 3]);
-  if (h == 0) A.pml[at] = make_float2(m * A.c, l);
+          make_float4(w.o[dt][4 * i], w.o[dt][4 * i + 1], w.o[dt][4 * i + 2], w.o[dt][4 * i + 3]);
+  if (h == 0) A.pml[at] = make_float2(w.m * A.c, l);
 }
 
 // Joins a row's items: weights relative to the largest maximum, in slot order.
-template <bool F16, int D, int KT>
+template <bool F16, int D>
 __global__ __launch_bounds__(256) void merge_kernel(Args A) {
   constexpr int LPR = D / 4;  // lanes of a row
   const int64_t row = (int64_t)blockIdx.x * (256 / LPR) + threadIdx.x / LPR;
@@ -390,25 +609,31 @@ __global__ __launch_bounds__(256) void merge_kernel(Args A) {
   const int d = threadIdx.x % LPR * 4;
   const int token = (int)(row / A.Hq), hq = (int)(row % A.Hq);
   const int len = list_len(A, token / A.B);
+  const int own = len - own_begin(len, A.B, A.shared);
+  const int slots = A.slots_sh + (own ? (own - 1) / own_chunk(own, A.s_own, A.step_own) + 1 : 0);
   float m = -INFINITY, l = 0.f;
   float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-  for (int s = 0; s < A.s_sh + A.s_own; ++s) {
-    if (s >= A.s_sh) {
-      const int2 r = own_range(len, A.shared, s - A.s_sh, A.s_own, KT);
-      if (r.y <= r.x) break;
+  for (int s0 = 0; s0 < slots; s0 += 4) {  // four slots' loads in flight
+    float2 ml[4];
+    float4 x[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      const int64_t at = (int64_t)min(s0 + j, slots - 1) * n + row;
+      ml[j] = A.pml[at];
+      x[j] = *reinterpret_cast<const float4*>(A.po + at * D + d);
     }
-    const int64_t at = s * n + row;
-    const float2 ml = A.pml[at];
-    if (ml.y == 0.f) continue;
-    const float4 x = *reinterpret_cast<const float4*>(A.po + at * D + d);
-    const float mn = fmaxf(m, ml.x);
-    const float a = __builtin_amdgcn_exp2f(m - mn), b = __builtin_amdgcn_exp2f(ml.x - mn);
-    l = l * a + ml.y * b;
-    o.x = o.x * a + x.x * b;
-    o.y = o.y * a + x.y * b;
-    o.z = o.z * a + x.z * b;
-    o.w = o.w * a + x.w * b;
-    m = mn;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      if (s0 + j >= slots || ml[j].y == 0.f) continue;
+      const float mn = fmaxf(m, ml[j].x);
+      const float a = __builtin_amdgcn_exp2f(m - mn), b = __builtin_amdgcn_exp2f(ml[j].x - mn);
+      l = l * a + ml[j].y * b;
+      o.x = o.x * a + x[j].x * b;
+      o.y = o.y * a + x[j].y * b;
+      o.z = o.z * a + x[j].z * b;
+      o.w = o.w * a + x[j].w * b;
+      m = mn;
+    }
   }
   const float inv = l == 0.f ? 0.f : 1.f / l;
   uint2 w;
@@ -420,14 +645,20 @@ __global__ __launch_bounds__(256) void merge_kernel(Args A) {
 
 // How a call is cut into items.
 struct Plan {
+  bool wide;  // the shared part goes to a launch of wide items
   int tiles_sh, s_sh, chunk_sh, tiles_own, s_own;
   int slots() const { return s_sh + s_own; }
 };
 
-constexpr int waves_of(int D) { return D == 256 ? 4 : 8; }
-constexpr int step_of(int D) { return D == 256 ? 32 : 64; }
-constexpr int kItems = 512;   // items a call is cut into where its rows alone give fewer
-constexpr int kSplits = 64;   // splits of one row's keys at most (more where ids do not fit in LDS)
+constexpr int kTile = 64;  // the shared part is a multiple of it
+constexpr int narrow_step(int D) { return D == 64 ? 64 : 32; }  // keys of a tile
+constexpr int wide_step(int D) { return D == 256 ? 32 : 64; }
+constexpr int kCUs = 256;
+constexpr int kWideRows = 512;  // query rows a head from which the shared part goes to wide items
+constexpr int kWideItems = 2048;
+constexpr int kItems = 512;  // narrow items wanted where the rows alone give fewer
+constexpr int kLeast = 128;  // keys of a split at least
+constexpr int kSplits = 64;  // splits of one row's keys at most (more where ids do not fit in LDS)
 
 int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 
@@ -435,17 +666,38 @@ int64_t ceil_div(int64_t a, int64_t b) { return (a + b - 1) / b; }
 int64_t most_keys(const xpress_cache& c) { return (int64_t)(kIds - 2) * c.page / 64 * 64; }
 
 Plan plan_of(const xpress_cache& c, int N, int B, int Hq, int shared) {
-  const int NW = waves_of(c.D), KT = step_of(c.D), G = Hq / c.Hkv;
-  const int64_t own = (int64_t)c.table_ld * c.page - shared, most = most_keys(c);
+  const int G = Hq / c.Hkv;
+  const int64_t cap = (int64_t)c.table_ld * c.page, most = most_keys(c), own = cap - shared;
+  const int64_t rows = (int64_t)N * B * G;
   Plan p{};
-  p.tiles_own = (int)ceil_div((int64_t)B * G, NW * 32);
-  int64_t s = ceil_div(kItems, (int64_t)N * c.Hkv * p.tiles_own);
-  s = std::max<int64_t>(1, std::min({s, ceil_div(own, 2 * KT), (int64_t)kSplits}));
-  p.s_own = (int)std::max(s, ceil_div(own, most));
+  p.wide = shared > 0 && rows >= kWideRows;
+  p.tiles_own = (int)ceil_div((int64_t)B * G, kNarrow * 32);
+  const int want = shared > 0 && !p.wide ? kItems / 2 : kItems;
+  int64_t s = ceil_div(want, (int64_t)N * c.Hkv * p.tiles_own);
+  s = std::max<int64_t>(1, std::min({s, ceil_div(own, kLeast), (int64_t)kSplits}));
+  // (a request that does not see the whole shared part has less than shared + B keys, all its own)
+  p.s_own = (int)std::max(s, ceil_div(std::max(own, std::min<int64_t>(cap, (int64_t)shared + B)), most));
   if (shared > 0) {
-    p.tiles_sh = (int)ceil_div((int64_t)N * B * G, NW * 32);
-    s = ceil_div(kItems, (int64_t)c.Hkv * p.tiles_sh);
-    s = std::max<int64_t>(1, std::min({s, ceil_div(shared, 4 * KT), (int64_t)kSplits}));
+    const int KT = p.wide ? wide_step(c.D) : narrow_step(c.D);
+    p.tiles_sh = (int)ceil_div(rows, (p.wide ? kWide : kNarrow) * 32);
+    const int64_t tiles = (int64_t)c.Hkv * p.tiles_sh;
+    if (p.wide) {
+      // One workgroup a CU: rounds of the card times the keys of an item, with what an item's start
+      // and end and one more slot to join cost in tiles.
+      int64_t best = 0;
+      for (int64_t x = 1; x <= std::min<int64_t>(kSplits, ceil_div(shared, 4 * KT)); ++x) {
+        const int64_t cost = ceil_div(tiles * x, kCUs) * (ceil_div(shared, x * KT) + 4) +
+                             x * rows * c.Hkv / (kCUs * 32);
+        if (best == 0 || cost < best) {
+          best = cost;
+          s = x;
+        }
+      }
+      if (best == 0) s = 1;
+    } else {
+      s = ceil_div(want, tiles);
+      s = std::max<int64_t>(1, std::min({s, ceil_div(shared, kLeast), (int64_t)kSplits}));
+    }
     s = std::max(s, ceil_div(shared, most));
     p.chunk_sh = (int)(ceil_div(ceil_div(shared, s), KT) * KT);
     p.s_sh = (int)ceil_div(shared, p.chunk_sh);
@@ -456,27 +708,38 @@ Plan plan_of(const xpress_cache& c, int N, int B, int Hq, int shared) {
 // Largest number of (row of the batch, slot) pairs of any N <= n and any shared: with A items
 // wanted for n requests, n * ceil(A / n) <= A + n; every bound grows with n.
 int64_t most_row_slots(const xpress_cache& c, int n, int B, int Hq) {
-  const int rows = waves_of(c.D) * 32, KT = step_of(c.D), G = Hq / c.Hkv;
+  const int G = Hq / c.Hkv;
   const int64_t cap = (int64_t)c.table_ld * c.page, ids = ceil_div(cap, most_keys(c));
-  const int64_t tiles = ceil_div((int64_t)B * G, rows);
-  const int64_t own = std::min({ceil_div(kItems, c.Hkv * tiles) + n, n * ceil_div(cap, 2 * KT),
-                                (int64_t)n * kSplits});
-  const int64_t sh = std::min({ceil_div((int64_t)kItems * rows, (int64_t)c.Hkv * B * G) + n,
-                               n * ceil_div(cap, 4 * KT), (int64_t)n * kSplits});
+  const int64_t tiles = ceil_div((int64_t)B * G, kNarrow * 32);
+  const int64_t fits = std::min<int64_t>(kSplits, ceil_div(cap, kLeast));
+  const int64_t own = std::min(ceil_div(kItems, c.Hkv * tiles) + n, n * fits);
+  // (a narrow call splits as far as kItems / 2 items, a wide one as far as kWideItems)
+  const int64_t sh = std::min(
+      ceil_div((int64_t)kWideItems * kWide * 32, (int64_t)c.Hkv * B * G) + n, n * fits);
   return std::max<int64_t>(own, n * ids) + std::max<int64_t>(sh, n * ids);
 }
 
 template <bool F16, int D>
-hipError_t launch_t(const Args& A, hipStream_t s) {
-  constexpr int NW = waves_of(D), KT = step_of(D);
-  const int64_t items = (int64_t)A.Hkv * A.tiles_sh * A.s_sh + (int64_t)A.Hkv * A.s_own * A.tiles_own * A.N;
-  hipLaunchKernelGGL((attend_kernel<F16, D, NW, KT>), dim3((unsigned)items), dim3(NW * 64), 0, s, A);
+hipError_t launch_t(Args A, bool wide, hipStream_t s) {
+  const int64_t own = (int64_t)A.Hkv * A.s_own * A.tiles_own * A.N;
+  int64_t shared = (int64_t)A.Hkv * A.tiles_sh * A.s_sh;
+  A.slots_sh = A.s_sh;
+  A.step_own = narrow_step(D);
+  if (wide) {
+    hipLaunchKernelGGL((attend_kernel<F16, D, kWide, wide_step(D)>), dim3((unsigned)shared),
+                       dim3(kWide * 64), 0, s, A);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+    shared = A.tiles_sh = A.s_sh = 0;  // done
+  }
+  hipLaunchKernelGGL((attend_kernel<F16, D, kNarrow, narrow_step(D)>),
+                     dim3((unsigned)(shared + own)), dim3(kNarrow * 64), 0, s, A);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || A.s_sh + A.s_own == 1) return e;
+  if (e != hipSuccess || A.slots_sh + A.s_own == 1) return e;
   const int64_t rows = (int64_t)A.N * A.B * A.Hq;
   const int per = 256 / (D / 4);
-  hipLaunchKernelGGL((merge_kernel<F16, D, KT>), dim3((unsigned)((rows + per - 1) / per)), dim3(256),
-                     0, s, A);
+  hipLaunchKernelGGL((merge_kernel<F16, D>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0,
+                     s, A);
   return hipGetLastError();
 }
 
@@ -487,7 +750,7 @@ size_t attention_scratch_bytes(const xpress_cache& c, int N, int B, int Hq) {
 }
 
 int64_t attention_items(const xpress_cache& c, int N, int B, int Hq, int shared) {
-  const Plan p = plan_of(c, N, B, Hq, shared);
+  const Plan p = plan_of(c, N, B, Hq, shared / kTile * kTile);
   return c.Hkv * ((int64_t)p.tiles_sh * p.s_sh + (int64_t)p.tiles_own * p.s_own * N);
 }
 
@@ -496,6 +759,7 @@ hipError_t launch_block_attention(const xpress_cache& c, int layer, const void* 
                                   int shared, void* out, int64_t out_ld, float* lse, void* ws,
                                   hipStream_t s) {
   const int64_t at = (int64_t)layer * c.n_pages * c.Hkv * c.page * c.D;
+  shared = shared / kTile * kTile;
   const Plan p = plan_of(c, N, B, Hq, shared);
   Args A;
   A.q = static_cast<const uint16_t*>(q);
@@ -528,9 +792,9 @@ hipError_t launch_block_attention(const xpress_cache& c, int layer, const void* 
   A.pml = reinterpret_cast<float2*>(A.po + (size_t)p.slots() * N * B * Hq * c.D);
   const bool f16 = c.dtype == XPRESS_F16;
   switch (c.D) {
-    case 64: return f16 ? launch_t<true, 64>(A, s) : launch_t<false, 64>(A, s);
-    case 128: return f16 ? launch_t<true, 128>(A, s) : launch_t<false, 128>(A, s);
-    default: return f16 ? launch_t<true, 256>(A, s) : launch_t<false, 256>(A, s);
+    case 64: return f16 ? launch_t<true, 64>(A, p.wide, s) : launch_t<false, 64>(A, p.wide, s);
+    case 128: return f16 ? launch_t<true, 128>(A, p.wide, s) : launch_t<false, 128>(A, p.wide, s);
+    default: return f16 ? launch_t<true, 256>(A, p.wide, s) : launch_t<false, 256>(A, p.wide, s);
   }
 }
 

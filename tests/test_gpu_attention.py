@@ -114,6 +114,14 @@ CASES = [
     dict(lengths=[1025], shared=0, B=16, Hkv=2, G=7, D=128, page=16),
     dict(lengths=[260] * 9, shared=256, B=2, Hkv=3, G=1, D=64, page=32),
     dict(lengths=[90, 91, 92, 93], shared=80, B=33, Hkv=1, G=9, D=64, page=16),  # 297 rows a request
+    # many query rows a head: the shared part in wide items, whole tiles, a part of one, rows that
+    # end inside the prefix, rows without tokens, a last item of few rows
+    dict(lengths=[420 + 3 * i for i in range(40)], shared=384, B=16, Hkv=1, G=1, D=64, page=32),
+    dict(lengths=[400, 0, 395, 17, 300, 399, 396, 401], shared=390, B=13, Hkv=2, G=6, D=128, page=16),
+    dict(lengths=[70] * 70, shared=64, B=2, Hkv=1, G=5, D=128, page=64),
+    dict(lengths=[1300, 1301], shared=1279, B=64, Hkv=1, G=4, D=128, page=128),
+    dict(lengths=[60] * 11, shared=43, B=16, Hkv=1, G=3, D=64, page=16),  # less than a tile
+    dict(lengths=[150, 160, 170, 180, 0], shared=130, B=30, Hkv=1, G=4, D=256, page=32),
 ]
 
 
