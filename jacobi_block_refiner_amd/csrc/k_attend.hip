@@ -43,15 +43,12 @@ struct Args {
   int tiles_sh, s_sh, chunk_sh, tiles_own, s_own;
   int slots_sh;  // slots of the shared part (items of this launch or of one before it)
   int step_own;  // own ranges are multiples of it
+  bool direct;   // own items are their rows' last and write the result
   uint16_t* out;
   float* lse;
   float* po;   // [slots, N*B, Hq, D]
   float2* pml; // [slots, N*B, Hq]: maximum (log2 units), sum
 };
-
-template <bool F16> __device__ __forceinline__ float value(short x) {
-  return F16 ? (float)__builtin_bit_cast(_Float16, x) : bf16_to_f32((uint16_t)x);
-}
 
 // Two weights rounded to the type (to nearest even) in one register: the matrix core takes them as
 // bf16 or fp16. Relative error half a step each, against the 32-bit sum of the unrounded weights.
@@ -204,87 +201,41 @@ template <bool F16, int D, int KT> struct Core {
     l = (sum[0] + sum[1]) + (sum[2] + sum[3]);
   }
 
-  // Adds the weights times the V tile at byte vb.
-  __device__ __forceinline__ void values(int vb) {
+  // V^T of 32 channels dt for the 16 keys kk of the tile at byte vb.
+  __device__ __forceinline__ s16x8 v_frag(int vb, int kk, int dt) const {
     const int i16 = lane & 15, vkey = 4 * h + (i16 >> 2);         // key of the transposing read
     const int vpiece = ((lane >> 4) & 1) * 2 + ((i16 >> 1) & 1);  // 16-byte piece of 32 channels
+    s16x4 part[2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      const int key = kk * 16 + 8 * x + vkey;
+      part[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
+          (__attribute__((address_space(3))) s16x4*)(lds + vb + key * D * 2 +
+                                                     (((dt * 4 + vpiece) ^ v_swizzle(key)) * 16) +
+                                                     (i16 & 1) * 8));
+    }
+    return __builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7);
+  }
+
+  // Adds the weights times the V tile at byte vb.
+  __device__ __forceinline__ void values(int vb) {
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk)
 #pragma unroll
-      for (int dt = 0; dt < DT; ++dt) {
-        s16x4 part[2];
-#pragma unroll
-        for (int x = 0; x < 2; ++x) {
-          const int key = kk * 16 + 8 * x + vkey;
-          part[x] = __builtin_amdgcn_ds_read_tr16_b64_v4i16(
-              (__attribute__((address_space(3))) s16x4*)(lds + vb + key * D * 2 +
-                                                         (((dt * 4 + vpiece) ^ v_swizzle(key)) * 16) +
-                                                         (i16 & 1) * 8));
-        }
-        o[dt] = mfma<F16>(__builtin_shufflevector(part[0], part[1], 0, 1, 2, 3, 4, 5, 6, 7), pf[kk],
-                          o[dt]);
-      }
-  }
-
-  // Whether the V tile holds a value that is not finite.
-  __device__ __forceinline__ bool wild(int vb) const {
-    constexpr uint32_t E = F16 ? 0x7c00u : 0x7f80u;
-    bool found = false;
-#pragma unroll 4
-    for (int x = lane; x < KT * CPR; x += 64) {
-      const uint4 u = *reinterpret_cast<const uint4*>(lds + vb + x * 16);
-      const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-#pragma unroll
-      for (int y = 0; y < 4; ++y) found |= (w[y] & E) == E || ((w[y] >> 16) & E) == E;
-    }
-    return __any(found);
-  }
-
-  // A tile some of whose keys some rows do not see. Values in masked places must not reach a row,
-  // and 0 * inf would: where such a tile holds a value that is not finite it goes key by key
-  // (slowly), each row taking the keys that it sees.
-  __device__ __forceinline__ void masked_tile(int kb, int vb, int t0, int vis) {
-    scores(kb);
-    mask(t0, vis);
-    rise();
-    if (!wild(vb)) {
-      weights();
-      values(vb);
-      return;
-    }
-    const float mc = -m * c;
-#pragma unroll 1
-    for (int key = 0; key < KT; ++key) {
-      float dot = 0.f;
-#pragma unroll
-      for (int d = 0; d < DS; ++d) {
-        const s16x8 k = *reinterpret_cast<const s16x8*>(lds + kb + key * D * 2 +
-                                                        (((2 * d + h) ^ k_swizzle(key)) * 16));
-        s16x8 q = qf[d];
-        asm volatile("" : "+v"(q));  // (or its conversions stay in registers all along)
-#pragma unroll
-        for (int j = 0; j < 8; ++j) dot = fmaf(value<F16>(k[j]), value<F16>(q[j]), dot);
-      }
-      const float2 dots = both_halves(dot);
-      const bool sees = t0 + key < vis;
-      const float p = sees ? __builtin_amdgcn_exp2f(fmaf(dots.x + dots.y, c, mc)) : 0.f;
-      l += h == 0 ? p : 0.f;
-#pragma unroll
-      for (int dt = 0; dt < DT; ++dt)
-#pragma unroll
-        for (int i = 0; i < 4; ++i) {
-          const int piece = dt * 4 + i;
-          const s16x4 x = *reinterpret_cast<const s16x4*>(
-              lds + vb + key * D * 2 + ((piece ^ v_swizzle(key)) * 16) + h * 8);
-#pragma unroll
-          for (int y = 0; y < 4; ++y) {
-            const float at = o[dt][4 * i + y];
-            o[dt][4 * i + y] = sees ? fmaf(p, value<F16>(x[y]), at) : at;
-          }
-        }
-    }
+      for (int dt = 0; dt < DT; ++dt) o[dt] = mfma<F16>(v_frag(vb, kk, dt), pf[kk], o[dt]);
   }
 };
+
+// The 16-bit values of u that are not finite set to 0; whether there were any.
+template <bool F16> __device__ __forceinline__ bool tame(uint32_t& u) {
+  constexpr uint32_t E = F16 ? 0x7c00u : 0x7f80u;
+  const bool lo = (u & E) == E, hi = ((u >> 16) & E) == E;
+  u &= (lo ? 0u : 0xffffu) | (hi ? 0u : 0xffff0000u);
+  return lo || hi;
+}
+template <bool F16> __device__ __forceinline__ float value(uint32_t x) {
+  return F16 ? (float)__builtin_bit_cast(_Float16, (uint16_t)x) : bf16_to_f32((uint16_t)x);
+}
 
 // Where an item's K and V come from: a range of one row's tokens, its table entries in LDS. A lane
 // copies 16 bytes of one key's line at a time; keys past the range copy the last one (their weights
@@ -403,7 +354,7 @@ template <int N> __device__ __forceinline__ void feed() {
 // weights, and after each such half they meet and change roles. A tile needs about as many cycles of
 // the matrix core as of the vector unit; with both waves in step, each unit waited for the other.
 template <bool F16, int D, int NW, int KT>
-__global__ __launch_bounds__(NW * 64, NW == kWide || D == 128 ? 2 : D == 256 ? 1 : 3) void attend_kernel(
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : NW == kWide ? 2 : 3) void attend_kernel(
     Args A) {
   using C = Core<F16, D, KT>;
   using S = Source<D, KT, NW>;
@@ -411,6 +362,7 @@ __global__ __launch_bounds__(NW * 64, NW == kWide || D == 128 ? 2 : D == 256 ? 1
   constexpr int NS = WIDE ? 4 : 3, STAGE = 2 * C::SIDE, CW = S::CW;
   __shared__ uint4 s_tile[NS * STAGE / 16];
   __shared__ int s_ids[kIds];
+  __shared__ int s_wild[2];  // first and last masked tile with V values that are not finite
 
   const int lane = threadIdx.x & 63, h = lane >> 5, col = lane & 31;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -444,7 +396,7 @@ __global__ __launch_bounds__(NW * 64, NW == kWide || D == 128 ? 2 : D == 256 ? 1
     kend = r.y;
     nrows = A.B * A.G;
   }
-  const bool direct = A.slots_sh + A.s_own == 1;
+  const bool direct = !WIDE && A.direct;
   if (kend <= kbeg && !direct) return;
 
   // this lane's query; `blind`: it sees nothing here (what it computes is dropped)
@@ -462,8 +414,16 @@ __global__ __launch_bounds__(NW * 64, NW == kWide || D == 128 ? 2 : D == 256 ? 1
     const int first = kbeg >> A.shift, n = kend > kbeg ? ((kend - 1) >> A.shift) - first + 1 : 0;
     const int32_t* t = A.table + (int64_t)max(list_row(A, req), 0) * A.ld + first;
     for (int j = threadIdx.x; j < n; j += NW * 64) s_ids[j] = clamp_page(t[j], A.n_pages);
+    if (threadIdx.x == 0) {
+      s_wild[0] = INT_MAX;
+      s_wild[1] = -1;
+    }
   }
   __syncthreads();
+  // q has to be in before the first copies: the compiler waits for it at its first use by a count of
+  // loads in flight, in which the copies, which it does not know, would take the loads' places
+#pragma unroll
+  for (int x = 0; x < C::DS; ++x) asm volatile("" : "+v"(w.qf[x]));
   const int nt = (kend - kbeg + KT - 1) / KT;
   S src;
   if (nt > 0)
@@ -522,14 +482,12 @@ __global__ __launch_bounds__(NW * 64, NW == kWide || D == 128 ? 2 : D == 256 ? 1
     meet<0>();
   } else {
     const int vis = blind ? INT_MAX : sight;
-    int vmin = vis, vmax = blind ? 0 : sight;
-#pragma unroll
-    for (int x = 16; x; x >>= 1) {
-      vmin = min(vmin, __shfl_xor(vmin, x));
-      vmax = max(vmax, __shfl_xor(vmax, x));
-    }
-    vmax = __builtin_amdgcn_readfirstlane(vmax);
-    vmin = __builtin_amdgcn_readfirstlane(vmin);
+    // no rows, no products: only copies and meetings
+    const bool idle = __ballot(!blind) == 0;
+    // tiles that every row sees whole: all of a shared item's, else up to the reach of the request's
+    // first query
+    const int len0 = is_shared ? 0 : list_len(A, req);
+    const int whole = is_shared ? nt : max(min(in_sight(len0, A.B, 0), kend) - kbeg, 0) / KT;
     int t = 0, at = 0, to = 0;
     auto copy_both = [&](int next) {
       src.turn(next);
@@ -550,29 +508,91 @@ __global__ __launch_bounds__(NW * 64, NW == kWide || D == 128 ? 2 : D == 256 ? 1
     };
     if (nt > 0) copy_both(1);
     if (nt > 1) copy_both(2);
-    // tiles that every row of the wave sees whole, then those that some see in part
-    const int whole = vmax == 0 ? 0 : (vmin - kbeg) / KT;
-    while (t < nt && t < whole) {
+    while (t < min(nt, whole)) {
       enter();
-      w.scores(at);
-      w.rise();
-      w.weights();
-      w.values(at + C::SIDE);
+      if (!idle) {
+        w.scores(at);
+        w.rise();
+        w.weights();
+        w.values(at + C::SIDE);
+      }
       leave();
     }
+    // The others. Values in masked places must not reach a row, and 0 * inf would: V values that are
+    // not finite are set to 0 in LDS here, and added to the rows that see them at the end.
     while (t < nt) {
       enter();
-      const int t0 = kbeg + t * KT;
-      if (t0 < vmax) w.masked_tile(at, at + C::SIDE, t0, vis);
+      bool wild = false;
+      for (int x = threadIdx.x; x < KT * C::CPR; x += NW * 64) {
+        uint4& v = s_tile[(at + C::SIDE) / 16 + x];
+        uint4 u = v;
+        if (tame<F16>(u.x) | tame<F16>(u.y) | tame<F16>(u.z) | tame<F16>(u.w)) {
+          v = u;
+          wild = true;
+        }
+      }
+      if (wild) {
+        atomicMin(&s_wild[0], t);
+        atomicMax(&s_wild[1], t);
+      }
+      meet_reads();
+      if (!idle) {
+        w.scores(at);
+        w.mask(kbeg + t * KT, vis);
+        w.rise();
+        w.weights();
+        w.values(at + C::SIDE);
+      }
       leave();
+    }
+    if (s_wild[1] >= 0 && !idle) {
+#pragma unroll 1
+      for (int pos = kbeg + s_wild[0] * KT; pos < min(kbeg + (s_wild[1] + 1) * KT, kend); ++pos) {
+        const int64_t from = line_offset(s_ids[(pos >> A.shift) - (kbeg >> A.shift)], hk,
+                                         pos & ((1 << A.shift) - 1), A.Hkv, A.shift, D);
+#pragma unroll
+        for (int i = 0; i < C::DT * 4; ++i) {
+          const uint2 v = *reinterpret_cast<const uint2*>(A.v + from + 4 * h + 8 * i);
+          const uint32_t x[4] = {v.x & 0xffff, v.x >> 16, v.y & 0xffff, v.y >> 16};
+#pragma unroll
+          for (int j = 0; j < 4; ++j) {
+            uint32_t tamed = x[j];
+            // (a weight is never 0 in exact arithmetic: the value itself reaches the sum)
+            w.o[i / 4][i % 4 * 4 + j] += tame<F16>(tamed) && pos < vis ? value<F16>(x[j]) : 0.f;
+          }
+        }
+      }
     }
   }
 
   const float2 ls = both_halves(w.l);
-  const float l = blind ? 0.f : ls.x + ls.y;
+  float l = blind ? 0.f : ls.x + ls.y;
   if (!valid) return;
-  const int64_t row = (int64_t)token * A.Hq + hq;
+  const int64_t row = (int64_t)token * A.Hq + hq, rows = (int64_t)A.N * A.B * A.Hq;
   if (direct) {
+    // the shared items' parts of this row, from the launch before this one
+    float m = l == 0.f ? -INFINITY : w.m * A.c;
+    for (int s = 0; s < A.slots_sh; ++s) {
+      const int64_t at = s * rows + row;
+      const float2 ml = A.pml[at];
+      float4 x[C::DT * 4];
+#pragma unroll
+      for (int i = 0; i < C::DT * 4; ++i)
+        x[i] = *reinterpret_cast<const float4*>(A.po + at * D + 4 * h + 8 * i);
+      if (ml.y == 0.f) continue;
+      const float mn = fmaxf(m, ml.x);
+      const float a = __builtin_amdgcn_exp2f(m - mn), b = __builtin_amdgcn_exp2f(ml.x - mn);
+      m = mn;
+      l = l * a + ml.y * b;
+#pragma unroll
+      for (int i = 0; i < C::DT * 4; ++i) {
+        f32x16& o = w.o[i / 4];
+        o[i % 4 * 4] = o[i % 4 * 4] * a + x[i].x * b;
+        o[i % 4 * 4 + 1] = o[i % 4 * 4 + 1] * a + x[i].y * b;
+        o[i % 4 * 4 + 2] = o[i % 4 * 4 + 2] * a + x[i].z * b;
+        o[i % 4 * 4 + 3] = o[i % 4 * 4 + 3] * a + x[i].w * b;
+      }
+    }
     const float inv = 1.f / l;
     uint16_t* op = A.out + token * A.out_ld + (int64_t)hq * D + 4 * h;
 #pragma unroll
@@ -585,10 +605,10 @@ __global__ __launch_bounds__(NW * 64, NW == kWide || D == 128 ? 2 : D == 256 ? 1
         *reinterpret_cast<uint2*>(op + dt * 32 + 8 * i) = l == 0.f ? make_uint2(0, 0) : u;
       }
     if (A.lse && h == 0)
-      A.lse[row] = l == 0.f ? -INFINITY : (w.m * A.c + log2f(l)) * 0.69314718056f;
+      A.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
     return;
   }
-  const int64_t at = (int64_t)slot * A.N * A.B * A.Hq + row;
+  const int64_t at = slot * rows + row;
   float* op = A.po + at * D + 4 * h;
 #pragma unroll
   for (int dt = 0; dt < C::DT; ++dt)
@@ -652,11 +672,11 @@ struct Plan {
 
 constexpr int kTile = 64;  // the shared part is a multiple of it
 constexpr int narrow_step(int D) { return D == 64 ? 64 : 32; }  // keys of a tile
-constexpr int wide_step(int D) { return D == 256 ? 32 : 64; }
+constexpr int kWideStep = 64;
 constexpr int kCUs = 256;
-constexpr int kWideRows = 512;  // query rows a head from which the shared part goes to wide items
+constexpr int kWideRows = 2048;  // query rows a head from which the shared part goes to wide items
 constexpr int kWideItems = 2048;
-constexpr int kItems = 512;  // narrow items wanted where the rows alone give fewer
+constexpr int kItems = 1024;  // narrow items wanted where the rows alone give fewer
 constexpr int kLeast = 128;  // keys of a split at least
 constexpr int kSplits = 64;  // splits of one row's keys at most (more where ids do not fit in LDS)
 
@@ -670,15 +690,15 @@ Plan plan_of(const xpress_cache& c, int N, int B, int Hq, int shared) {
   const int64_t cap = (int64_t)c.table_ld * c.page, most = most_keys(c), own = cap - shared;
   const int64_t rows = (int64_t)N * B * G;
   Plan p{};
-  p.wide = shared > 0 && rows >= kWideRows;
+  p.wide = shared > 0 && c.D == 128 && rows >= kWideRows;
   p.tiles_own = (int)ceil_div((int64_t)B * G, kNarrow * 32);
-  const int want = shared > 0 && !p.wide ? kItems / 2 : kItems;
+  const int want = p.wide ? kCUs : shared > 0 ? kItems / 2 : kItems;
   int64_t s = ceil_div(want, (int64_t)N * c.Hkv * p.tiles_own);
-  s = std::max<int64_t>(1, std::min({s, ceil_div(own, kLeast), (int64_t)kSplits}));
+  s = std::max<int64_t>(1, std::min({s, ceil_div(own, p.wide ? 4 * kLeast : kLeast), (int64_t)kSplits}));
   // (a request that does not see the whole shared part has less than shared + B keys, all its own)
   p.s_own = (int)std::max(s, ceil_div(std::max(own, std::min<int64_t>(cap, (int64_t)shared + B)), most));
   if (shared > 0) {
-    const int KT = p.wide ? wide_step(c.D) : narrow_step(c.D);
+    const int KT = p.wide ? kWideStep : narrow_step(c.D);
     p.tiles_sh = (int)ceil_div(rows, (p.wide ? kWide : kNarrow) * 32);
     const int64_t tiles = (int64_t)c.Hkv * p.tiles_sh;
     if (p.wide) {
@@ -725,8 +745,9 @@ hipError_t launch_t(Args A, bool wide, hipStream_t s) {
   int64_t shared = (int64_t)A.Hkv * A.tiles_sh * A.s_sh;
   A.slots_sh = A.s_sh;
   A.step_own = narrow_step(D);
-  if (wide) {
-    hipLaunchKernelGGL((attend_kernel<F16, D, kWide, wide_step(D)>), dim3((unsigned)shared),
+  A.direct = A.s_own == 1 && (wide || A.s_sh == 0);
+  if constexpr (D == 128) if (wide) {
+    hipLaunchKernelGGL((attend_kernel<F16, D, kWide, kWideStep>), dim3((unsigned)shared),
                        dim3(kWide * 64), 0, s, A);
     const hipError_t e = hipGetLastError();
     if (e != hipSuccess) return e;
@@ -735,7 +756,7 @@ hipError_t launch_t(Args A, bool wide, hipStream_t s) {
   hipLaunchKernelGGL((attend_kernel<F16, D, kNarrow, narrow_step(D)>),
                      dim3((unsigned)(shared + own)), dim3(kNarrow * 64), 0, s, A);
   hipError_t e = hipGetLastError();
-  if (e != hipSuccess || A.slots_sh + A.s_own == 1) return e;
+  if (e != hipSuccess || A.direct) return e;
   const int64_t rows = (int64_t)A.N * A.B * A.Hq;
   const int per = 256 / (D / 4);
   hipLaunchKernelGGL((merge_kernel<F16, D>), dim3((unsigned)((rows + per - 1) / per)), dim3(256), 0,
