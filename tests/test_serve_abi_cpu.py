@@ -222,6 +222,61 @@ def test_index_arithmetic_on_the_host(tmp_path):
     assert subprocess.run([str(exe)]).returncode == 0
 
 
+PLAN = r"""
+#include "attend_plan.hpp"
+#include <cstdio>
+#include <initializer_list>
+using namespace xpress;
+int main() {
+  xpress_cache c = {};
+  for (int D : {64, 128, 256}) for (int page : {16, 256}) for (int Hkv : {1, 2, 8, 32})
+  for (int64_t cap : {16LL, 100LL, 700LL, 5000LL, 20000LL, 70000LL, 1LL << 20}) {
+    c.D = D, c.page = page, c.Hkv = Hkv, c.table_ld = (cap + page - 1) / page;
+    cap = (int64_t)c.table_ld * page;
+    for (int G : {1, 5, 16}) for (int B : {1, 3, 16, 64}) {
+      int64_t last = 0;
+      for (int N : {1, 2, 5, 31, 64, 257, 1000, 4096}) {
+        const int64_t most = most_row_slots(c, N, B, Hkv * G);
+        if (most < last) return 1;  // a workspace for more requests serves fewer
+        last = most;
+        for (int64_t sh : {0LL, 64LL, 640LL, 4096LL, 19968LL, 65536LL, 1LL << 20}) {
+          if (sh > cap) continue;
+          const AttendPlan p = plan_of(c, N, B, Hkv * G, (int)(sh / kTile * kTile));
+          if ((int64_t)p.slots() * N > most) {
+            printf("D %d page %d Hkv %d cap %lld G %d B %d N %d shared %lld: %d slots, %lld rows\n", D,
+                   page, Hkv, (long long)cap, G, B, N, (long long)sh, p.slots(), (long long)most);
+            return 2;
+          }
+          // every key of the shared part in one split, every row in one tile, ids that fit
+          if (sh >= kTile && ((int64_t)p.s_sh * p.chunk_sh < sh / kTile * kTile || p.chunk_sh % 32 ||
+                              p.chunk_sh / page + 2 > kIds)) return 3;
+          if (sh >= kTile && (int64_t)p.tiles_sh * (p.wide ? kWide : kNarrow) * 32 < (int64_t)N * B * G)
+            return 4;
+          if ((int64_t)p.tiles_own * kNarrow * 32 < (int64_t)B * G || p.s_own < 1) return 5;
+          const int64_t own = std::max(cap - sh / kTile * kTile, std::min<int64_t>(cap, sh / kTile * kTile + B));
+          const int64_t chunk = ((own + p.s_own - 1) / p.s_own + 63) / 64 * 64;
+          if (chunk / page + 2 > kIds) return 6;
+        }
+      }
+    }
+  }
+  return 0;
+}
+"""
+
+
+def test_the_workspace_covers_every_split(tmp_path):
+    """The partial results of every plan fit in the workspace that is asked for, also when it was
+    asked for with more requests, and an item's page ids fit where the kernel keeps them."""
+    src = tmp_path / "plan.cpp"
+    src.write_text(PLAN)
+    exe = tmp_path / "plan"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover",
+                    f"-I{build.CSRC}", f"-I{build.INCLUDE}", str(src), "-o", str(exe)], check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert got.returncode == 0, (got.returncode, got.stdout)
+
+
 def test_oracles_on_cases_with_known_answers():
     """The oracles themselves: one token's attention is its value; a causal block; a fork that is
     extended; verification by hand."""
