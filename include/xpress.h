@@ -310,7 +310,7 @@ xpress_status xpress_graph_destroy(void* graph);
  * every layer). Entries of a row past its last page are -1. ref[p] is the number of rows that hold
  * page p (0: the page is free). The caller owns every buffer and starts with ref = 0, len = 0 and
  * table = -1; the calls below keep them so.
- * Limits: n_layers >= 1; 1 <= n_pages <= 2^24; page in {16, 32, 64, 128, 256}; 1 <= Hkv <= 256; D
+ * Limits: 1 <= n_layers <= 2^16; 1 <= n_pages <= 2^24; page in {16, 32, 64, 128, 256}; 1 <= Hkv <= 256; D
  * in {64, 128, 256}; 1 <= rows <= 2^20; 1 <= table_ld <= 2^20; dtype XPRESS_BF16 or XPRESS_F16; k
  * and v 16-byte aligned, table, len and ref 4-byte aligned.
  * Lists of rows (`seq`, `src`, `dst`) are int32 on the device. seq NULL means rows 0..N-1. A row

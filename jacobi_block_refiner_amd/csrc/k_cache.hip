@@ -1,6 +1,11 @@
 // Pages of the K/V cache (gfx950): fork, extension with copy on write, append, freeing and
-// compaction. The metadata (tables, lengths, counts) is integer work of a few KB; the copies are
-// plain 16-byte streams.
+// compaction. The metadata (tables, lengths, counts) is integer work of a few KB, so its kernels take
+// the time of a launch and of the loads that wait for one another (row -> length -> table entry ->
+// holders, close to 1 us each): what does not depend on such a load is asked for before it. The
+// copies are plain 16-byte streams. 32 rows of about 8600 tokens, 6 of them forks, in pages of 64
+// tokens of 4 layers of 8 heads of 128: fork 3.9 us, extension 6.0 and its copies (a dozen pages of 1
+// MiB at most) 6.4, append of 16 tokens 3.2 a layer, trim 2.3. A launch takes 3 to 4 us on the host,
+// so a turn that is not captured into a graph is bound by its launches.
 #include "serve.hpp"
 #include "cache_index.hpp"
 
@@ -11,6 +16,7 @@ namespace xpress {
 namespace {
 
 constexpr int kPlan = 1024;  // threads of the single workgroup that plans an allocation
+constexpr int kScan = 4;     // counts of a thread in a step of a walk over the pool
 
 int shift_of(int page) { return __builtin_ctz((unsigned)page); }
 
@@ -53,21 +59,57 @@ __device__ int block_scan(int v, int* total) {
   return before + x - v;
 }
 
+// Sum of v over the waves before this one (v is the same in a wave's lanes); *total gets the sum.
+__device__ __forceinline__ int waves_before(int v, int* total) {
+  __shared__ int s_part[kPlan / 64];
+  const int lane = threadIdx.x & 63, w = threadIdx.x >> 6;
+  __syncthreads();  // the previous call's s_part has been read
+  if (lane == 0) s_part[w] = v;
+  __syncthreads();
+  int before = 0, all = 0;
+#pragma unroll
+  for (int i = 0; i < kPlan / 64; ++i) {
+    const int p = s_part[i];
+    before += i < w ? p : 0;
+    all += p;
+  }
+  *total = all;
+  return before;
+}
+
+// A walk over the pool's counts takes kPlan * kScan pages a step; a wave has kScan * 64 of them in a
+// row, each lane every 64th, so that a ballot gives the ranks in id order.
+__device__ __forceinline__ int walk_at(int p0, int i) {
+  return p0 + (threadIdx.x >> 6) * kScan * 64 + i * 64 + (threadIdx.x & 63);
+}
+__device__ __forceinline__ void counts_at(const Pages& P, int p0, int* ref) {
+#pragma unroll
+  for (int i = 0; i < kScan; ++i) {
+    const int p = walk_at(p0, i);
+    ref[i] = p < P.n_pages ? P.ref[p] : -1;
+  }
+}
+__device__ __forceinline__ int lanes_before(uint64_t m) {
+  return __builtin_amdgcn_mbcnt_hi((uint32_t)(m >> 32), __builtin_amdgcn_mbcnt_lo((uint32_t)m, 0));
+}
+
+// One workgroup a row; a thread an entry. The lengths are needed for the counts alone, so the entries
+// are read beside them.
 __global__ __launch_bounds__(256) void fork_kernel(Pages P, const int32_t* src, const int32_t* dst) {
   const int from = row_of(src, blockIdx.x, P.rows), to = row_of(dst, blockIdx.x, P.rows);
   if (from < 0 || to < 0 || from == to) return;
   const int old_len = clamp_len(P.len[to], P.ld, P.shift);
   const int new_len = clamp_len(P.len[from], P.ld, P.shift);
   const int old_pages = pages_of(old_len, P.shift), new_pages = pages_of(new_len, P.shift);
-  __syncthreads();  // every thread has read both lengths
   const int32_t* a = P.table + (int64_t)from * P.ld;
   int32_t* b = P.table + (int64_t)to * P.ld;
   for (int j = threadIdx.x; j < P.ld; j += blockDim.x) {
-    const int old = b[j], id = a[j];
+    const int old = b[j], id = a[j];  // (the first of these loads do not wait for the lengths)
     if (j < old_pages && page_ok(old, P.n_pages)) atomicSub(&P.ref[old], 1);
     if (j < new_pages && page_ok(id, P.n_pages)) atomicAdd(&P.ref[id], 1);
     b[j] = id;
   }
+  __syncthreads();  // every thread has read the length
   if (threadIdx.x == 0) P.len[to] = new_len;
 }
 
@@ -130,6 +172,8 @@ __host__ __device__ inline ExtendScratch extend_scratch(void* ws, int N) {
                        p + 4 + 4 * n, p + 4 + 5 * n};
 }
 
+// The copies are a launch of their own: they need the plan of all rows, and a flag to wait for it
+// would need a workspace that the caller has cleared.
 // One workgroup: the rows' needs in list order (prefix sums), the first `total` free pages in id
 // order, then the tables. The whole plan is made before anything is written.
 __global__ __launch_bounds__(kPlan) void extend_kernel(Pages P, const int32_t* seq, int N,
@@ -137,6 +181,8 @@ __global__ __launch_bounds__(kPlan) void extend_kernel(Pages P, const int32_t* s
                                                        int32_t* lacking, void* ws) {
   const ExtendScratch S = extend_scratch(ws, N);
   const int t = threadIdx.x;
+  int ref[kScan];
+  counts_at(P, 0, ref);  // in flight beside the rows' loads
   __shared__ int s_over;
   if (t == 0) s_over = 0;
   __syncthreads();
@@ -159,12 +205,22 @@ __global__ __launch_bounds__(kPlan) void extend_kernel(Pages P, const int32_t* s
   int found = 0;
   const int want = (int)min(total, (int64_t)P.n_pages);
   if (!s_over)
-    for (int p0 = 0; p0 < P.n_pages && found < want; p0 += kPlan) {
-      const int p = p0 + t;
-      int all;
-      const bool is_free = p < P.n_pages && P.ref[p] == 0;
-      const int k = found + block_scan(is_free, &all);
-      if (is_free && k < want) S.free_ids[k] = p;
+    for (int p0 = 0; p0 < P.n_pages && found < want; p0 += kPlan * kScan) {
+      if (p0) counts_at(P, p0, ref);
+      uint64_t is_free[kScan];
+      int mine = 0, all;
+#pragma unroll
+      for (int i = 0; i < kScan; ++i) {
+        is_free[i] = __ballot(ref[i] == 0);
+        mine += __popcll(is_free[i]);
+      }
+      int k = found + waves_before(mine, &all);
+#pragma unroll
+      for (int i = 0; i < kScan; ++i) {
+        const int at = k + lanes_before(is_free[i]);
+        if (ref[i] == 0 && at < want) S.free_ids[at] = walk_at(p0, i);
+        k += __popcll(is_free[i]);
+      }
       found += all;
     }
   const bool no = s_over || found < total;
@@ -195,45 +251,62 @@ __global__ __launch_bounds__(kPlan) void extend_kernel(Pages P, const int32_t* s
   }
 }
 
+typedef uint32_t u32x4 __attribute__((ext_vector_type(4)));
+
+constexpr int kCopy = 8;  // loads of a thread in flight: 32 KB a workgroup (with one, a
+                           // dozen pages of 1 MiB took 9.2 us instead of 6.4, 512 of them 221
+                           // instead of 213)
+
 // Copies pages from[i] -> to[i], i < *count, in every layer of K and V. One workgroup per (page,
-// layer and side) at a time; `chunks` 16-byte pieces per page.
+// layer and side) at a time; `chunks` 16-byte pieces per page. 537 MB read and as much written: 213 us,
+// 5.0 TB/s, the rate of a copy of 4 GiB.
 __global__ __launch_bounds__(256) void copy_pages_kernel(const int32_t* __restrict__ count,
                                                          const int32_t* __restrict__ from,
                                                          const int32_t* __restrict__ to,
-                                                         uint4* k, uint4* v, int n_layers,
+                                                         u32x4* k, u32x4* v, int n_layers,
                                                          int64_t n_pages, int64_t chunks) {
   const int64_t items = (int64_t)*count * n_layers * 2;
   for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
     const int i = (int)(it / (n_layers * 2)), side = (int)(it % (n_layers * 2));
     const int a = from[i];
     if (a < 0) continue;
-    uint4* pool = (side & 1 ? v : k) + (int64_t)(side >> 1) * n_pages * chunks;
-    const uint4* x = pool + a * chunks;
-    uint4* y = pool + to[i] * chunks;
-    for (int64_t j = threadIdx.x; j < chunks; j += blockDim.x) y[j] = x[j];
+    u32x4* pool = (side & 1 ? v : k) + (int64_t)(side >> 1) * n_pages * chunks;
+    const u32x4* x = pool + a * chunks;
+    u32x4* y = pool + to[i] * chunks;
+    int j = threadIdx.x;
+    for (; j + 256 * (kCopy - 1) < chunks; j += 256 * kCopy) {
+      u32x4 c[kCopy];
+#pragma unroll
+      for (int u = 0; u < kCopy; ++u) c[u] = x[j + u * 256];
+#pragma unroll
+      for (int u = 0; u < kCopy; ++u) y[j + u * 256] = c[u];
+    }
+    for (; j < chunks; j += 256) y[j] = x[j];
   }
 }
 
+// A thread a 16-byte piece of a token. The new values are read beside the row's length and table.
 __global__ __launch_bounds__(256) void append_kernel(Pages P, uint16_t* k, uint16_t* v,
                                                      const uint16_t* __restrict__ k_new,
                                                      const uint16_t* __restrict__ v_new,
                                                      int64_t ld_new, const int32_t* seq, int N,
                                                      int B, int Hkv, int D) {
-  const int per = Hkv * D / 8;  // 16-byte pieces of a token
-  const int64_t i = (int64_t)blockIdx.x * blockDim.x + threadIdx.x;
-  if (i >= (int64_t)N * B * per) return;
-  const int64_t token = i / per;
-  const int piece = (int)(i % per), e = (int)(token / B), b = (int)(token % B);
+  const unsigned per = Hkv * D / 8;  // 16-byte pieces of a token
+  const unsigned i = blockIdx.x * 256u + threadIdx.x;  // (below 2^31: N*B*Hkv is below 2^26)
+  if (i >= (unsigned)N * B * per) return;
+  const unsigned token = i / per, piece = i % per;
+  const int e = token / (unsigned)B, b = token % (unsigned)B;
+  const uint4 x = *reinterpret_cast<const uint4*>((blockIdx.y ? v_new : k_new) +
+                                                  (int64_t)token * ld_new + piece * 8);
   const int r = row_of(seq, e, P.rows);
   if (r < 0) return;
   const int pos = in_sight(clamp_len(P.len[r], P.ld, P.shift), B, b) - 1;
   if (pos < 0) return;
   const int id = P.table[(int64_t)r * P.ld + (pos >> P.shift)];
   if (!page_ok(id, P.n_pages)) return;
-  const int h = piece * 8 / D, d = piece * 8 % D;
+  const int h = piece * 8 / (unsigned)D, d = piece * 8 % (unsigned)D;
   const int64_t to = line_offset(id, h, pos & ((1 << P.shift) - 1), Hkv, P.shift, D) + d;
-  const uint16_t* x = (blockIdx.y ? v_new : k_new) + token * ld_new + piece * 8;
-  *reinterpret_cast<uint4*>((blockIdx.y ? v : k) + to) = *reinterpret_cast<const uint4*>(x);
+  *reinterpret_cast<uint4*>((blockIdx.y ? v : k) + to) = x;
 }
 
 // Scratch of a compaction: the number of moves, the moves, and where each page goes.
@@ -245,27 +318,46 @@ __host__ __device__ inline CompactScratch compact_scratch(void* ws, int n_pages)
   return CompactScratch{p, p + 4, p + 4 + n_pages, p + 4 + 2 * (int64_t)n_pages};
 }
 
+// One workgroup, two walks over the counts: how many pages live (L), then the live ones from L on and
+// the free ones before it, which pair up in id order. 4.8 us for 2048 pages.
 __global__ __launch_bounds__(kPlan) void compact_plan_kernel(Pages P, int32_t* live, void* ws) {
   const CompactScratch S = compact_scratch(ws, P.n_pages);
   const int t = threadIdx.x;
-  int L = 0;
-  for (int p0 = 0; p0 < P.n_pages; p0 += kPlan) {
-    int all;
-    block_scan(p0 + t < P.n_pages && P.ref[p0 + t] > 0, &all);
+  int ref[kScan];
+  int L = 0, all;
+  for (int p0 = 0; p0 < P.n_pages; p0 += kPlan * kScan) {
+    counts_at(P, p0, ref);
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) mine += __popcll(__ballot(ref[i] > 0));
+    waves_before(mine, &all);
     L += all;
   }
   int nfrom = 0, nto = 0;
-  for (int p0 = 0; p0 < P.n_pages; p0 += kPlan) {
-    const int p = p0 + t;
-    const bool alive = p < P.n_pages && P.ref[p] > 0;
-    const bool out = alive && p >= L, in = p < P.n_pages && !alive && p < L;
-    int all;
-    const int a = nfrom + block_scan(out, &all);
-    nfrom += all;
-    const int b = nto + block_scan(in, &all);
-    nto += all;
-    if (out) S.from[a] = p;
-    if (in) S.to[b] = p;
+  for (int p0 = 0; p0 < P.n_pages; p0 += kPlan * kScan) {
+    if (P.n_pages > kPlan * kScan) counts_at(P, p0, ref);
+    // live pages from L on and free ones before it, both counts in one word (4096 a step at most)
+    uint64_t out[kScan], in[kScan];
+    int mine = 0;
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) {
+      const int p = walk_at(p0, i);
+      out[i] = __ballot(ref[i] > 0 && p >= L);
+      in[i] = __ballot(ref[i] == 0 && p < L);
+      mine += __popcll(out[i]) + (__popcll(in[i]) << 16);
+    }
+    const int before = waves_before(mine, &all);
+    int a = nfrom + (before & 0xffff), b = nto + (before >> 16);
+#pragma unroll
+    for (int i = 0; i < kScan; ++i) {
+      const int p = walk_at(p0, i);
+      if (ref[i] > 0 && p >= L) S.from[a + lanes_before(out[i])] = p;
+      if (ref[i] == 0 && p < L) S.to[b + lanes_before(in[i])] = p;
+      a += __popcll(out[i]);
+      b += __popcll(in[i]);
+    }
+    nfrom += all & 0xffff;
+    nto += all >> 16;
   }
   __syncthreads();
   for (int i = t; i < nfrom; i += kPlan) {
@@ -297,7 +389,7 @@ hipError_t launch_copy(const xpress_cache& c, const int32_t* count, const int32_
   const int64_t chunks = (int64_t)c.Hkv * c.page * c.D * 2 / 16;
   const int64_t items = most * c.n_layers * 2;
   hipLaunchKernelGGL(copy_pages_kernel, dim3((unsigned)(items < 2048 ? items : 2048)), dim3(256),
-                     0, s, count, from, to, static_cast<uint4*>(c.k), static_cast<uint4*>(c.v),
+                     0, s, count, from, to, static_cast<u32x4*>(c.k), static_cast<u32x4*>(c.v),
                      c.n_layers, (int64_t)c.n_pages, chunks);
   return hipGetLastError();
 }

@@ -25,7 +25,8 @@ hipStream_t hip_stream(xpress_stream s) { return reinterpret_cast<hipStream_t>(s
 // Sizes of a cache; with `pools` its K and V pointers, with `tables` its metadata pointers.
 xpress_status check_cache(const xpress_cache* c, bool pools, bool tables) {
   if (c == nullptr) return fail(XPRESS_ERR_ARG, "cache struct is NULL");
-  if (c->n_layers < 1) return fail(XPRESS_ERR_ARG, "n_layers=%d < 1", c->n_layers);
+  if (c->n_layers < 1 || c->n_layers > 1 << 16)
+    return fail(XPRESS_ERR_ARG, "n_layers=%d outside [1, 2^16]", c->n_layers);
   if (c->n_pages < 1 || c->n_pages > 1 << 24)
     return fail(XPRESS_ERR_ARG, "n_pages=%d outside [1, 2^24]", c->n_pages);
   if (c->page != 16 && c->page != 32 && c->page != 64 && c->page != 128 && c->page != 256)

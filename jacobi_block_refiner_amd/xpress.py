@@ -426,10 +426,11 @@ def _tokens(t, n: int, width: int, dtype, name: str) -> int:
     """A [n, width] view with unit column stride; its row stride in elements."""
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA {dtype} tensor")
-    if t.dim() != 2 or t.shape[0] < n or t.shape[1] != width or (width > 1 and t.stride(1) != 1):
-        raise ValueError(f"{name} is {tuple(t.shape)}; the call needs [{n}, {width}] rows with unit "
+    shape = t.shape
+    if len(shape) != 2 or shape[0] < n or shape[1] != width or (width > 1 and t.stride(1) != 1):
+        raise ValueError(f"{name} is {tuple(shape)}; the call needs [{n}, {width}] rows with unit "
                          "column stride")
-    return t.stride(0) if t.shape[0] > 1 else max(t.stride(0), width)
+    return t.stride(0) if shape[0] > 1 else max(t.stride(0), width)
 
 
 def _ws(ws):
@@ -469,6 +470,7 @@ class Cache:
                               self.k.data_ptr(), self.v.data_ptr(), self.table.data_ptr(),
                               self.length.data_ptr(), self.ref.data_ptr())
         self._ref = ctypes.byref(self._struct)
+        self._dtype, self._width, self._D = self.k.dtype, Hkv * D, D
 
     @classmethod
     def empty(cls, n_layers: int, n_pages: int, Hkv: int, page: int, D: int, rows: int,
@@ -521,9 +523,8 @@ def cache_append(cache: Cache, layer: int, k_new: torch.Tensor, v_new: torch.Ten
     """K and V of one layer for the last B tokens of each row; k_new, v_new: [N*B, Hkv*D] views
     with the same row stride."""
     N = cache._rows(seq, N)
-    width = cache.k.shape[2] * cache.k.shape[4]
-    ld = _tokens(k_new, N * B, width, cache.k.dtype, "k_new")
-    if _tokens(v_new, N * B, width, cache.k.dtype, "v_new") != ld:
+    ld = _tokens(k_new, N * B, cache._width, cache._dtype, "k_new")
+    if _tokens(v_new, N * B, cache._width, cache._dtype, "v_new") != ld:
         raise ValueError("k_new and v_new must have the same row stride")
     _check(lib().xpress_cache_append(cache._ref, layer, k_new.data_ptr(), v_new.data_ptr(), ld,
                                      _list(seq, N, torch.int32, "seq"), N, B, _stream()))
@@ -557,9 +558,9 @@ def block_attention(cache: Cache, layer: int, q: torch.Tensor, *, B: int, Hq: in
     """Attention of the last B tokens of each row over one layer; q and out: [N*B, Hq*D] views.
     The first ``shared`` tokens, common to all rows, are read once. scale defaults to D**-0.5."""
     N = cache._rows(seq, N)
-    D = cache.k.shape[4]
-    q_ld = _tokens(q, N * B, Hq * D, cache.k.dtype, "q")
-    out_ld = _tokens(out, N * B, Hq * D, cache.k.dtype, "out")
+    D = cache._D
+    q_ld = _tokens(q, N * B, Hq * D, cache._dtype, "q")
+    out_ld = _tokens(out, N * B, Hq * D, cache._dtype, "out")
     ws_ptr, ws_bytes = _ws(ws)
     _check(lib().xpress_block_attention(
         cache._ref, layer, q.data_ptr(), q_ld, _list(seq, N, torch.int32, "seq"), N, B, Hq,
