@@ -289,3 +289,53 @@ def test_a_captured_call_follows_the_lengths():
         x.check(got, what=f"replay {lengths}")
         eager = x.run(c, ws=ws)
         assert torch.equal(got[0], eager[0]) and torch.equal(got[1], eager[1])
+
+
+# Many query rows a head (2048 and more, D 128), where the shared part has items of its own kind.
+MANY_ROWS = [
+    dict(lengths=[400, 0, 395, 17, 300, 399, 396, 401] * 2, shared=390, B=16, Hkv=2, G=8, D=128, page=16),
+    dict(lengths=[200 + i for i in range(9)], shared=192, B=57, Hkv=1, G=4, D=128, page=64),  # 2052 rows
+    dict(lengths=[1300 - 40 * i for i in range(16)], shared=640, B=16, Hkv=1, G=8, D=128, page=128),
+    dict(lengths=[70] * 128, shared=64, B=4, Hkv=1, G=4, D=128, page=16),  # one tile of keys
+]
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("i", range(len(MANY_ROWS)))
+def test_many_query_rows(i, dtype):
+    c = MANY_ROWS[i]
+    x = Case(**c, dtype=dtype, seed=40 + i)
+    cache = x.cache()
+    x.check(x.run(cache), what=f"many rows {i} {dtype}")
+    x.check(x.run(cache, lse=False), what="no lse")
+
+
+@pytest.mark.parametrize("bad", [math.inf, math.nan])
+def test_many_query_rows_with_values_that_are_not_finite(bad):
+    """The last token of rows that end past the prefix is infinite or NaN: the queries before it do
+    not see it. (A row that ends inside the prefix shares its last token with the others.)"""
+    N, B = 16, 16
+    lengths = [90 + 3 * i for i in range(N - 2)] + [40, 0]
+    x = Case(lengths=lengths, shared=64, B=B, Hkv=1, G=8, D=128, page=16, seed=50)
+    for r, n in enumerate(lengths):
+        if n > 64:
+            p = x.table[r, (n - 1) // 16]
+            x.v[0, p, :, (n - 1) % 16] = bad
+            x.k[0, p, :, (n - 1) % 16, :64] = bad
+    got = x.run(x.cache())
+    early = [t for t in range(N * B) if t % B != B - 1]
+    assert not bool(got[0][early].isnan().any())
+    out, lse, mass, size = attention(
+        torch.nan_to_num(x.k[0], 0, 0, 0), torch.nan_to_num(x.v[0], 0, 0, 0), x.table, lengths, 16,
+        x.q, range(N), B, x.Hq, 128 ** -0.5)
+    bound, _ = attention_bounds(out, mass, size, max(lengths), 128, x.dtype)
+    assert bool(((got[0].double() - out).abs() <= bound)[early].all())
+    if math.isnan(bad):
+        assert bool(got[0][B - 1:(N - 2) * B:B].isnan().all())
+
+
+@pytest.mark.parametrize("shared", [0, 16500])
+def test_more_pages_than_an_item_holds(shared):
+    """Rows of more than a thousand small pages are split whatever their number."""
+    x = Case(lengths=[20000, 17001, 16501], shared=shared, B=2, Hkv=1, G=2, D=64, page=16, seed=60)
+    x.check(x.run(x.cache()), what=f"many pages, shared {shared}")

@@ -244,3 +244,60 @@ def test_workspace_contents_streams_and_replays():
         got = out.cpu().numpy(), acc.cpu().numpy()
         w = verify(f64(t), blk, lengths, None, temperature, u)
         assert np.array_equal(got[0], w[0]) and np.array_equal(got[1], w[1])
+
+
+@pytest.mark.parametrize("drawn", [False, True], ids=["point", "drawn"])
+@pytest.mark.parametrize("V", [1000, 20011])
+def test_numbers_next_to_the_border(V, drawn):
+    """u is p(d) / q(d) rounded to 32 bits, or a few steps beside it: the test is decided in 64 bits."""
+    N, B = 41, 2
+    rng, x, blk, u, _, _ = draw(N, B, V, 31, agree=1.0)
+    t = strided(x, torch.float32, 0)
+    temperature = rng.choice([0.7, 1.0, 1.6], N).astype(np.float32)
+    q = None
+    if drawn:
+        noisy = x.reshape(N, B, V)[:, 0] + rng.standard_normal((N, V)) * 0.3
+        q = strided(torch.softmax(torch.as_tensor(noisy), -1).numpy(), torch.float32, 0)
+    y = f64(t).reshape(N, B, V)[:, 0] / temperature.astype(np.float64)[:, None]
+    p = np.exp(y - y.max(1, keepdims=True))
+    p /= p.sum(1, keepdims=True)
+    i = np.arange(N)
+    border = p[i, blk[:, 1]] / (1 if q is None else f64(q)[i, blk[:, 1]])
+    steps = np.tile(np.array([0, 1, -1, 2, -3], np.int32), 9)[:N]
+    u[:, 0] = np.minimum(border, 1 - 2.0 ** -20).astype(np.float32)
+    u[:, 0] = (u[:, 0].view(np.int32) + steps).view(np.float32)
+    want = verify(f64(t), blk, None, None if q is None else f64(q), temperature, u)
+    got = run(t, blk, q=q, u=u, temperature=temperature)
+    assert 0 < want[1].sum() < N
+    assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0])
+
+
+@pytest.mark.parametrize("V", [524289, 700001])
+def test_long_vocabularies(V):
+    rng, x, blk, u, _, _ = draw(3, 2, V, 12, agree=0.5)
+    x[1, V - 2] = x[3, V - 1] = 14.0  # most of the weight at the end
+    for dtype in (torch.bfloat16, torch.float32):
+        t = strided(x, dtype, 1)
+        for temperature in (np.array([0, 1, 0.5], np.float32), np.array([1, 0.8, 0], np.float32)):
+            want = verify(f64(t), blk, None, None, temperature, u)
+            got = run(t, blk, u=u, temperature=temperature)
+            assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0])
+
+
+def test_infinite_logits_in_several_chunks_and_infinite_temperature():
+    inf, V = math.inf, 20011
+    rng = np.random.default_rng(8)
+    x = rng.standard_normal((8, V)).astype(np.float32)
+    x[0, [5, 9000, 20010]] = inf
+    x[2, [8191, 8192]] = inf
+    x[2, 100:200] = math.nan
+    blk = np.array([[0, 7], [0, 8192], [0, 3], [0, 4]])
+    temperature = np.array([1, 1, inf, inf], np.float32)
+    x[6, ::3] = -inf
+    u = np.array([[0.5, 0.6], [0.4, 0.2], [0.9, 0.37], [0.5, 0.999]], np.float32)
+    t = strided(x, torch.float32, 0)
+    flat = f64(t)
+    flat[4:] = np.where(np.isneginf(flat[4:]), -inf, 0)  # equal weights at an infinite temperature
+    want = verify(flat, blk, None, None, np.ones(4, np.float32), u)
+    got = run(t, blk, u=u, temperature=temperature)
+    assert np.array_equal(got[1], want[1]) and np.array_equal(got[0], want[0])
