@@ -9,6 +9,8 @@
 #include "serve.hpp"
 #include "cache_index.hpp"
 
+#include <algorithm>
+
 #include <limits.h>
 
 namespace xpress {
@@ -257,32 +259,38 @@ constexpr int kCopy = 8;  // loads of a thread in flight: 32 KB a workgroup (wit
                            // dozen pages of 1 MiB took 9.2 us instead of 6.4, 512 of them 221
                            // instead of 213)
 
-// Copies pages from[i] -> to[i], i < *count, in every layer of K and V. One workgroup per (page,
-// layer and side) at a time; `chunks` 16-byte pieces per page. 537 MB read and as much written: 213 us,
-// 5.0 TB/s, the rate of a copy of 4 GiB.
-__global__ __launch_bounds__(256) void copy_pages_kernel(const int32_t* __restrict__ count,
-                                                         const int32_t* __restrict__ from,
-                                                         const int32_t* __restrict__ to,
-                                                         u32x4* k, u32x4* v, int n_layers,
-                                                         int64_t n_pages, int64_t chunks) {
-  const int64_t items = (int64_t)*count * n_layers * 2;
-  for (int64_t it = blockIdx.x; it < items; it += gridDim.x) {
-    const int i = (int)(it / (n_layers * 2)), side = (int)(it % (n_layers * 2));
-    const int a = from[i];
+// Page copies from[i] -> to[i], i < *count, in every layer of K and V.
+struct Copies {
+  const int32_t *count, *from, *to;
+  u32x4 *k, *v;
+  int n_layers;
+  int64_t n_pages, chunks;  // 16-byte pieces of a page
+};
+
+// One workgroup per (page, layer and side) at a time. 537 MB read and as much written: 213 us, 5.0
+// TB/s, the rate of a copy of 4 GiB.
+__device__ __forceinline__ void copy_pages(const Copies& C, unsigned first, unsigned step) {
+  const int64_t items = (int64_t)*C.count * C.n_layers * 2;
+  for (int64_t it = first; it < items; it += step) {
+    const int i = (int)(it / (C.n_layers * 2)), side = (int)(it % (C.n_layers * 2));
+    const int a = C.from[i];
     if (a < 0) continue;
-    u32x4* pool = (side & 1 ? v : k) + (int64_t)(side >> 1) * n_pages * chunks;
-    const u32x4* x = pool + a * chunks;
-    u32x4* y = pool + to[i] * chunks;
+    u32x4* pool = (side & 1 ? C.v : C.k) + (int64_t)(side >> 1) * C.n_pages * C.chunks;
+    const u32x4* x = pool + a * C.chunks;
+    u32x4* y = pool + C.to[i] * C.chunks;
     int j = threadIdx.x;
-    for (; j + 256 * (kCopy - 1) < chunks; j += 256 * kCopy) {
+    for (; j + 256 * (kCopy - 1) < C.chunks; j += 256 * kCopy) {
       u32x4 c[kCopy];
 #pragma unroll
       for (int u = 0; u < kCopy; ++u) c[u] = x[j + u * 256];
 #pragma unroll
       for (int u = 0; u < kCopy; ++u) y[j + u * 256] = c[u];
     }
-    for (; j < chunks; j += 256) y[j] = x[j];
+    for (; j < C.chunks; j += 256) y[j] = x[j];
   }
+}
+__global__ __launch_bounds__(256) void copy_pages_kernel(Copies C) {
+  copy_pages(C, blockIdx.x, gridDim.x);
 }
 
 // A thread a 16-byte piece of a token. The new values are read beside the row's length and table.
@@ -372,26 +380,29 @@ __global__ __launch_bounds__(kPlan) void compact_plan_kernel(Pages P, int32_t* l
   }
 }
 
-__global__ __launch_bounds__(256) void compact_tables_kernel(Pages P, const int32_t* live,
-                                                             void* ws) {
-  const CompactScratch S = compact_scratch(ws, P.n_pages);
+// The tables (a workgroup a row) and the copies, which need the plan alone, in one launch.
+__global__ __launch_bounds__(256) void compact_move_kernel(Pages P, const int32_t* live,
+                                                           const int32_t* place, Copies C) {
   const int r = blockIdx.x, L = *live;
+  if (r >= P.rows) {
+    copy_pages(C, r - P.rows, gridDim.x - P.rows);
+    return;
+  }
   const int n = pages_of(clamp_len(P.len[r], P.ld, P.shift), P.shift);
   int32_t* t = P.table + (int64_t)r * P.ld;
   for (int j = threadIdx.x; j < n; j += blockDim.x) {
     const int id = t[j];
-    if (page_ok(id, P.n_pages) && id >= L) t[j] = S.place[id];
+    if (page_ok(id, P.n_pages) && id >= L) t[j] = place[id];
   }
 }
 
-hipError_t launch_copy(const xpress_cache& c, const int32_t* count, const int32_t* from,
-                       const int32_t* to, int64_t most, hipStream_t s) {
-  const int64_t chunks = (int64_t)c.Hkv * c.page * c.D * 2 / 16;
-  const int64_t items = most * c.n_layers * 2;
-  hipLaunchKernelGGL(copy_pages_kernel, dim3((unsigned)(items < 2048 ? items : 2048)), dim3(256),
-                     0, s, count, from, to, static_cast<u32x4*>(c.k), static_cast<u32x4*>(c.v),
-                     c.n_layers, (int64_t)c.n_pages, chunks);
-  return hipGetLastError();
+Copies copies(const xpress_cache& c, const int32_t* count, const int32_t* from, const int32_t* to) {
+  return Copies{count, from, to, static_cast<u32x4*>(c.k), static_cast<u32x4*>(c.v), c.n_layers,
+                c.n_pages, (int64_t)c.Hkv * c.page * c.D * 2 / 16};
+}
+// Workgroups for `most` page copies.
+unsigned copy_grid(const xpress_cache& c, int64_t most) {
+  return (unsigned)std::min<int64_t>(most * c.n_layers * 2, 2048);
 }
 
 }  // namespace
@@ -416,7 +427,9 @@ hipError_t launch_cache_extend(const xpress_cache& c, const int32_t* seq, int N,
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const ExtendScratch S = extend_scratch(ws, N);
-  return launch_copy(c, S.ncopy, S.from, S.to, N, s);
+  hipLaunchKernelGGL(copy_pages_kernel, dim3(copy_grid(c, N)), dim3(256), 0, s,
+                     copies(c, S.ncopy, S.from, S.to));
+  return hipGetLastError();
 }
 
 hipError_t launch_cache_append(const xpress_cache& c, int layer, const void* k_new,
@@ -440,14 +453,13 @@ hipError_t launch_cache_trim(const xpress_cache& c, const int32_t* seq, int N, c
 
 hipError_t launch_cache_compact(const xpress_cache& c, int32_t* live, void* ws, hipStream_t s) {
   hipLaunchKernelGGL(compact_plan_kernel, dim3(1), dim3(kPlan), 0, s, pages(c), live, ws);
-  hipError_t e = hipGetLastError();
-  if (e != hipSuccess) return e;
-  hipLaunchKernelGGL(compact_tables_kernel, dim3(c.rows), dim3(256), 0, s, pages(c),
-                     static_cast<const int32_t*>(live), ws);
-  e = hipGetLastError();
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess) return e;
   const CompactScratch S = compact_scratch(ws, c.n_pages);
-  return launch_copy(c, S.nmove, S.from, S.to, (c.n_pages + 1) / 2, s);
+  hipLaunchKernelGGL(compact_move_kernel, dim3(c.rows + copy_grid(c, (c.n_pages + 1) / 2)), dim3(256),
+                     0, s, pages(c), static_cast<const int32_t*>(live), S.place,
+                     copies(c, S.nmove, S.from, S.to));
+  return hipGetLastError();
 }
 
 }  // namespace xpress
