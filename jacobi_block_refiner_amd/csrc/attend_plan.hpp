@@ -30,7 +30,13 @@ constexpr int kCUs = 256;
 // wave's sums alone take 256 registers.
 constexpr int kWideRows = 2048;
 constexpr int kWideItems = 2048;  // wide items at most, unless one split a tile makes more
-constexpr int kItems = 1024;  // narrow items wanted where the rows alone give fewer
+// Narrow items wanted where the rows alone give fewer: kItems without a shared part; with one, of the
+// shared part half of it at D 64 (three workgroups a CU) and a quarter else (two, one): more slots
+// cost their join (16 requests of 16 tokens x 4 heads, 4096 shared and 512 own keys, D 128: 47 us
+// with 512 items of the shared part, 42 with 256; 32 requests x 8 heads at D 64: 59 and 65), and of
+// the requests' own half of it, but a quarter at D 256 (32 requests decoding, D 128: 33 us with
+// 512, 38 with 256; 32 requests at D 256: 159 and 156).
+constexpr int kItems = 1024;
 constexpr int kLeast = 128;  // keys of a split of one request's own at least,
 constexpr int kLeastShared = 256;  // and of the shared part (more splits cost the join: 41 -> 36 us)
 constexpr int kFewRows = 2048;  // rows of out up to which the join takes four groups of slots
@@ -48,7 +54,10 @@ inline AttendPlan plan_of(const xpress_cache& c, int N, int B, int Hq, int share
   AttendPlan p{};
   p.wide = shared > 0 && c.D == 128 && rows >= kWideRows;
   p.tiles_own = (int)ceil_div((int64_t)B * G, kNarrow * 32);
-  const int want = p.wide ? kCUs : shared > 0 ? kItems / 2 : kItems;
+  const int want = p.wide ? kCUs
+                   : shared == 0 ? kItems
+                   : c.D == 256  ? kItems / 4
+                                 : kItems / 2;
   int64_t s = ceil_div(want, (int64_t)N * c.Hkv * p.tiles_own);
   s = std::max<int64_t>(1, std::min({s, ceil_div(own, p.wide ? 4 * kLeast : kLeast), (int64_t)kSplits}));
   // (a request that does not see the whole shared part has less than shared + B keys, all its own)
@@ -72,7 +81,7 @@ inline AttendPlan plan_of(const xpress_cache& c, int N, int B, int Hq, int share
         }
       }
     } else {
-      s = ceil_div(want, tiles);
+      s = ceil_div(c.D == 64 ? kItems / 2 : kItems / 4, tiles);
       s = std::max<int64_t>(1, std::min({s, ceil_div(shared, kLeastShared), (int64_t)kSplits}));
     }
     s = std::max(s, ceil_div(shared, most));

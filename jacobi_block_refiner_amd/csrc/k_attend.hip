@@ -342,20 +342,23 @@ template <int N> __device__ __forceinline__ void feed() {
 // One work item: NW waves of 32 query rows each; K and V tiles of KT keys go from HBM straight into an
 // LDS ring of three or four stages.
 //
-// Narrow (NW = 4, two or three workgroups a CU): for items that wait for HBM. Tiles are taken one
-// after the other with one barrier each; the workgroups of a CU fill each other's waits.
+// Narrow (NW = 4): for items that wait for HBM. Tiles are taken one after the other with one barrier
+// each; the workgroups of a CU (three at D 64, two at 128, one at 256) fill each other's waits. At D
+// 128 a tile is 16 KB, and two workgroups that ask three tiles ahead read faster than three that ask
+// two ahead: 256 requests decoding 1024 tokens 110 us (4.9 TB/s) and 136, 32 decoding behind 4096
+// shared ones 33 and 35. At D 64 three are faster (32 requests, 8192 shared tokens: 59 and 63 us).
 //
 // Wide (NW = 8, one workgroup a CU): shared items that the matrix core bounds. The two waves of a SIMD
 // are half a tile apart: while one multiplies (scores of tile t, values of tile t-1) the other forms
 // weights, and after each such half they meet and change roles. A tile needs about as many cycles of
 // the matrix core as of the vector unit; with both waves in step, each unit waited for the other.
 template <bool F16, int D, int NW, int KT>
-__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : NW == kWide ? 2 : 3) void attend_kernel(
+__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void attend_kernel(
     Args A) {
   using C = Core<F16, D, KT>;
   using S = Source<D, KT, NW>;
   constexpr bool WIDE = NW == kWide;
-  constexpr int NS = WIDE ? 4 : 3, STAGE = 2 * C::SIDE, CW = S::CW;
+  constexpr int NS = WIDE || D == 128 ? 4 : 3, STAGE = 2 * C::SIDE, CW = S::CW;
   __shared__ uint4 s_tile[NS * STAGE / 16];
   __shared__ int s_ids[kIds];
   __shared__ int s_wild[2];  // first and last masked tile with V values that are not finite
@@ -489,21 +492,24 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : NW == kWide ? 2 : 3) void a
       src.turn(next);
       src.copy_k(to);
       src.template copy_v<false>(to + C::SIDE);
-      to = to == 2 * STAGE ? 0 : to + STAGE;
+      to = to == (NS - 1) * STAGE ? 0 : to + STAGE;
     };
     auto enter = [&] {
-      if (t + 1 < nt)
+      if (t + NS - 2 < nt)
+        meet<2 * CW * (NS - 2)>();
+      else if (NS > 3 && t + 1 < nt)
         meet<2 * CW>();
       else
         meet<0>();
-      if (t + 2 < nt) copy_both(t + 3);
+      if (t + NS - 1 < nt) copy_both(t + NS);
     };
     auto leave = [&] {
-      at = at == 2 * STAGE ? 0 : at + STAGE;
+      at = at == (NS - 1) * STAGE ? 0 : at + STAGE;
       ++t;
     };
-    if (nt > 0) copy_both(1);
-    if (nt > 1) copy_both(2);
+#pragma unroll
+    for (int i = 1; i < NS; ++i)
+      if (nt >= i) copy_both(i);
     while (t < min(nt, whole)) {
       enter();
       if (!idle) {
