@@ -23,12 +23,12 @@ constexpr int narrow_step(int D) { return D == 64 ? 64 : 32; }  // keys of a til
 constexpr int kWideStep = 64;
 constexpr int kCUs = 256;
 // Query rows a head from which the shared part goes to wide items, D 128 alone. Narrow against wide,
-// us a call: 512 rows, 8192 keys 42 and 62; 1024 rows, 4096 keys 48 and 54; 2048 rows, 4096 keys 67
-// and 64; 2048 rows, 16384 keys 170 and 163; 4096 rows, 2048 keys 73 and 65; 20480 rows, 16384 keys
-// 1777 and 1523. At D 64 (4096 and 16384 rows, 8192 keys) 62 and 80, 199 and 244: its tiles have half
-// the products for the same weights; at D 256 (2048 and 8192 rows) 177 and 205, 510 and 638: one
-// wave's sums alone take 256 registers.
-constexpr int kWideRows = 2048;
+// us a call: 512 rows, 8192 keys 39 and 54; 1024 rows, 4096 keys 39 and 50; 1536 rows, 4096 keys 58
+// and 53; 2048 rows, 4096 keys 62 and 59; 2048 rows, 16384 keys 197 and 160; 4096 rows, 2048 keys 65
+// and 59; 20480 rows, 16384 keys 1579 and 1495. At D 64 (4096 and 16384 rows, 8192 keys) 62 and 80,
+// 199 and 244: its tiles have half the products for the same weights; at D 256 (2048 and 8192 rows)
+// 177 and 205, 510 and 638: one wave's sums alone take 256 registers.
+constexpr int kWideRows = 1536;
 constexpr int kWideItems = 2048;  // wide items at most, unless one split a tile makes more
 // Narrow items wanted where the rows alone give fewer: kItems without a shared part; with one, of the
 // shared part half of it at D 64 (three workgroups a CU) and a quarter else (two, one): more slots
