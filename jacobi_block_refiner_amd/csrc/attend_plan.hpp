@@ -9,7 +9,7 @@
 
 namespace xpress {
 
-constexpr int kNarrow = 4, kWide = 8;  // waves (of 32 query rows) of an item
+constexpr int kSlim = 2, kNarrow = 4, kWide = 8;  // waves (of 32 query rows) of an item
 constexpr int kIds = 1024;  // table entries an item keeps in LDS: bounds its range of keys
 
 struct AttendPlan {

@@ -340,13 +340,20 @@ template <int N> __device__ __forceinline__ void feed() {
 }
 
 // One work item: NW waves of 32 query rows each; K and V tiles of KT keys go from HBM straight into an
-// LDS ring of three or four stages.
+// LDS ring of two to four stages.
 //
 // Narrow (NW = 4): for items that wait for HBM. Tiles are taken one after the other with one barrier
 // each; the workgroups of a CU (three at D 64, two at 128, one at 256) fill each other's waits. At D
 // 128 a tile is 16 KB, and two workgroups that ask three tiles ahead read faster than three that ask
 // two ahead: 256 requests decoding 1024 tokens 110 us (4.9 TB/s) and 136, 32 decoding behind 4096
 // shared ones 33 and 35. At D 64 three are faster (32 requests, 8192 shared tokens: 59 and 63 us).
+//
+// Slim (NW = 2, D 256): items of a request's own keys alone, at most 64 query rows, where they fill
+// more than one round of the card. A narrow item at D 256 keeps a CU to itself (its registers, and 96
+// KB of tiles), and with one row of queries three of its four waves only copy; two slim ones share a
+// CU. 64 requests decoding 1024 tokens (8 heads, 4 queries each) 70 us and 105 narrow, 256 requests
+// 225 and 348. Beside shared items they would be a launch of their own: 168 and 100 us for 64
+// requests behind 4096 tokens, so there the narrow ones stay.
 //
 // Wide (NW = 8, one workgroup a CU): shared items that the matrix core bounds. The two waves of a SIMD
 // are half a tile apart: while one multiplies (scores of tile t, values of tile t-1) the other forms
@@ -360,7 +367,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void atte
   using C = Core<F16, D, KT>;
   using S = Source<D, KT, NW>;
   constexpr bool WIDE = NW == kWide;
-  constexpr int NS = WIDE || D == 128 ? 4 : 3, STAGE = 2 * C::SIDE, CW = S::CW;
+  constexpr int NS = NW == kSlim ? 2 : WIDE || D == 128 ? 4 : 3, STAGE = 2 * C::SIDE, CW = S::CW;
   __shared__ uint4 s_tile[NS * STAGE / 16];
   __shared__ int s_ids[kIds];
   __shared__ int s_wild[2];  // first and last masked tile with V values that are not finite
@@ -699,9 +706,17 @@ hipError_t launch_t(Args A, bool wide, hipStream_t s) {
     if (e != hipSuccess) return e;
     shared = A.tiles_sh = A.s_sh = 0;  // done
   }
-  hipLaunchKernelGGL((attend_kernel<F16, D, kNarrow, narrow_step(D)>),
-                     dim3((unsigned)(shared + own)), dim3(kNarrow * 64), 0, s, A);
-  hipError_t e = hipGetLastError();
+  bool slim = false;
+  if constexpr (D == 256) slim = shared == 0 && A.B * A.G <= kSlim * 32 && own > kCUs;
+  if (slim) {
+    if constexpr (D == 256)
+      hipLaunchKernelGGL((attend_kernel<F16, D, kSlim, narrow_step(D)>), dim3((unsigned)own),
+                         dim3(kSlim * 64), 0, s, A);
+  } else {
+    hipLaunchKernelGGL((attend_kernel<F16, D, kNarrow, narrow_step(D)>),
+                       dim3((unsigned)(shared + own)), dim3(kNarrow * 64), 0, s, A);
+  }
+  const hipError_t e = hipGetLastError();
   if (e != hipSuccess || A.direct) return e;
   const int64_t rows = (int64_t)A.N * A.B * A.Hq;
   const int groups = rows <= kFewRows ? 4 : 1, per = 256 / (D / 4 * groups);

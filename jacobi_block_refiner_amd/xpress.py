@@ -442,7 +442,8 @@ def _ws(ws):
 @dataclass
 class Cache:
     """A paged K/V cache (``xpress_cache``): pools of pages, one table row a sequence, tokens a
-    sequence and holders a page. The caller owns the tensors; the struct is built once."""
+    sequence and holders a page. The caller owns the tensors; the struct is built with the object, and
+    anew when one of its tensors is replaced."""
 
     k: torch.Tensor  # [n_layers, n_pages, Hkv, page, D] bf16 or fp16
     v: torch.Tensor
@@ -471,6 +472,16 @@ class Cache:
                               self.length.data_ptr(), self.ref.data_ptr())
         self._ref = ctypes.byref(self._struct)
         self._dtype, self._width, self._D = self.k.dtype, Hkv * D, D
+
+    def __setattr__(self, name, value):
+        before = self.__dict__.get(name)
+        object.__setattr__(self, name, value)
+        if isinstance(before, torch.Tensor) and "_ref" in self.__dict__:
+            try:
+                self.__post_init__()
+            except Exception:
+                object.__setattr__(self, name, before)
+                raise
 
     @classmethod
     def empty(cls, n_layers: int, n_pages: int, Hkv: int, page: int, D: int, rows: int,

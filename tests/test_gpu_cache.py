@@ -231,3 +231,15 @@ def test_offsets_past_32_bits(page, Hkv, D):
     assert c.ref[:4].tolist() == [2, 1, 1, 0] and int(c.ref.sum().item()) == 4
     del c, ws
     torch.cuda.empty_cache()
+
+
+def test_replaced_tensors_are_the_ones_used():
+    c = xpress.Cache.empty(1, 8, 1, 16, 64, 2, 4)
+    lacking, ws = torch.full((1,), 9, dtype=torch.int32, device="cuda"), xpress.cache_workspace(c, 2)
+    old = c.length
+    c.length = torch.zeros_like(old)
+    xpress.cache_extend(c, 20, lacking=lacking, ws=ws)
+    assert c.length.tolist() == [20, 20] and old.tolist() == [0, 0] and lacking.item() == 0
+    with pytest.raises(ValueError):
+        c.ref = torch.zeros(7, dtype=torch.int32, device="cuda")
+    assert c.ref.numel() == 8  # refused: the one before stays
