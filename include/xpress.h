@@ -310,9 +310,9 @@ xpress_status xpress_graph_destroy(void* graph);
  * every layer). Entries of a row past its last page are -1. ref[p] is the number of rows that hold
  * page p (0: the page is free). The caller owns every buffer and starts with ref = 0, len = 0 and
  * table = -1; the calls below keep them so.
- * Limits: 1 <= n_layers <= 2^16; 1 <= n_pages <= 2^24; page in {16, 32, 64, 128, 256}; 1 <= Hkv <= 256; D
- * in {64, 128, 256}; 1 <= rows <= 2^20; 1 <= table_ld <= 2^20; dtype XPRESS_BF16 or XPRESS_F16; k
- * and v 16-byte aligned, table, len and ref 4-byte aligned.
+ * Limits: 1 <= n_layers <= 2^16; 1 <= n_pages <= 2^24; page in {16, 32, 64, 128, 256}; 1 <= Hkv <=
+ * 256; D in {64, 128, 256}; 1 <= rows <= 2^20; 1 <= table_ld <= 2^20; dtype XPRESS_BF16 or
+ * XPRESS_F16; k and v 16-byte aligned, table, len and ref 4-byte aligned.
  * Lists of rows (`seq`, `src`, `dst`) are int32 on the device. seq NULL means rows 0..N-1. A row
  * outside [0, rows) is skipped. A row twice in one list is the caller's error (the metadata is
  * then unspecified; nothing outside the buffers is touched). A page id outside [0, n_pages) in
@@ -410,7 +410,8 @@ xpress_status xpress_block_attention(const xpress_cache* c, int32_t layer, const
  * appended. u: [N, B] fp32 in [0, 1) (nullable if temperature is NULL). blk: [N, B] int64;
  * out: [N, B] int64; accepted, drop: [N] int32; logits and q: XPRESS_BF16, _F16 or _F32 with row
  * strides ld >= V and q_ld >= V in elements, any alignment of the rows to their own elements.
- * 1 <= B <= 64; 1 <= V < 2^31; N*B*ceil((V+7)/8192) < 2^24. Deterministic: the same inputs give the same tokens. */
+ * 1 <= B <= 64; 1 <= V < 2^31; N*B*ceil((V+7)/8192) < 2^24. Deterministic: the same inputs give the
+ * same tokens. */
 xpress_status xpress_verify_workspace_size(int32_t n_max, int32_t B, int64_t V, size_t* bytes);
 xpress_status xpress_verify_draft(const void* logits, uint32_t logits_dtype, int64_t ld,
                                   const int64_t* blk, const int32_t* draft_len, const void* q,

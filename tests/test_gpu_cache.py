@@ -243,3 +243,37 @@ def test_replaced_tensors_are_the_ones_used():
     with pytest.raises(ValueError):
         c.ref = torch.zeros(7, dtype=torch.int32, device="cuda")
     assert c.ref.numel() == 8  # refused: the one before stays
+
+
+def test_more_rows_and_pages_than_a_step_of_the_plan():
+    """1100 rows and 9500 pages: the rows' needs, the free pages and the live ones take several steps."""
+    rng = np.random.default_rng(4)
+    rows = 1100
+    o = CacheOracle(1, 9500, 1, 16, 64, rows, 20, torch.bfloat16, 4)
+    c = device_cache(o)
+    ws = xpress.cache_workspace(c, rows)
+    lacking, live = torch.zeros(1, dtype=torch.int32, device="cuda"), i32([0])
+    every = np.arange(rows)
+    for turn, most in enumerate((200, 60, 90)):
+        each = np.minimum(rng.integers(0, most, rows), 320 - o.length)
+        want = o.extend(every, each)
+        xpress.cache_extend(c, i32(each), lacking=lacking, ws=ws)
+        same(c, o, f"turn {turn} extend")
+        assert int(lacking.item()) == want == (0, 0, 99)[turn]
+        drop = np.where(rng.random(rows) < 0.25, rng.integers(0, 150, rows), 0)
+        o.trim(every, drop)
+        xpress.cache_trim(c, i32(drop))
+        src, dst = rng.permutation(rows)[:200].reshape(2, 100)
+        o.fork(src, dst)
+        xpress.cache_fork(c, i32(src), i32(dst))
+        same(c, o, f"turn {turn} trim and fork")
+        if turn:
+            want = o.compact()
+            xpress.cache_compact(c, live=live, ws=ws)
+            same(c, o, f"turn {turn} compact")
+            assert int(live.item()) == want > 4096
+    each = np.minimum(rng.integers(100, 200, rows), 320 - o.length)
+    want = o.extend(every, each)
+    xpress.cache_extend(c, i32(each), lacking=lacking, ws=ws)
+    same(c, o, "too many pages")
+    assert int(lacking.item()) == want > 0
