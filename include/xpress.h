@@ -373,8 +373,8 @@ xpress_status xpress_cache_compact(const xpress_cache* c, int32_t* live, void* w
  *   out[i, b, h] = sum_t softmax_t(scale * q[i, b, h] . k[t, h / (Hq/Hkv)]) v[t, h / (Hq/Hkv)]
  * over the tokens t = 0 .. len[seq[i]] - B + b of row seq[i] (the block's own tokens are the
  * row's last B, so the mask is causal inside the block; B = 1 is plain decoding). The first
- * `shared` tokens are read once for all query rows, through the first request's table: the caller
- * vouches that every row's first min(shared, len) tokens are the same. The result is that of
+ * `shared` tokens are read once for many query rows, through the table of one request that sees them
+ * all: the caller vouches that every row's first min(shared, len) tokens are the same. The result is that of
  * attending over each row alone. A query that sees no token gives 0 (and lse = -inf).
  * q: token i*B + b at element (i*B + b)*q_ld, [Hq, D] dense; out likewise with out_ld; both of the
  * cache's dtype, 16-byte aligned, strides multiples of 8. lse: [N*B, Hq] fp32, nullable, the

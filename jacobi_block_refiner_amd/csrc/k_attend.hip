@@ -370,6 +370,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void atte
   constexpr int NS = NW == kSlim ? 2 : WIDE || D == 128 ? 4 : 3, STAGE = 2 * C::SIDE, CW = S::CW;
   __shared__ uint4 s_tile[NS * STAGE / 16];
   __shared__ int s_ids[kIds];
+  __shared__ int s_req;
   __shared__ int s_wild[2];  // first and last masked tile with V values that are not finite
 
   const int lane = threadIdx.x & 63, h = lane >> 5, col = lane & 31;
@@ -416,6 +417,16 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void atte
   const int sight = min(in_sight(len, A.B, token % A.B), kend);
   const bool blind =
       !valid || sight <= kbeg || (is_shared && own_begin(len, A.B, A.shared) < A.shared);
+  // Whose table leads to the shared part: the first request's, unless it ends inside it (a short or an
+  // empty row); then that of any request whose rows are here. Where there is none, all is dropped.
+  if (is_shared && own_begin(list_len(A, 0), A.B, A.shared) < A.shared) {
+    if (threadIdx.x == 0) s_req = INT_MAX;
+    __syncthreads();
+    if (!blind) atomicMin(&s_req, token / A.B);
+    __syncthreads();
+    req = __builtin_amdgcn_readfirstlane(s_req);
+    if (req == INT_MAX) req = 0;
+  }
   C w;
   w.begin(s_tile, A.q + token * A.q_ld + (int64_t)hq * D, A.c);
   {

@@ -360,3 +360,15 @@ def test_many_requests_of_wide_heads(B, G, page, dtype):
                                          bad.q, range(len(lengths)), B, bad.Hq, 256 ** -0.5)
         bound, _ = attention_bounds(out, mass, size, max(lengths), 256, dtype)
         assert bool(((got[0].double() - out).abs() <= bound)[early].all())
+
+
+@pytest.mark.parametrize("lengths,B,G,D,page", [
+    ([0, 400, 395, 17, 300, 399], 5, 3, 64, 16), ([70, 300, 290], 16, 4, 128, 32),
+    ([3, 0, 0, 310, 309], 2, 2, 256, 64), ([0] * 5 + [250, 350, 0, 299] * 3, 64, 4, 128, 16),  # wide
+    ([100, 0, 30], 4, 2, 128, 16)])  # no row sees the whole prefix
+def test_a_first_request_that_ends_inside_the_prefix(lengths, B, G, D, page):
+    x = Case(lengths=lengths, shared=270, B=B, Hkv=2 if B < 64 else 1, G=G, D=D, page=page, seed=80)
+    x.check(x.run(x.cache()), what=f"short first row, D {D}")
+    rows = list(range(len(lengths)))[::-1]
+    x.check(x.run(x.cache(), seq=torch.tensor(rows, dtype=torch.int32, device="cuda"), rows=rows),
+            rows=rows, what="the other way round")
