@@ -315,9 +315,9 @@ __global__ __launch_bounds__(kThreads, 8) void stats_kernel(Args A) {
       all = wave_sum(all);
       if (fabs(test * all - drafted) <= 1e-5 * drafted) {
         all = 0;
-        const int pieces = (A.V + row.off + E - 1) / E;
+        const int64_t pieces = ((int64_t)A.V + row.off + E - 1) / E;
 #pragma unroll 1
-        for (int j = t; j < pieces; j += 64) {
+        for (int64_t j = t; j < pieces; j += 64) {
           const Piece<T> y = row.load(j);
 #pragma unroll
           for (int e = 0; e < E; ++e) all += weight(y[e], w.m, scale);
