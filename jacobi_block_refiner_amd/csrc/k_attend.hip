@@ -359,8 +359,9 @@ template <int N> __device__ __forceinline__ void feed() {
 // are half a tile apart: while one multiplies (scores of tile t, values of tile t-1) the other forms
 // weights, and after each such half they meet and change roles. A tile needs about as many cycles of
 // the matrix core as of the vector unit; with both waves in step, each unit waited for the other.
-// 20480 rows a head, 16384 keys, 8 heads: 1377 us, 1.0 PFLOP/s, where the card's power limit holds
-// the clock at 1.9 GHz; 2560 rows, 8192 keys: 106 us, 0.8 PFLOP/s on 240 CUs.
+// 20480 rows a head, 16384 keys, 8 heads: 1377 us, 1.0 PFLOP/s at 1.9 to 2.0 GHz (the power limit
+// takes the rest of 2.3), the matrix core busy 47% of the cycles; 2560 rows, 8192 keys: 106 us, 0.8
+// PFLOP/s on 240 CUs.
 template <bool F16, int D, int NW, int KT>
 __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void attend_kernel(
     Args A) {
