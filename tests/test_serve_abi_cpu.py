@@ -31,7 +31,7 @@ def says(status, text, want=xpress.ERR_ARG):
     assert text in L().xpress_last_error(), L().xpress_last_error()
 
 
-BAD_CACHES = [(dict(n_layers=0), b"n_layers"), (dict(n_pages=0), b"n_pages"),
+BAD_CACHES = [(dict(n_layers=0), b"n_layers"), (dict(n_layers=65537), b"n_layers"), (dict(n_pages=0), b"n_pages"),
               (dict(n_pages=(1 << 24) + 1), b"n_pages"), (dict(page=8), b"page"),
               (dict(page=48), b"page"), (dict(Hkv=0), b"Hkv"), (dict(Hkv=257), b"Hkv"),
               (dict(D=96), b"D="), (dict(dtype=xpress.F32), b"dtype"), (dict(rows=0), b"rows"),
