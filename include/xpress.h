@@ -315,7 +315,8 @@ xpress_status xpress_graph_destroy(void* graph);
  * XPRESS_F16; k and v 16-byte aligned, table, len and ref 4-byte aligned.
  * Lists of rows (`seq`, `src`, `dst`) are int32 on the device. seq NULL means rows 0..N-1. A row
  * outside [0, rows) is skipped. A row twice in one list is the caller's error (the metadata is
- * then unspecified; nothing outside the buffers is touched). A page id outside [0, n_pages) in
+ * then unspecified, counts below 0 among it, which count as 0; nothing outside the buffers is
+ * touched, by that call or a later one). A page id outside [0, n_pages) in
  * the used part of a table is too: it is clamped where it is read and never counted. */
 typedef struct {
   int32_t n_layers, n_pages, page, Hkv, D;

@@ -31,6 +31,16 @@ XP_HD int clamp_page(int id, int n_pages) {
 }
 XP_HD bool page_ok(int id, int n_pages) { return id >= 0 && id < n_pages; }
 
+// Rows that hold a page, by its count. A list that names a row twice may give its pages back twice and
+// leave a count below 0: nobody holds such a page.
+XP_HD int holders(int ref) { return ref > 0 ? ref : 0; }
+
+// The two sides of a compaction to `live` pages (those with holders): a page that moves out of the
+// pool's rest, and a free one of the front that takes it in. There are as many of one side as of the
+// other, since all live pages fit in the front.
+XP_HD bool moves_out(int ref, int p, int live) { return holders(ref) > 0 && p >= live; }
+XP_HD bool takes_in(int ref, int p, int live) { return holders(ref) == 0 && p < live; }
+
 // Element offset of line `line` of page `id`, head `h`, inside one layer of K or V. 64 bits: a
 // layer of 2^16 pages of 64 tokens, 8 heads of 128 already holds 2^32 elements.
 XP_HD int64_t line_offset(int id, int h, int line, int Hkv, int page_shift, int D) {

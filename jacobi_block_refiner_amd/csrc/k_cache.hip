@@ -80,7 +80,7 @@ __device__ __forceinline__ int waves_before(int v, int* total) {
 }
 
 // A walk over the pool's counts takes kPlan * kScan pages a step; a wave has kScan * 64 of them in a
-// row, each lane every 64th, so that a ballot gives the ranks in id order.
+// row, each lane every 64th, so that a ballot gives the ranks in id order. Pages past the pool count -1.
 __device__ __forceinline__ int walk_at(int p0, int i) {
   return p0 + (threadIdx.x >> 6) * kScan * 64 + i * 64 + (threadIdx.x & 63);
 }
@@ -88,7 +88,7 @@ __device__ __forceinline__ void counts_at(const Pages& P, int p0, int* ref) {
 #pragma unroll
   for (int i = 0; i < kScan; ++i) {
     const int p = walk_at(p0, i);
-    ref[i] = p < P.n_pages ? P.ref[p] : -1;
+    ref[i] = p < P.n_pages ? holders(P.ref[p]) : -1;
   }
 }
 __device__ __forceinline__ int lanes_before(uint64_t m) {
@@ -350,8 +350,8 @@ __global__ __launch_bounds__(kPlan) void compact_plan_kernel(Pages P, int32_t* l
 #pragma unroll
     for (int i = 0; i < kScan; ++i) {
       const int p = walk_at(p0, i);
-      out[i] = __ballot(ref[i] > 0 && p >= L);
-      in[i] = __ballot(ref[i] == 0 && p < L);
+      out[i] = __ballot(moves_out(ref[i], p, L));
+      in[i] = __ballot(takes_in(ref[i], p, L));
       mine += __popcll(out[i]) + (__popcll(in[i]) << 16);
     }
     const int before = waves_before(mine, &all);
@@ -359,8 +359,9 @@ __global__ __launch_bounds__(kPlan) void compact_plan_kernel(Pages P, int32_t* l
 #pragma unroll
     for (int i = 0; i < kScan; ++i) {
       const int p = walk_at(p0, i);
-      if (ref[i] > 0 && p >= L) S.from[a + lanes_before(out[i])] = p;
-      if (ref[i] == 0 && p < L) S.to[b + lanes_before(in[i])] = p;
+      if (moves_out(ref[i], p, L)) S.from[a + lanes_before(out[i])] = p;
+      if (takes_in(ref[i], p, L)) S.to[b + lanes_before(in[i])] = p;
+      if (p >= L && p < P.n_pages) S.place[p] = p;  // unless it moves
       a += __popcll(out[i]);
       b += __popcll(in[i]);
     }
@@ -368,7 +369,9 @@ __global__ __launch_bounds__(kPlan) void compact_plan_kernel(Pages P, int32_t* l
     nto += all >> 16;
   }
   __syncthreads();
-  for (int i = t; i < nfrom; i += kPlan) {
+  // (the two sides are equal unless another stream changes counts between the walks)
+  const int nmove = min(nfrom, nto);
+  for (int i = t; i < nmove; i += kPlan) {
     const int a = S.from[i], b = S.to[i];
     S.place[a] = b;
     P.ref[b] = P.ref[a];
@@ -376,7 +379,7 @@ __global__ __launch_bounds__(kPlan) void compact_plan_kernel(Pages P, int32_t* l
   }
   if (t == 0) {
     *live = L;
-    *S.nmove = nfrom;
+    *S.nmove = nmove;
   }
 }
 

@@ -304,3 +304,47 @@ def test_oracles_on_cases_with_known_answers():
     q1 = np.array([[0.2, 0.8, 0.0]])
     assert verify(x, blk, None, q1, t, np.array([[0.3, 0.5]]))[0].tolist() == [[1, 2]]
     assert verify(x, blk, None, q1, t, np.array([[0.4, 0.6]]))[0].tolist() == [[2, -1]]
+
+
+COUNTS = r"""
+#include "cache_index.hpp"
+#include <cstdio>
+#include <vector>
+using namespace xpress;
+int main() {
+  uint32_t seed = 1;
+  for (int turn = 0; turn < 20000; ++turn) {
+    auto next = [&] { return (seed = seed * 1664525u + 1013904223u) >> 16; };
+    const int n = 1 + next() % 40;
+    std::vector<int> ref(n);
+    for (int& r : ref) r = (int)(next() % 6) - 2;  // -2 .. 3 holders
+    int live = 0, out = 0, in = 0;
+    for (int r : ref) live += holders(r) > 0;
+    for (int p = 0; p < n; ++p) {
+      if (holders(ref[p]) < 0 || (ref[p] >= 0 && holders(ref[p]) != ref[p])) return 1;
+      if (moves_out(ref[p], p, live) && takes_in(ref[p], p, live)) return 2;
+      // in the front a page is live or takes one in; past it a page moves out or is free
+      if ((holders(ref[p]) > 0) == (p < live ? takes_in(ref[p], p, live) : !moves_out(ref[p], p, live)))
+        return 3;
+      out += moves_out(ref[p], p, live);
+      in += takes_in(ref[p], p, live);
+    }
+    if (out != in) {
+      printf("turn %d: %d pages move, %d take them in\n", turn, out, in);
+      return 4;
+    }
+  }
+  return 0;
+}
+"""
+
+
+def test_a_compaction_has_a_place_for_every_page_it_moves(tmp_path):
+    """Whatever the counts, below 0 too (after a row twice in a list): no move without a target."""
+    src = tmp_path / "counts.cpp"
+    src.write_text(COUNTS)
+    exe = tmp_path / "counts"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover",
+                    f"-I{build.CSRC}", str(src), "-o", str(exe)], check=True)
+    got = subprocess.run([str(exe)], capture_output=True, text=True)
+    assert got.returncode == 0, (got.returncode, got.stdout)
