@@ -292,11 +292,11 @@ xpress_status xpress_graph_destroy(void* graph);
  * and the verification of the drafts. One turn of a batch is
  *   xpress_jacobi_step                  drafts B-1 tokens a request;
  *   xpress_cache_extend                 room for the block's B tokens (anchor and drafts);
- *   xpress_cache_append, xpress_block_attention   once a layer of the target;
+ *   xpress_cache_append_if, xpress_block_attention   once a layer of the target;
  *   xpress_verify_draft                 which drafts stand, and the next token;
- *   xpress_cache_trim                   gives back the refused drafts' tokens.
+ *   xpress_cache_trim_if                gives back the refused drafts' tokens.
  * The conventions above hold (device pointers, stream order, nothing allocated, host-side argument
- * errors, N == 0 is a no-op). Page tables, lengths and counts live on the device and are read when
+ * errors, N == 0 is a no-op). (The _if calls do nothing where the extension found no room.) Page tables, lengths and counts live on the device and are read when
  * the kernels run, so a captured turn follows them from replay to replay.
  * ------------------------------------------------------------------------------------------- */
 
@@ -344,7 +344,10 @@ xpress_status xpress_cache_fork(const xpress_cache* c, const int32_t* src, const
  * new tokens. Pages are taken in ascending id order among those with ref = 0 when the call
  * starts, rows in list order. *lacking (device, written): 0, or the number of pages that are
  * missing, or -1 where a row would pass table_ld pages; in both latter cases nothing is changed,
- * and the caller must not write the tokens it asked room for. */
+ * and the tokens that room was asked for must not be written or trimmed: they would be the rows' own
+ * last tokens, in pages that other rows may share. xpress_cache_append_if and xpress_cache_trim_if
+ * see to that on the device, so that a turn need not wait for *lacking; whoever reads the turn's
+ * tokens reads it beside them, and drops them where it is not 0. */
 xpress_status xpress_cache_extend(const xpress_cache* c, const int32_t* seq, int32_t N,
                                   const int32_t* add, int32_t add_all, int32_t* lacking, void* ws,
                                   size_t ws_bytes, xpress_stream stream);
@@ -353,15 +356,25 @@ xpress_status xpress_cache_extend(const xpress_cache* c, const int32_t* seq, int
  * position len[seq[i]] - B + b (skipped where that is negative). k_new, v_new: token i*B + b at
  * element (i*B + b)*ld_new, [Hkv, D] dense, the cache's dtype, 16-byte aligned, ld_new a multiple
  * of 8 and at least Hkv*D (so slices of a fused projection's output can be passed).
- * N*B*Hkv < 2^26. */
+ * N*B*Hkv < 2^26.
+ * _append_if: the same, unless *lacking (device, nullable), as an extension wrote it, is not 0 when
+ * the kernel runs: then nothing is written. */
 xpress_status xpress_cache_append(const xpress_cache* c, int32_t layer, const void* k_new,
                                   const void* v_new, int64_t ld_new, const int32_t* seq, int32_t N,
                                   int32_t B, xpress_stream stream);
+xpress_status xpress_cache_append_if(const xpress_cache* c, const int32_t* lacking, int32_t layer,
+                                     const void* k_new, const void* v_new, int64_t ld_new,
+                                     const int32_t* seq, int32_t N, int32_t B,
+                                     xpress_stream stream);
 
 /* Freeing: row seq[i] loses its last drop[i] tokens (clamped to [0, len]; drop NULL: all of them);
- * pages that hold none of its tokens any more leave its table and their counts go down. */
+ * pages that hold none of its tokens any more leave its table and their counts go down.
+ * _trim_if: the same, unless *lacking (device, nullable), as an extension wrote it, is not 0 when the
+ * kernel runs: then nothing is freed. */
 xpress_status xpress_cache_trim(const xpress_cache* c, const int32_t* seq, int32_t N,
                                 const int32_t* drop, xpress_stream stream);
+xpress_status xpress_cache_trim_if(const xpress_cache* c, const int32_t* lacking, const int32_t* seq,
+                                   int32_t N, const int32_t* drop, xpress_stream stream);
 
 /* Compaction: with L = number of pages with ref > 0, the live pages with ids >= L (ascending) move
  * to the free ids < L (ascending), in every layer; counts and the tables of all rows follow.

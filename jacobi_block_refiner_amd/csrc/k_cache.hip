@@ -115,10 +115,11 @@ __global__ __launch_bounds__(256) void fork_kernel(Pages P, const int32_t* src, 
   if (threadIdx.x == 0) P.len[to] = new_len;
 }
 
-__global__ __launch_bounds__(256) void trim_kernel(Pages P, const int32_t* seq,
-                                                   const int32_t* drop) {
+__global__ __launch_bounds__(256) void trim_kernel(Pages P, const int32_t* lacking,
+                                                   const int32_t* seq, const int32_t* drop) {
+  const int no = lacking ? *lacking : 0;
   const int r = row_of(seq, blockIdx.x, P.rows);
-  if (r < 0) return;
+  if (r < 0 || no) return;
   const int len = clamp_len(P.len[r], P.ld, P.shift);
   const int d = drop ? min(max(drop[blockIdx.x], 0), len) : len;
   __syncthreads();  // every thread has read the length
@@ -293,8 +294,10 @@ __global__ __launch_bounds__(256) void copy_pages_kernel(Copies C) {
   copy_pages(C, blockIdx.x, gridDim.x);
 }
 
-// A thread a 16-byte piece of a token. The new values are read beside the row's length and table.
-__global__ __launch_bounds__(256) void append_kernel(Pages P, uint16_t* k, uint16_t* v,
+// A thread a 16-byte piece of a token. The new values and `lacking` are read beside the row's length
+// and table.
+__global__ __launch_bounds__(256) void append_kernel(Pages P, const int32_t* lacking, uint16_t* k,
+                                                     uint16_t* v,
                                                      const uint16_t* __restrict__ k_new,
                                                      const uint16_t* __restrict__ v_new,
                                                      int64_t ld_new, const int32_t* seq, int N,
@@ -306,8 +309,9 @@ __global__ __launch_bounds__(256) void append_kernel(Pages P, uint16_t* k, uint1
   const int e = token / (unsigned)B, b = token % (unsigned)B;
   const uint4 x = *reinterpret_cast<const uint4*>((blockIdx.y ? v_new : k_new) +
                                                   (int64_t)token * ld_new + piece * 8);
+  const int no = lacking ? *lacking : 0;
   const int r = row_of(seq, e, P.rows);
-  if (r < 0) return;
+  if (r < 0 || no) return;
   const int pos = in_sight(clamp_len(P.len[r], P.ld, P.shift), B, b) - 1;
   if (pos < 0) return;
   const int id = P.table[(int64_t)r * P.ld + (pos >> P.shift)];
@@ -435,22 +439,22 @@ hipError_t launch_cache_extend(const xpress_cache& c, const int32_t* seq, int N,
   return hipGetLastError();
 }
 
-hipError_t launch_cache_append(const xpress_cache& c, int layer, const void* k_new,
-                               const void* v_new, int64_t ld_new, const int32_t* seq, int N, int B,
-                               hipStream_t s) {
+hipError_t launch_cache_append(const xpress_cache& c, const int32_t* lacking, int layer,
+                               const void* k_new, const void* v_new, int64_t ld_new,
+                               const int32_t* seq, int N, int B, hipStream_t s) {
   const int64_t n = (int64_t)N * B * (c.Hkv * c.D / 8);
   const int64_t layer_elems = (int64_t)c.n_pages * c.Hkv * c.page * c.D;
   hipLaunchKernelGGL(append_kernel, dim3((unsigned)((n + 255) / 256), 2), dim3(256), 0, s,
-                     pages(c), static_cast<uint16_t*>(c.k) + layer * layer_elems,
+                     pages(c), lacking, static_cast<uint16_t*>(c.k) + layer * layer_elems,
                      static_cast<uint16_t*>(c.v) + layer * layer_elems,
                      static_cast<const uint16_t*>(k_new), static_cast<const uint16_t*>(v_new),
                      ld_new, seq, N, B, c.Hkv, c.D);
   return hipGetLastError();
 }
 
-hipError_t launch_cache_trim(const xpress_cache& c, const int32_t* seq, int N, const int32_t* drop,
-                             hipStream_t s) {
-  hipLaunchKernelGGL(trim_kernel, dim3(N), dim3(256), 0, s, pages(c), seq, drop);
+hipError_t launch_cache_trim(const xpress_cache& c, const int32_t* lacking, const int32_t* seq, int N,
+                             const int32_t* drop, hipStream_t s) {
+  hipLaunchKernelGGL(trim_kernel, dim3(N), dim3(256), 0, s, pages(c), lacking, seq, drop);
   return hipGetLastError();
 }
 

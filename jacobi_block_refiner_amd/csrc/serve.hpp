@@ -16,11 +16,11 @@ hipError_t launch_cache_fork(const xpress_cache& c, const int32_t* src, const in
 hipError_t launch_cache_extend(const xpress_cache& c, const int32_t* seq, int N,
                                const int32_t* add, int add_all, int32_t* lacking, void* ws,
                                hipStream_t s);
-hipError_t launch_cache_append(const xpress_cache& c, int layer, const void* k_new,
-                               const void* v_new, int64_t ld_new, const int32_t* seq, int N, int B,
-                               hipStream_t s);
-hipError_t launch_cache_trim(const xpress_cache& c, const int32_t* seq, int N, const int32_t* drop,
-                             hipStream_t s);
+hipError_t launch_cache_append(const xpress_cache& c, const int32_t* lacking, int layer,
+                               const void* k_new, const void* v_new, int64_t ld_new,
+                               const int32_t* seq, int N, int B, hipStream_t s);
+hipError_t launch_cache_trim(const xpress_cache& c, const int32_t* lacking, const int32_t* seq, int N,
+                             const int32_t* drop, hipStream_t s);
 hipError_t launch_cache_compact(const xpress_cache& c, int32_t* live, void* ws, hipStream_t s);
 
 size_t attention_scratch_bytes(const xpress_cache& c, int N, int B, int Hq);

@@ -142,9 +142,10 @@ xpress_status xpress_cache_extend(const xpress_cache* c, const int32_t* seq, int
   return XPRESS_OK;
 }
 
-xpress_status xpress_cache_append(const xpress_cache* c, int32_t layer, const void* k_new,
-                                  const void* v_new, int64_t ld_new, const int32_t* seq, int32_t N,
-                                  int32_t B, xpress_stream stream) {
+xpress_status xpress_cache_append_if(const xpress_cache* c, const int32_t* lacking, int32_t layer,
+                                     const void* k_new, const void* v_new, int64_t ld_new,
+                                     const int32_t* seq, int32_t N, int32_t B,
+                                     xpress_stream stream) {
   xpress_status st = check_cache(c, true, true);
   if (st != XPRESS_OK) return st;
   st = check_rows(c, seq, N);
@@ -157,25 +158,38 @@ xpress_status xpress_cache_append(const xpress_cache* c, int32_t layer, const vo
   if (ld_new < (int64_t)c->Hkv * c->D || ld_new % 8)
     return fail(XPRESS_ERR_ARG, "ld_new=%lld must be >= Hkv*D=%d and a multiple of 8",
                 (long long)ld_new, c->Hkv * c->D);
+  XP_WORDS_OR_NULL(lacking);
   if (N == 0 || B == 0) return XPRESS_OK;
   XP_PTR(k_new);
   XP_PTR(v_new);
-  XP_TRY(xpress::launch_cache_append(*c, layer, k_new, v_new, ld_new, seq, N, B,
+  XP_TRY(xpress::launch_cache_append(*c, lacking, layer, k_new, v_new, ld_new, seq, N, B,
                                      hip_stream(stream)),
          "cache append");
   return XPRESS_OK;
 }
 
-xpress_status xpress_cache_trim(const xpress_cache* c, const int32_t* seq, int32_t N,
-                                const int32_t* drop, xpress_stream stream) {
+xpress_status xpress_cache_append(const xpress_cache* c, int32_t layer, const void* k_new,
+                                  const void* v_new, int64_t ld_new, const int32_t* seq, int32_t N,
+                                  int32_t B, xpress_stream stream) {
+  return xpress_cache_append_if(c, nullptr, layer, k_new, v_new, ld_new, seq, N, B, stream);
+}
+
+xpress_status xpress_cache_trim_if(const xpress_cache* c, const int32_t* lacking, const int32_t* seq,
+                                   int32_t N, const int32_t* drop, xpress_stream stream) {
   xpress_status st = check_cache(c, false, true);
   if (st != XPRESS_OK) return st;
   st = check_rows(c, seq, N);
   if (st != XPRESS_OK) return st;
+  XP_WORDS_OR_NULL(lacking);
   if (N == 0) return XPRESS_OK;
   XP_WORDS_OR_NULL(drop);
-  XP_TRY(xpress::launch_cache_trim(*c, seq, N, drop, hip_stream(stream)), "cache trim");
+  XP_TRY(xpress::launch_cache_trim(*c, lacking, seq, N, drop, hip_stream(stream)), "cache trim");
   return XPRESS_OK;
+}
+
+xpress_status xpress_cache_trim(const xpress_cache* c, const int32_t* seq, int32_t N,
+                                const int32_t* drop, xpress_stream stream) {
+  return xpress_cache_trim_if(c, nullptr, seq, N, drop, stream);
 }
 
 xpress_status xpress_cache_compact(const xpress_cache* c, int32_t* live, void* ws, size_t ws_bytes,

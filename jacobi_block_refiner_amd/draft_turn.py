@@ -4,8 +4,9 @@ A small random target model (its dense products are plain torch) keeps its K and
 The prompt is run once and forked to every sample; then each turn drafts a block with the refiner,
 runs the target over the block and keeps what the target confirms:
 
-    xpress_jacobi_step -> xpress_cache_extend -> (xpress_cache_append, xpress_block_attention) a layer
-    -> xpress_verify_draft -> xpress_cache_trim
+    xpress_jacobi_step -> xpress_cache_extend
+    -> (xpress_cache_append_if, xpress_block_attention) a layer
+    -> xpress_verify_draft -> xpress_cache_trim_if
 
 At the end all samples but one are freed and the pool is compacted.
 
@@ -105,7 +106,7 @@ class Decoder:
         at = (end[:, None] - B + torch.arange(B, device=end.device)).reshape(-1)
 
         def attend(layer, q, k, v):
-            xpress.cache_append(self.cache, layer, k, v, N=N, B=B)
+            xpress.cache_append(self.cache, layer, k, v, N=N, B=B, lacking=self.lacking)
             return xpress.block_attention(self.cache, layer, q, N=N, B=B, Hq=self.target.Hq,
                                           shared=self.shared, out=torch.empty(
                                               q.shape, dtype=q.dtype, device=q.device),
@@ -123,13 +124,15 @@ class Decoder:
         self._check_room()
         rows = torch.arange(N, dtype=torch.int32, device=ids.device)
         xpress.cache_fork(self.cache, torch.zeros_like(rows[1:]), rows[1:])
-        self.shared = P
+        self.shared = self.reach = P
         self.anchor, self.am1 = ids[-1].repeat(N), ids[-2].repeat(N)
         # the refiner's view of the slots to come: the last state and logits, over the block
         self.h = h[-1].repeat(N, B, 1)
         self.base = logits[-1].repeat(N * (B - 1), 1)
 
     def turn(self) -> Turn:
+        """One turn of all samples. Raises where a row's table is full; the cache and the anchors are
+        then as they were."""
         N, B, V = self.N, self.B, self.target.V
         xpress.jacobi_step(self.refiner, self.h, self.base, self.anchor, self.am1, self.blk, K=B,
                            flags=xpress.INIT_FROM_BASE | xpress.STOP_AT_FIXED_POINT, ws=self.step_ws)
@@ -137,7 +140,11 @@ class Decoder:
         u = torch.rand(N, B, device=h.device, generator=self.rng)
         xpress.verify_draft(logits, self.blk, u=u, temperature=self.temperature, out=self.out,
                             accepted=self.accepted, drop=self.drop, ws=self.verify_ws)
-        xpress.cache_trim(self.cache, self.drop, N=N)
+        xpress.cache_trim(self.cache, self.drop, N=N, lacking=self.lacking)
+        # tokens of the longest row at most: the host waits for the card only where they might not fit
+        self.reach += B
+        if self.reach > self.cache.table.shape[1] * self.cache.k.shape[3]:
+            self._check_room()
         # the extra token is the next anchor; the state it was drawn from serves the next block
         a = self.accepted.to(torch.int64)[:, None]
         self.anchor, self.am1 = self.out.gather(1, a)[:, 0], self.blk.gather(1, a)[:, 0]
@@ -179,7 +186,6 @@ def main(argv=None) -> None:
     text = [[] for _ in range(a.samples)]
     for _ in range(a.turns):
         t = dec.turn()
-        dec._check_room()
         for row, new in zip(text, t.out.tolist()):
             row += [x for x in new if x >= 0]
     for i, row in enumerate(text):

@@ -96,7 +96,9 @@ def lib() -> ctypes.CDLL:
             "xpress_cache_fork": [C, P, P, i32, P],
             "xpress_cache_extend": [C, P, i32, P, i32, P, P, sz, P],
             "xpress_cache_append": [C, i32, P, P, i64, P, i32, i32, P],
+            "xpress_cache_append_if": [C, P, i32, P, P, i64, P, i32, i32, P],
             "xpress_cache_trim": [C, P, i32, P, P],
+            "xpress_cache_trim_if": [C, P, P, i32, P, P],
             "xpress_cache_compact": [C, P, P, sz, P],
             "xpress_attention_workspace_size": [C, i32, i32, i32, ctypes.POINTER(sz)],
             "xpress_block_attention": [C, i32, P, i64, P, i32, i32, i32, f32, i32, P, i64, P, P,
@@ -530,22 +532,27 @@ def cache_extend(cache: Cache, add, *, lacking: torch.Tensor, ws: torch.Tensor, 
 
 
 def cache_append(cache: Cache, layer: int, k_new: torch.Tensor, v_new: torch.Tensor, *, B: int,
-                 seq=None, N: int | None = None) -> None:
+                 seq=None, N: int | None = None, lacking: torch.Tensor | None = None) -> None:
     """K and V of one layer for the last B tokens of each row; k_new, v_new: [N*B, Hkv*D] views
-    with the same row stride."""
+    with the same row stride. lacking (as ``cache_extend`` wrote it): nothing is written unless it
+    is 0."""
     N = cache._rows(seq, N)
     ld = _tokens(k_new, N * B, cache._width, cache._dtype, "k_new")
     if _tokens(v_new, N * B, cache._width, cache._dtype, "v_new") != ld:
         raise ValueError("k_new and v_new must have the same row stride")
-    _check(lib().xpress_cache_append(cache._ref, layer, k_new.data_ptr(), v_new.data_ptr(), ld,
-                                     _list(seq, N, torch.int32, "seq"), N, B, _stream()))
+    _check(lib().xpress_cache_append_if(cache._ref, _list(lacking, 1, torch.int32, "lacking"), layer,
+                                        k_new.data_ptr(), v_new.data_ptr(), ld,
+                                        _list(seq, N, torch.int32, "seq"), N, B, _stream()))
 
 
-def cache_trim(cache: Cache, drop=None, *, seq=None, N: int | None = None) -> None:
-    """Row seq[i] loses its last drop[i] tokens (drop None: all of them)."""
+def cache_trim(cache: Cache, drop=None, *, seq=None, N: int | None = None,
+               lacking: torch.Tensor | None = None) -> None:
+    """Row seq[i] loses its last drop[i] tokens (drop None: all of them). lacking (as
+    ``cache_extend`` wrote it): nothing is freed unless it is 0."""
     N = cache._rows(seq, N)
-    _check(lib().xpress_cache_trim(cache._ref, _list(seq, N, torch.int32, "seq"), N,
-                                   _list(drop, N, torch.int32, "drop"), _stream()))
+    _check(lib().xpress_cache_trim_if(cache._ref, _list(lacking, 1, torch.int32, "lacking"),
+                                      _list(seq, N, torch.int32, "seq"), N,
+                                      _list(drop, N, torch.int32, "drop"), _stream()))
 
 
 def cache_compact(cache: Cache, *, live: torch.Tensor, ws: torch.Tensor) -> torch.Tensor:

@@ -339,3 +339,61 @@ def test_compaction_after_a_row_twice_in_a_list(twice, n_pages):
     xpress.cache_extend(c, 30, lacking=lacking, ws=ws, seq=i32([4]))
     assert int(lacking.item()) == 0 and int(length[4]) == 120
     assert table[4, 6:].tolist() == [n, n + 1] and ref[n:n + 3].tolist() == [1, 1, 0]
+
+
+@pytest.mark.parametrize("why", ["no pages", "a full row"])
+def test_a_turn_without_room_changes_nothing(why):
+    """Rows that share a prompt, one table or the pool too small for the next block: extension, append
+    and trim leave every row, count and page as it was, also captured and replayed, and the same
+    graph goes on once there is room."""
+    B, n_pages, ld = 6, 24, 6
+    o = CacheOracle(2, n_pages, 2, 16, 64, 4, ld, torch.bfloat16, 5)
+    o.extend([0], [40])
+    o.fork([0, 0], [1, 2])
+    o.extend([1, 2], [9, 13])
+    if why == "a full row":
+        o.extend([3], [ld * 16 - B + 1])
+    else:
+        o.ref[o.ref == 0] = 1  # held by rows that are not in the batch
+    c = device_cache(o)
+    ws = xpress.cache_workspace(c, 4)
+    lacking, drop = i32([0]), i32([2, 0, 5, 1])
+    new = torch.randn(4 * B, 2 * 2 * 64, device="cuda").to(torch.bfloat16)
+
+    def turn():
+        xpress.cache_extend(c, B, N=4, lacking=lacking, ws=ws)
+        for layer in range(2):
+            xpress.cache_append(c, layer, new[:, :128], new[:, 128:], N=4, B=B, lacking=lacking)
+        xpress.cache_trim(c, drop, N=4, lacking=lacking)
+
+    def state():
+        return [getattr(c, name).clone() for name in ("table", "length", "ref", "k", "v")]
+
+    before = state()
+    turn()
+    torch.cuda.synchronize()
+    assert (int(lacking.item()) < 0) == (why == "a full row") and int(lacking.item()) != 0
+    assert all(torch.equal(a, b) for a, b in zip(before, state()))
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        turn()
+    for _ in range(2):
+        graph.replay()
+        torch.cuda.synchronize()
+        assert int(lacking.item()) != 0
+        assert all(torch.equal(a, b) for a, b in zip(before, state()))
+    if why == "a full row":  # freed while lacking is not 0: the plain call
+        xpress.cache_trim(c, seq=i32([3]))
+        o.trim([3], None)
+    else:
+        held = [int(p) for r in range(4) for p in o.table[r, :o.pages(o.length[r])]]
+        o.ref[[p for p in range(n_pages) if p not in held]] = 0
+        c.ref.copy_(torch.from_numpy(o.ref))
+    graph.replay()
+    torch.cuda.synchronize()
+    assert int(lacking.item()) == o.extend(range(4), [B] * 4) == 0
+    for layer in range(2):
+        kv = new.cpu().view(-1, 2, 2, 64)
+        o.append(layer, kv[:, 0], kv[:, 1], range(4), B)
+    o.trim(range(4), drop.tolist())
+    same(c, o, "with room")

@@ -153,3 +153,28 @@ def test_the_command_runs(capsys):
     main(["--samples", "2", "--turns", "3", "--prompt", "40", "--greedy"])
     said = capsys.readouterr().out.splitlines()
     assert len(said) == 3 and said[0].startswith("sample 0:") and said[-1].startswith("pages after")
+
+
+def test_a_decoder_whose_table_is_full():
+    """Turns past the decoder's tokens: the turn that finds no room raises and leaves the cache and the
+    anchors as they were."""
+    inp = synth.make_inputs(1).rounded_bf16()
+    target = Target(inp.wl.V, inp.wl.H, most=64)
+    dec = Decoder(target, upload.weights(inp), 3, page=16, most=30, temperature=0.0)
+    dec.prompt(torch.randint(inp.wl.V, (25,), generator=torch.Generator().manual_seed(5)).cuda())
+
+    def state():
+        c = dec.cache
+        return [x.clone() for x in (c.table, c.length, c.ref, c.k.view(torch.int16),
+                                    c.v.view(torch.int16), dec.anchor, dec.am1, dec.h, dec.base)]
+
+    with pytest.raises(RuntimeError, match="table is full"):
+        for _ in range(40):
+            before = state()
+            dec.turn()
+    assert all(torch.equal(a, b) for a, b in zip(before, state()))
+    room = dec.cache.table.shape[1] * 16
+    assert room - dec.B < int(dec.cache.length.max()) <= room
+    with pytest.raises(RuntimeError, match="table is full"):
+        dec.turn()
+    assert all(torch.equal(a, b) for a, b in zip(before, state()))

@@ -348,3 +348,15 @@ def test_a_compaction_has_a_place_for_every_page_it_moves(tmp_path):
                     f"-I{build.CSRC}", str(src), "-o", str(exe)], check=True)
     got = subprocess.run([str(exe)], capture_output=True, text=True)
     assert got.returncode == 0, (got.returncode, got.stdout)
+
+
+def test_conditional_cache_calls_check_their_arguments():
+    c = cache()
+    says(L().xpress_cache_append_if(c, ODD2, 0, FAKE, FAKE, 1024, None, 4, 16, None), b"lacking")
+    says(L().xpress_cache_append_if(c, FAKE, 2, FAKE, FAKE, 1024, None, 4, 16, None), b"layer")
+    says(L().xpress_cache_append_if(c, FAKE, 0, ODD8, FAKE, 1024, None, 4, 16, None), b"k_new")
+    says(L().xpress_cache_trim_if(c, ODD2, None, 4, None, None), b"lacking")
+    says(L().xpress_cache_trim_if(c, FAKE, ODD2, 4, None, None), b"seq")
+    says(L().xpress_cache_trim_if(c, FAKE, None, 17, None, None), b"rows")
+    assert L().xpress_cache_append_if(c, None, 0, FAKE, FAKE, 1024, None, 0, 16, None) == xpress.OK
+    assert L().xpress_cache_trim_if(c, FAKE, None, 0, None, None) == xpress.OK
