@@ -593,7 +593,12 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void atte
   if (!valid) return;
   const int64_t row = (int64_t)token * A.Hq + hq, rows = (int64_t)A.N * A.B * A.Hq;
   if (direct) {
-    // the shared items' parts of this row, from the launch before this one
+    // the shared items' parts of this row, from the launch before this one (0 times what a row that
+    // sees nothing here holds, tokens that it must not see among it, would be no number)
+    if (l == 0.f) {
+#pragma unroll
+      for (int dt = 0; dt < C::DT; ++dt) w.o[dt] = f32x16{};
+    }
     float m = l == 0.f ? -INFINITY : w.m * A.c;
     for (int s = 0; s < A.slots_sh; ++s) {
       const int64_t at = s * rows + row;

@@ -372,3 +372,30 @@ def test_a_first_request_that_ends_inside_the_prefix(lengths, B, G, D, page):
     rows = list(range(len(lengths)))[::-1]
     x.check(x.run(x.cache(), seq=torch.tensor(rows, dtype=torch.int32, device="cuda"), rows=rows),
             rows=rows, what="the other way round")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_a_first_query_that_sees_the_prefix_alone(bad, dtype):
+    """Many query rows, rows of prefix + B - 1 tokens: a block's first query sees the shared part and
+    nothing else, and the later tokens of its block, infinite or NaN, do not reach it (nor the queries
+    before them)."""
+    N, B = 16, 16
+    lengths = [79] * 8 + [79 + i for i in range(8)]  # 64 shared tokens
+    x = Case(lengths=lengths, shared=64, B=B, Hkv=1, G=8, D=128, page=16, dtype=dtype, seed=51)
+    assert len(lengths) * B * 8 >= 1536
+    for r, n in enumerate(lengths):
+        p = x.table[r, (n - 1) // 16]
+        x.v[0, p, :, (n - 1) % 16] = bad
+        x.k[0, p, :, (n - 1) % 16, :64] = bad
+    got = x.run(x.cache())
+    early = [t for t in range(N * B) if t % B != B - 1]
+    assert not bool(got[0][early].isnan().any())
+    out, lse, mass, size = attention(
+        torch.nan_to_num(x.k[0], 0, 0, 0), torch.nan_to_num(x.v[0], 0, 0, 0), x.table, lengths, 16,
+        x.q, range(N), B, x.Hq, 128 ** -0.5)
+    bound, lse_bound = attention_bounds(out, mass, size, max(lengths), 128, dtype)
+    assert bool(((got[0].double() - out).abs() <= bound)[early].all())
+    assert bool(((got[1].double() - lse).abs() <= lse_bound + lse.abs() * 2.0 ** -22)[early].all())
+    if math.isnan(bad):
+        assert bool(got[0][B - 1::B].isnan().all())
