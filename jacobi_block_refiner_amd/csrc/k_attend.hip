@@ -6,7 +6,7 @@
 // part (its K and V are read once per tile of 128 or 256 rows instead of once per request), tiles
 // over one request's rows for its own part. Each item runs the softmax in one pass over its keys with
 // a running maximum and sum; where a row has more than one item, they leave (sum of weighted values,
-// maximum, sum) in the workspace and merge_kernel joins them.
+// unit of the weights, sum) in the workspace and merge_kernel joins them.
 //
 // The shared part is cut to whole tiles of 64 keys; what is left of it goes with the requests' own.
 // A request whose queries do not all see the whole shared part (a short or an empty row) takes all
@@ -43,11 +43,12 @@ struct Args {
   uint16_t* out;
   float* lse;
   float* po;   // [slots, N*B, Hq, D]
-  float2* pml; // [slots, N*B, Hq]: maximum (log2 units), sum
+  float2* pml; // [slots, N*B, Hq]: log2 of the weights' unit, their sum in it
 };
 
-// Two weights rounded to the type (to nearest even) in one register: the matrix core takes them as
-// bf16 or fp16. Relative error half a step each, against the 32-bit sum of the unrounded weights.
+// Two weights rounded to the type (to nearest even) in one register: the matrix core takes 16-bit
+// operands at its full rate, while the sum of the weights and the sums of weighted values have 32 bits.
+// The rounding is off by half a step of each weight: as much again as that of the result itself.
 template <bool F16> __device__ __forceinline__ uint32_t pack2(float a, float b) {
   const f32x2 x = {a, b};
   return F16 ? __builtin_bit_cast(uint32_t, __builtin_convertvector(x, f16x2))
@@ -108,6 +109,12 @@ template <bool F16, int D, int KT> struct Core {
   static constexpr int KPC = 64 / CPR;        // keys of a 1 KiB copy
   static constexpr int SIDE = KT * CPR * 16;  // bytes of a K or V tile
   static constexpr int KH = KT / 32, KK = KT / 16, DT = D / 32, DS = D / 16;
+  // Weights are 2^kLift times those relative to the running maximum, which they pass by 2^8 at most
+  // (rise). fp16 has whole precision from 2^-14 to 2^16 only: without the factor a weight below 2^-14
+  // of the maximum lost bits and one below 2^-25 vanished, and 60,000 of them 17 nats under one key
+  // were off by 44%. With it steps are coarser from 2^-21 on and nothing is left from 2^-32 on: half a
+  // step of 2^21 such keys is 2^-11 of the row, the result's own rounding.
+  static constexpr float kLift = F16 ? 7.f : 0.f;
 
   char* lds;
   int lane, h, col;
@@ -149,6 +156,9 @@ template <bool F16, int D, int KT> struct Core {
       }
   }
 
+  // log2 of the weights' unit.
+  __device__ __forceinline__ float unit() const { return fmaf(m, c, -kLift); }
+
   // Keys t0.. of which this lane's query sees those below vis.
   __device__ __forceinline__ void mask(int t0, int vis) {
 #pragma unroll
@@ -159,8 +169,8 @@ template <bool F16, int D, int KT> struct Core {
   }
 
   // Takes the tile's maximum in. The sums are rescaled only when some row's maximum grew by more than
-  // 2^8 in weight: weights stay below 2^8, which 32-bit sums and the rounded weights' relative
-  // precision do not feel.
+  // 2^8 in weight: weights relative to it stay below 2^8, which 32-bit sums and the rounded weights'
+  // relative precision do not feel.
   __device__ __forceinline__ void rise() {
     float top = s[0][0];
 #pragma unroll
@@ -180,7 +190,7 @@ template <bool F16, int D, int KT> struct Core {
   }
 
   __device__ __forceinline__ void weights() {
-    const float mc = -m * c;
+    const float mc = -unit();
     float sum[4] = {l, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
@@ -599,7 +609,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void atte
 #pragma unroll
       for (int dt = 0; dt < C::DT; ++dt) w.o[dt] = f32x16{};
     }
-    float m = l == 0.f ? -INFINITY : w.m * A.c;
+    float m = l == 0.f ? -INFINITY : w.unit();
     for (int s = 0; s < A.slots_sh; ++s) {
       const int64_t at = s * rows + row;
       const float2 ml = A.pml[at];
@@ -644,7 +654,7 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void atte
     for (int i = 0; i < 4; ++i)
       *reinterpret_cast<float4*>(op + dt * 32 + 8 * i) =
           make_float4(w.o[dt][4 * i], w.o[dt][4 * i + 1], w.o[dt][4 * i + 2], w.o[dt][4 * i + 3]);
-  if (h == 0) A.pml[at] = make_float2(w.m * A.c, l);
+  if (h == 0) A.pml[at] = make_float2(w.unit(), l);
 }
 
 // Joins a row's items: weights relative to the largest maximum. J groups of threads take every J-th

@@ -399,3 +399,50 @@ def test_a_first_query_that_sees_the_prefix_alone(bad, dtype):
     assert bool(((got[1].double() - lse).abs() <= lse_bound + lse.abs() * 2.0 ** -22)[early].all())
     if math.isnan(bad):
         assert bool(got[0][B - 1::B].isnan().all())
+
+
+@pytest.mark.parametrize("gap", [9.0, 12.3, 17.0, 18.0])
+@pytest.mark.parametrize("D,N,B,G,lengths,shared", [
+    (64, 1, 1, 1, [60000], 0), (128, 1, 2, 2, [60000], 0), (256, 1, 1, 2, [60000], 0),
+    (128, 2, 64, 12, [30000, 30040], 29000),  # wide items
+    (64, 3, 2, 2, [40000, 39000, 100], 30000)])
+def test_a_key_far_ahead_of_many_others(D, N, B, G, lengths, shared, gap):
+    """fp16: one key's weight is e^gap times each of the others', and its value is 0 where theirs are 1:
+    what many small weights add up to is kept."""
+    page, Hq = 64, G
+    scale = D ** -0.5
+    most = max(lengths)
+    pages = -(-most // page)
+    g = torch.Generator().manual_seed(9)
+    # a query's first component is 8: the keys' first component alone makes the scores
+    k = torch.zeros(1, pages, 1, page, D)
+    k[..., 0] = (torch.rand(1, pages, 1, page, generator=g) * 0.02).half().float()
+    k[0, 0, 0, 0, 0] = gap / scale / 8
+    v = torch.ones(1, pages, 1, page, D)
+    v[..., 1::2] = 1 + 0.25 * torch.rand(1, pages, 1, page, D // 2, generator=g)
+    v[0, 0, 0, 0] = 0
+    k, v = k.half(), v.half()
+    q = torch.zeros(N * B, Hq * D)
+    q[:, ::D] = 8
+    q = q.half()
+    table = np.tile(np.arange(pages, dtype=np.int32), (N, 1))  # the rows' own tokens are the same too
+    c = xpress.Cache(k=k.cuda(), v=v.cuda(), table=torch.from_numpy(table).cuda(),
+                     length=torch.tensor(lengths, dtype=torch.int32, device="cuda"),
+                     ref=torch.full((pages,), N, dtype=torch.int32, device="cuda"))
+    out = torch.empty(N * B, Hq * D, dtype=torch.float16, device="cuda")
+    lse = torch.empty(N * B, Hq, device="cuda")
+    xpress.block_attention(c, 0, q.cuda(), B=B, Hq=Hq, N=N, out=out, lse=lse, shared=shared,
+                           ws=xpress.attention_workspace(c, N, B, Hq))
+    # all heads and most queries see nearly the same: the definition for one head of each row's ends
+    for i, n in enumerate(lengths):
+        for b in {0, B - 1}:
+            want, wl, mass, size = attention(k[0], v[0], table, [n - (B - 1 - b)] * N, page,
+                                             q[:1, :D], [i], 1, 1, scale)
+            bound, lse_bound = attention_bounds(want, mass, size, most, D, torch.float16)
+            t = i * B + b
+            got = out[t].cpu().double().view(Hq, D)
+            worst = float(((got - want[0]).abs() / bound[0]).max())
+            log(f"  far ahead D {D} gap {gap} row {i} query {b}: {worst:.3f} of the bound")
+            assert worst <= 1, (i, b)
+            assert float((lse[t].cpu().double() - wl[0]).abs().max()) <= float(
+                (lse_bound + wl.abs() * 2.0 ** -22).max())
