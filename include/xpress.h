@@ -343,7 +343,7 @@ xpress_status xpress_cache_fork(const xpress_cache* c, const int32_t* src, const
  * of its own for it first, with a copy of the old one (all layers, K and V); then pages for the
  * new tokens. Pages are taken in ascending id order among those with ref = 0 when the call
  * starts, rows in list order. *lacking (device, written): 0, or the number of pages that are
- * missing, or -1 where a row would pass table_ld pages; in both latter cases nothing is changed,
+ * missing (2^31 - 1 at most), or -1 where a row would pass table_ld pages; in both latter cases nothing is changed,
  * and the tokens that room was asked for must not be written or trimmed: they would be the rows' own
  * last tokens, in pages that other rows may share. xpress_cache_append_if and xpress_cache_trim_if
  * see to that on the device, so that a turn need not wait for *lacking; whoever reads the turn's

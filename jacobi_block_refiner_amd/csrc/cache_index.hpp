@@ -35,6 +35,13 @@ XP_HD bool page_ok(int id, int n_pages) { return id >= 0 && id < n_pages; }
 // leave a count below 0: nobody holds such a page.
 XP_HD int holders(int ref) { return ref > 0 ? ref : 0; }
 
+// What an extension says of `total` pages wanted (up to 2^40) and `found` free ones: the pages that are
+// missing, as far as an int holds them.
+XP_HD int pages_missing(int64_t total, int64_t found) {
+  const int64_t n = total > found ? total - found : 0;
+  return (int)(n < INT32_MAX ? n : INT32_MAX);
+}
+
 // The two sides of a compaction to `live` pages (those with holders): a page that moves out of the
 // pool's rest, and a free one of the front that takes it in. There are as many of one side as of the
 // other, since all live pages fit in the front.

@@ -228,7 +228,7 @@ __global__ __launch_bounds__(kPlan) void extend_kernel(Pages P, const int32_t* s
     }
   const bool no = s_over || found < total;
   if (t == 0) {
-    *lacking = s_over ? -1 : found < total ? (int)(total - found) : 0;
+    *lacking = s_over ? -1 : pages_missing(total, found);
     *S.ncopy = no ? 0 : N;
   }
   if (no) return;

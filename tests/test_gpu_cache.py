@@ -397,3 +397,20 @@ def test_a_turn_without_room_changes_nothing(why):
         o.append(layer, kv[:, 0], kv[:, 1], range(4), B)
     o.trim(range(4), drop.tolist())
     same(c, o, "with room")
+
+
+def test_more_missing_pages_than_32_bits_hold():
+    """4096 rows that ask for 2^20 pages each, in a pool without any: 2^32 pages are missing, not none."""
+    rows, ld = 4096, 1 << 20
+    c = xpress.Cache.empty(1, 8, 1, 16, 64, rows=rows, table_ld=ld)  # a table of 17 GB
+    log("extension by 2^32 pages")
+    c.ref.fill_(1)
+    ws, lacking = xpress.cache_workspace(c, rows), i32([9])
+    xpress.cache_extend(c, ld * 16, lacking=lacking, ws=ws)
+    assert int(lacking.item()) == 2 ** 31 - 1
+    xpress.cache_extend(c, 3 * 16, lacking=lacking, ws=ws)
+    assert int(lacking.item()) == 3 * rows
+    assert bool((c.length == 0).all()) and c.ref.tolist() == [1] * 8
+    assert all(bool((part == -1).all()) for part in c.table.split(512))
+    del c
+    torch.cuda.empty_cache()

@@ -360,3 +360,26 @@ def test_conditional_cache_calls_check_their_arguments():
     says(L().xpress_cache_trim_if(c, FAKE, None, 17, None, None), b"rows")
     assert L().xpress_cache_append_if(c, None, 0, FAKE, FAKE, 1024, None, 0, 16, None) == xpress.OK
     assert L().xpress_cache_trim_if(c, FAKE, None, 0, None, None) == xpress.OK
+
+
+MISSING = r"""
+#include "cache_index.hpp"
+#include <initializer_list>
+using namespace xpress;
+int main() {
+  for (int64_t found : {0LL, 1LL, 1LL << 24})
+    for (int64_t more : {0LL, 1LL, (1LL << 31) - 1, 1LL << 31, 1LL << 32, 3LL << 32, 1LL << 40})
+      if (pages_missing(found + more, found) != (more < INT32_MAX ? (int)more : INT32_MAX)) return 1;
+  return pages_missing(3, 5) == 0 ? 0 : 2;
+}
+"""
+
+
+def test_missing_pages_past_32_bits(tmp_path):
+    """2^20 rows may ask for 2^20 pages each: the number that is missing does not wrap round to 0."""
+    src = tmp_path / "missing.cpp"
+    src.write_text(MISSING)
+    exe = tmp_path / "missing"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover",
+                    f"-I{build.CSRC}", str(src), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)]).returncode == 0
