@@ -172,12 +172,16 @@ __device__ __forceinline__ Part get(const Part* at) {
 // Counts a chunk in, after its stores: they go through the caches to the card's point of coherence,
 // and the wait is for their acknowledgement. (A release at the card's scope also writes back the
 // whole L2 of the XCD and an acquire empties it, once a chunk: 278 against 74 us at 512 rows of
-// 151,936 ids.) Returns how many were in before.
+// 151,936 ids.) Returns how many were in before. What the last chunk then reads with get() must not be
+// read before the add has returned: the branch on its result keeps the loads behind it on the card,
+// and the compiler, which may move relaxed loads above a relaxed add, is kept from it here.
 __device__ __forceinline__ int count_in(int32_t* counter) {
   asm volatile("" ::: "memory");
   __builtin_amdgcn_s_waitcnt(0x0F70);  // vmcnt(0)
   asm volatile("" ::: "memory");
-  return __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  const int before = __hip_atomic_fetch_add(counter, 1, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+  asm volatile("" ::: "memory");
+  return before;
 }
 __device__ __forceinline__ void put(double* at, double v) {
   __hip_atomic_store(reinterpret_cast<uint64_t*>(at), (uint64_t)__double_as_longlong(v),
