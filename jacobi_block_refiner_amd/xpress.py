@@ -131,9 +131,15 @@ def _ptr(t: torch.Tensor | None):
     return ctypes.c_void_p(t.data_ptr())
 
 
-def _stream():
-    # the handle alone: building torch's Stream object around it takes 2.9 us, this 0.3
-    return torch._C._cuda_getCurrentRawStream(torch.cuda.current_device())
+# The current stream's handle alone: building torch's Stream object around it takes 2.9 us, this 0.3.
+# It is no public function, so a torch without it takes the object.
+_raw_stream = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+
+
+def _stream() -> int:
+    if _raw_stream is None:
+        return torch.cuda.current_stream().cuda_stream
+    return _raw_stream(torch.cuda.current_device())
 
 
 def _bf16(t: torch.Tensor, name: str) -> torch.Tensor:

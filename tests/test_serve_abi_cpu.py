@@ -2,6 +2,7 @@
 is launched by any call here), and the cache's index arithmetic is right at its limits."""
 import ctypes
 import subprocess
+import sys
 from pathlib import Path
 
 import numpy as np
@@ -383,3 +384,20 @@ def test_missing_pages_past_32_bits(tmp_path):
     subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover",
                     f"-I{build.CSRC}", str(src), "-o", str(exe)], check=True)
     assert subprocess.run([str(exe)]).returncode == 0
+
+
+def test_the_stream_of_a_torch_without_the_raw_handle():
+    """The binding loads and takes the public call's stream where torch lacks the function that gives
+    the handle alone."""
+    code = """
+import torch
+from types import SimpleNamespace
+if hasattr(torch._C, "_cuda_getCurrentRawStream"):
+    del torch._C._cuda_getCurrentRawStream
+torch.cuda.current_stream = lambda: SimpleNamespace(cuda_stream=123)
+from jacobi_block_refiner_amd import xpress
+assert xpress._stream() == 123
+"""
+    got = subprocess.run([sys.executable, "-c", code], cwd=Path(__file__).resolve().parents[1],
+                         capture_output=True, text=True)
+    assert got.returncode == 0, got.stderr
