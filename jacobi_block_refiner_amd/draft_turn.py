@@ -83,8 +83,9 @@ class Decoder:
         dev = target.embed.device
         N, B, V = self.N, self.B, target.V
         ld = -(-(most + B) // page)
-        self.cache = xpress.Cache.empty(len(target.layers), ld * N, target.Hkv, page, target.D, N, ld,
-                                        device=dev)
+        # every row's table full, and the prompt's last page while every sample copies it
+        self.cache = xpress.Cache.empty(len(target.layers), ld * N + 1, target.Hkv, page, target.D, N,
+                                        ld, device=dev)
         self.shared = 0
 
         def empty(*shape, dtype=torch.int32):

@@ -178,3 +178,17 @@ def test_a_decoder_whose_table_is_full():
     with pytest.raises(RuntimeError, match="table is full"):
         dec.turn()
     assert all(torch.equal(a, b) for a, b in zip(before, state()))
+
+
+def test_a_pool_with_room_for_every_table():
+    """Samples whose first block fits in the prompt's page: each copies it while it is still there."""
+    inp = synth.make_inputs(1).rounded_bf16()
+    B, N, prompt = inp.wl.B, 4, 3
+    target = Target(inp.wl.V, inp.wl.H, most=64)
+    dec = Decoder(target, upload.weights(inp), N, page=16, most=16 - B, temperature=0.0)
+    assert dec.cache.table.shape[1] == 1 and prompt - 1 + B <= 16
+    dec.prompt(torch.arange(prompt).cuda())
+    t = dec.turn()
+    assert int(dec.lacking.item()) == 0
+    assert (dec.cache.length == prompt + t.accepted).all() and dec.cache.ref.sum().item() == N
+    assert sorted(dec.cache.table.flatten().tolist()) == [1, 2, 3, 4] and int(dec.cache.ref[0]) == 0
