@@ -431,14 +431,15 @@ def _list(t, n: int, dtype, name: str):
 
 
 def _tokens(t, n: int, width: int, dtype, name: str) -> int:
-    """A [n, width] view with unit column stride; its row stride in elements."""
+    """A [n, width] view with unit column stride; its row stride in elements (of a single row, where
+    a view may have any: the width)."""
     if t.dtype != dtype or not t.is_cuda:
         raise TypeError(f"{name} must be a CUDA {dtype} tensor")
     shape = t.shape
     if len(shape) != 2 or shape[0] < n or shape[1] != width or (width > 1 and t.stride(1) != 1):
         raise ValueError(f"{name} is {tuple(shape)}; the call needs [{n}, {width}] rows with unit "
                          "column stride")
-    return t.stride(0) if shape[0] > 1 else max(t.stride(0), width)
+    return t.stride(0) if n > 1 else width
 
 
 def _ws(ws):

@@ -414,3 +414,19 @@ def test_more_missing_pages_than_32_bits_hold():
     assert all(bool((part == -1).all()) for part in c.table.split(512))
     del c
     torch.cuda.empty_cache()
+
+
+def test_a_single_token_of_any_row_stride():
+    """One row of one token: K of its own, V and q out of wider rows, whose strides mean nothing."""
+    c = xpress.Cache.empty(1, 2, 2, 16, 64, 1, 2)
+    ws, lacking = xpress.cache_workspace(c, 1), i32([9])
+    xpress.cache_extend(c, 1, lacking=lacking, ws=ws)
+    k = torch.randn(1, 128, device="cuda").to(torch.bfloat16)
+    v = torch.randn(1, 128 + 3, device="cuda").to(torch.bfloat16)[:, :128]
+    q = torch.randn(1, 256 + 5, device="cuda").to(torch.bfloat16)[:, :256]
+    xpress.cache_append(c, 0, k, v, B=1)
+    p = int(c.table[0, 0])
+    assert torch.equal(c.k[0, p, :, 0], k.view(2, 64)) and torch.equal(c.v[0, p, :, 0], v.view(2, 64))
+    out = torch.empty(1, 256 + 1, dtype=torch.bfloat16, device="cuda")[:, :256]
+    xpress.block_attention(c, 0, q, B=1, Hq=4, out=out, ws=xpress.attention_workspace(c, 1, 1, 4))
+    assert torch.equal(out.view(2, 2, 64), v.view(2, 1, 64).expand(2, 2, 64))
