@@ -120,6 +120,8 @@ class Decoder:
         sample."""
         N, B = self.N, self.B
         P = ids.numel() - 1
+        if P < 1:
+            raise ValueError("a prompt has two tokens at least: the anchor and the one before it")
         ws = xpress.attention_workspace(self.cache, 1, P, self.target.Hq)
         h, logits = self._run(ids[:-1], 1, P, ws)
         self._check_room()

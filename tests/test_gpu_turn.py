@@ -192,3 +192,15 @@ def test_a_pool_with_room_for_every_table():
     assert int(dec.lacking.item()) == 0
     assert (dec.cache.length == prompt + t.accepted).all() and dec.cache.ref.sum().item() == N
     assert sorted(dec.cache.table.flatten().tolist()) == [1, 2, 3, 4] and int(dec.cache.ref[0]) == 0
+
+
+def test_a_prompt_too_short_or_too_long():
+    inp = synth.make_inputs(1).rounded_bf16()
+    target = Target(inp.wl.V, inp.wl.H, most=64)
+    dec = Decoder(target, upload.weights(inp), 2, page=16, most=20)
+    for n in (0, 1):
+        with pytest.raises(ValueError, match="two tokens"):
+            dec.prompt(torch.zeros(n, dtype=torch.int64, device="cuda"))
+    with pytest.raises(RuntimeError, match="table is full"):
+        dec.prompt(torch.zeros(dec.cache.table.shape[1] * 16 + 2, dtype=torch.int64, device="cuda"))
+    assert not dec.cache.length.any() and not dec.cache.ref.any()
