@@ -123,6 +123,8 @@ template <bool F16, int D, int KT> struct Core {
   f32x16 s[KH], o[DT];
   s16x8 pf[KK];
   float m, l;
+  float shift;    // of the weights' exponents: 2^(s c + shift)
+  uint64_t huge;  // lanes whose unit is past kHuge
 
   __device__ static int k_swizzle(int key) { return D == 64 ? (key >> 1) & 7 : key & 15; }
   __device__ static int v_swizzle(int key) {
@@ -141,6 +143,7 @@ template <bool F16, int D, int KT> struct Core {
     for (int dt = 0; dt < DT; ++dt) o[dt] = f32x16{};
     m = -1e30f;
     l = 0.f;
+    huge = ~0ull;
   }
 
   // Scores of the K tile at byte kb.
@@ -156,6 +159,8 @@ template <bool F16, int D, int KT> struct Core {
       }
   }
 
+  static constexpr float kHuge = 0x1p20f;
+
   // log2 of the weights' unit.
   __device__ __forceinline__ float unit() const { return fmaf(m, c, -kLift); }
 
@@ -168,7 +173,11 @@ template <bool F16, int D, int KT> struct Core {
         s[kh][i] = t0 + kh * 32 + 8 * (i / 4) + 4 * h + i % 4 < vis ? s[kh][i] : -INFINITY;
   }
 
-  // Takes the tile's maximum in. The sums are rescaled only when some row's maximum grew by more than
+  // Takes the tile's maximum in.
+  // The exponents are s c - unit in one operation: the unit is rounded, but the weights are relative to
+  // what it was rounded to. Where half a step of it is no longer small beside the factor of 2 that
+  // fp16's range has left, the scores become s - m first.
+  // The sums are rescaled only when some row's maximum grew by more than
   // 2^8 in weight: weights relative to it stay below 2^8, which 32-bit sums and the rounded weights'
   // relative precision do not feel.
   __device__ __forceinline__ void rise() {
@@ -179,26 +188,32 @@ template <bool F16, int D, int KT> struct Core {
       for (int i = 0; i < 16; ++i) top = fmaxf(top, s[kh][i]);
     const float2 tops = both_halves(top);
     top = fmaxf(tops.x, tops.y);
-    if (__any((top - m) * c > 8.f)) {
+    if ((__ballot((top - m) * c > 8.f) | huge) != 0) {
       const float mn = fmaxf(m, top);
       const float alpha = __builtin_amdgcn_exp2f((m - mn) * c);
       l *= alpha;
 #pragma unroll
       for (int dt = 0; dt < DT; ++dt) o[dt] *= alpha;
       m = mn;
+      shift = -unit();
+      huge = __ballot(fabsf(shift) > kHuge);
+      if (huge != 0) {
+#pragma unroll
+        for (int kh = 0; kh < KH; ++kh) s[kh] -= m;
+        shift = kLift;
+      }
     }
   }
 
   __device__ __forceinline__ void weights() {
-    const float mc = -unit();
     float sum[4] = {l, 0.f, 0.f, 0.f};
 #pragma unroll
     for (int kk = 0; kk < KK; ++kk) {
       uint32_t w[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float a = __builtin_amdgcn_exp2f(fmaf(s[kk / 2][8 * (kk % 2) + 2 * j], c, mc));
-        const float b = __builtin_amdgcn_exp2f(fmaf(s[kk / 2][8 * (kk % 2) + 2 * j + 1], c, mc));
+        const float a = __builtin_amdgcn_exp2f(fmaf(s[kk / 2][8 * (kk % 2) + 2 * j], c, shift));
+        const float b = __builtin_amdgcn_exp2f(fmaf(s[kk / 2][8 * (kk % 2) + 2 * j + 1], c, shift));
         sum[j] += a + b;
         w[j] = pack2<F16>(a, b);
       }

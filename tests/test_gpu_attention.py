@@ -446,3 +446,76 @@ def test_a_key_far_ahead_of_many_others(D, N, B, G, lengths, shared, gap):
             assert worst <= 1, (i, b)
             assert float((lse[t].cpu().double() - wl[0]).abs().max()) <= float(
                 (lse_bound + wl.abs() * 2.0 ** -22).max())
+
+
+@pytest.mark.parametrize("D", [64, 128])
+def test_products_near_the_lowest_value(D):
+    """Rows whose only product q.k is -1e29 (a value like any other), and -1e32 (as masked)."""
+    c = xpress.Cache.empty(1, 4, 1, 16, D, 3, 2)
+    ws, lacking = xpress.cache_workspace(c, 3), torch.zeros(1, dtype=torch.int32, device="cuda")
+    xpress.cache_extend(c, 1, lacking=lacking, ws=ws)
+    q, k = torch.zeros(3, D, device="cuda"), torch.zeros(3, D, device="cuda")
+    v = torch.arange(3 * D, device="cuda").view(3, D).bfloat16()
+    q[:, 5] = torch.tensor([1e14, 1e16, 1.0])
+    k[:, 5] = torch.tensor([-1e15, -1e16, torch.finfo(torch.bfloat16).min])
+    xpress.cache_append(c, 0, k.bfloat16(), v, B=1)
+    out, lse = torch.full((3, D), 3.0, device="cuda").bfloat16(), torch.zeros(3, 1, device="cuda")
+    for scale in (D ** -0.5, 1.0):
+        xpress.block_attention(c, 0, q.bfloat16(), B=1, Hq=1, out=out, lse=lse, scale=scale,
+                               ws=xpress.attention_workspace(c, 3, 1, 1))
+        assert torch.equal(out[0], v[0]) and not out[1:].any()
+        assert lse[1:].flatten().tolist() == [-math.inf] * 2
+        want = -1e29 * scale  # (two bf16 roundings and two of the product)
+        assert abs(float(lse[0]) / want - 1) <= 2 * 2.0 ** -8 + 2.0 ** -20
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("D,N,B,G,own,shared", [(64, 2, 1, 1, 40, 0), (128, 3, 4, 2, 700, 0),
+                                                (256, 2, 3, 1, 100, 70), (128, 2, 16, 48, 90, 150)])
+@pytest.mark.parametrize("size", [1e3, 3e5, 1e7, 1e9, 1e11, 1e20, 1e28])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_scores_of_any_size(size, sign, D, N, B, G, own, shared, dtype):
+    """Products q.k of up to `size`, exact in 32 bits, hundreds apart or equal: the largest share all."""
+    if size > 65504.0 ** 2 * 0.9 and dtype == torch.float16:
+        pytest.skip("more than fp16's products reach")
+    page, keys = 16, shared + own
+    g = torch.Generator().manual_seed(3)
+    pages = -(-keys // page)
+    # eight bits each of q and k: the products are exact, their product with log2(e) is not
+    a = 129 / 128 * 2.0 ** math.floor(math.log2(size) / 2)
+    steps = torch.randint(1, 5, (pages * page,), generator=g).float()
+    if sign < 0:
+        steps = 5 - steps
+    steps += 11 / 32
+    k = torch.zeros(1, pages, 1, page, D)
+    k[0, :, 0, :, 3] = (sign * steps * 2.0 ** math.floor(math.log2(size / a / 5))).view(pages, page)
+    v = torch.randn(1, pages, 1, page, D, generator=g)
+    k, v = k.to(dtype), v.to(dtype)
+    q = torch.zeros(N * B, G * D)
+    q[:, 3::D] = a
+    assert bool(q.to(dtype).float().eq(q).all()) and float(k.float().abs().max()) * a <= size * 1.01
+    c = xpress.Cache(k=k.cuda(), v=v.cuda(),
+                     table=torch.arange(pages, dtype=torch.int32, device="cuda").repeat(N, 1),
+                     length=torch.full((N,), keys, dtype=torch.int32, device="cuda"),
+                     ref=torch.full((pages,), N, dtype=torch.int32, device="cuda"))
+    out = torch.empty(N * B, G * D, dtype=dtype, device="cuda")
+    lse = torch.empty(N * B, G, device="cuda")
+    xpress.block_attention(c, 0, q.to(dtype).cuda(), B=B, Hq=G, out=out, lse=lse, shared=shared,
+                           scale=1.0, ws=xpress.attention_workspace(c, N, B, G))
+    kk = k[0, :, 0, :, 3].double().flatten() * a
+    vv = v[0, :, 0].double().reshape(-1, D)
+    for b in range(B):
+        see = keys - B + b + 1
+        s = kk[:see]
+        p = torch.exp(s - s.max())
+        assert int((p > 1e-30).sum()) == int((p == 1).sum())
+        want = (p / p.sum()) @ vv[:see]
+        mass = (p / p.sum()) @ vv[:see].abs()
+        # the result's rounding, that of a common weight, 32-bit sums
+        half = torch.finfo(dtype).eps / 2
+        bound = half * want.abs() + mass * (half * (1 + half) + (keys + 8) * 2.0 ** -24) + 2.0 ** -24
+        rows = slice(b, None, B)
+        got = out.view(N * B, G, D)[rows].cpu().double()
+        assert bool(((got - want).abs() <= bound).all()), b
+        lw = float(s.max() + math.log(p.sum()))
+        assert bool(((lse[rows].cpu().double() - lw).abs() <= abs(lw) * 2.0 ** -22 + 2.0 ** -20).all()), b
