@@ -393,7 +393,8 @@ xpress_status xpress_cache_compact(const xpress_cache* c, int32_t* live, void* w
  * q: token i*B + b at element (i*B + b)*q_ld, [Hq, D] dense; out likewise with out_ld; both of the
  * cache's dtype, 16-byte aligned, strides multiples of 8. lse: [N*B, Hq] fp32, nullable, the
  * natural log of the sum of exp(scale * q.k). Hq a multiple of Hkv; B >= 1; N*B*Hq < 2^26;
- * 0 < scale <= 1e6; 0 <= shared <= table_ld*page. Scores below -1e30 / scale count as masked.
+ * 0 < scale <= 1e6; 0 <= shared <= table_ld*page. Products q.k below -1e30 - 90 / scale have no
+ * weight: a row that sees nothing else is as one that sees no token.
  * Values in masked places (beyond a row's end, in later tokens of the block) do not reach the
  * result, whatever they are. */
 xpress_status xpress_attention_workspace_size(const xpress_cache* c, int32_t n_max, int32_t B,
