@@ -296,8 +296,9 @@ xpress_status xpress_graph_destroy(void* graph);
  *   xpress_verify_draft                 which drafts stand, and the next token;
  *   xpress_cache_trim_if                gives back the refused drafts' tokens.
  * The conventions above hold (device pointers, stream order, nothing allocated, host-side argument
- * errors, N == 0 is a no-op). (The _if calls do nothing where the extension found no room.) Page tables, lengths and counts live on the device and are read when
- * the kernels run, so a captured turn follows them from replay to replay.
+ * errors, N == 0 is a no-op); the _if calls do nothing where the extension found no room. Page tables,
+ * lengths and counts live on the device and are read when the kernels run, so a captured turn follows
+ * them from replay to replay.
  * ------------------------------------------------------------------------------------------- */
 
 /* Element types of the tensors below that are passed as void*. */
@@ -343,9 +344,9 @@ xpress_status xpress_cache_fork(const xpress_cache* c, const int32_t* src, const
  * of its own for it first, with a copy of the old one (all layers, K and V); then pages for the
  * new tokens. Pages are taken in ascending id order among those with ref = 0 when the call
  * starts, rows in list order. *lacking (device, written): 0, or the number of pages that are
- * missing (2^31 - 1 at most), or -1 where a row would pass table_ld pages; in both latter cases nothing is changed,
- * and the tokens that room was asked for must not be written or trimmed: they would be the rows' own
- * last tokens, in pages that other rows may share. xpress_cache_append_if and xpress_cache_trim_if
+ * missing (2^31 - 1 at most), or -1 where a row would pass table_ld pages; in both latter cases
+ * nothing is changed, and the tokens that room was asked for must not be written or trimmed: they
+ * would be the rows' own last tokens, in pages that other rows may share. xpress_cache_append_if and xpress_cache_trim_if
  * see to that on the device, so that a turn need not wait for *lacking; whoever reads the turn's
  * tokens reads it beside them, and drops them where it is not 0. */
 xpress_status xpress_cache_extend(const xpress_cache* c, const int32_t* seq, int32_t N,
@@ -392,7 +393,9 @@ xpress_status xpress_cache_compact(const xpress_cache* c, int32_t* live, void* w
  * attending over each row alone. A query that sees no token gives 0 (and lse = -inf).
  * q: token i*B + b at element (i*B + b)*q_ld, [Hq, D] dense; out likewise with out_ld; both of the
  * cache's dtype, 16-byte aligned, strides multiples of 8. lse: [N*B, Hq] fp32, nullable, the
- * natural log of the sum of exp(scale * q.k). Hq a multiple of Hkv; B >= 1; N*B*Hq < 2^26;
+ * natural log of the sum of exp(scale * q.k). Scores, their maxima, exponentials and sums have 32 bits;
+ * the weights are rounded to the cache's type (16 bits) for the product with v, as the matrix core takes
+ * them, and the result once more. Hq a multiple of Hkv; B >= 1; N*B*Hq < 2^26;
  * 0 < scale <= 1e6; 0 <= shared <= table_ld*page. Products q.k below -1e30 - 90 / scale have no
  * weight: a row that sees nothing else is as one that sees no token.
  * Values in masked places (beyond a row's end, in later tokens of the block) do not reach the

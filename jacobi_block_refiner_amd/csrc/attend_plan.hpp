@@ -33,9 +33,9 @@ constexpr int kWideItems = 2048;  // wide items at most, unless one split a tile
 // Narrow items wanted where the rows alone give fewer: kItems without a shared part; with one, of the
 // shared part half of it at D 64 (three workgroups a CU) and a quarter else (two, one): more slots
 // cost their join (16 requests of 16 tokens x 4 heads, 4096 shared and 512 own keys, D 128: 47 us
-// with 512 items of the shared part, 42 with 256; 32 requests x 8 heads at D 64: 59 and 65), and of
-// the requests' own half of it, but a quarter at D 256 (32 requests decoding, D 128: 33 us with
-// 512, 38 with 256; 32 requests at D 256: 159 and 156).
+// with 512 items of the shared part, 42 with 256; 32 requests of 16 tokens x 32 heads at D 64, 8192
+// shared: 66 with 512, 82 with 256), and of the requests' own half of it, but a quarter at D 256 (32
+// requests decoding, D 128: 33 us with 512, 38 with 256; 32 requests at D 256: 159 and 156).
 constexpr int kItems = 1024;
 constexpr int kLeast = 128;  // keys of a split of one request's own at least,
 constexpr int kLeastShared = 256;  // and of the shared part (more splits cost the join: 41 -> 36 us)

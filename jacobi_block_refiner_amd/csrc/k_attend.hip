@@ -370,22 +370,23 @@ template <int N> __device__ __forceinline__ void feed() {
 // Narrow (NW = 4): for items that wait for HBM. Tiles are taken one after the other with one barrier
 // each; the workgroups of a CU (three at D 64, two at 128, one at 256) fill each other's waits. At D
 // 128 a tile is 16 KB, and two workgroups that ask three tiles ahead read faster than three that ask
-// two ahead: 256 requests decoding 1024 tokens 110 us (4.9 TB/s) and 136, 32 decoding behind 4096
-// shared ones 33 and 35. At D 64 three are faster (32 requests, 8192 shared tokens: 59 and 63 us).
+// two ahead: 256 requests decoding up to 1024 tokens each (8 heads, 4 queries each, 555 MB) 111 us (5.0
+// TB/s) and 136, 32 decoding behind 4096 shared ones 32 and 35. At D 64 three are faster (32 requests of
+// 16 tokens x 32 heads, 8192 shared tokens and up to 512 own: 66 and 70 us).
 //
 // Slim (NW = 2, D 256): items of a request's own keys alone, at most 64 query rows, where they fill
 // more than one round of the card. A narrow item at D 256 keeps a CU to itself (its registers, and 96
 // KB of tiles), and with one row of queries three of its four waves only copy; two slim ones share a
-// CU. 64 requests decoding 1024 tokens (8 heads, 4 queries each) 70 us and 105 narrow, 256 requests
-// 225 and 348. Beside shared items they would be a launch of their own: 168 and 100 us for 64
+// CU. 64 requests decoding up to 1024 tokens each (8 heads, 4 queries each) 73 us and 105 narrow, 256
+// requests 225 and 348. Beside shared items they would be a launch of their own: 168 and 100 us for 64
 // requests behind 4096 tokens, so there the narrow ones stay.
 //
 // Wide (NW = 8, one workgroup a CU): shared items that the matrix core bounds. The two waves of a SIMD
 // are half a tile apart: while one multiplies (scores of tile t, values of tile t-1) the other forms
 // weights, and after each such half they meet and change roles. A tile needs about as many cycles of
 // the matrix core as of the vector unit; with both waves in step, each unit waited for the other.
-// 20480 rows a head, 16384 keys, 8 heads: 1377 us, 1.0 PFLOP/s at 1.9 to 2.0 GHz (the power limit
-// takes the rest of 2.3), the matrix core busy 47% of the cycles; 2560 rows, 8192 keys: 106 us, 0.8
+// 20480 rows a head, 16384 keys, 8 heads: 1310 to 1400 us, 1.0 PFLOP/s at 1.9 to 2.0 GHz (the power
+// limit takes the rest of 2.3), the matrix core busy 47% of the cycles; 2560 rows, 8192 keys: 104 us, 0.8
 // PFLOP/s on 240 CUs.
 template <bool F16, int D, int NW, int KT>
 __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void attend_kernel(
