@@ -305,6 +305,10 @@ xpress_status xpress_graph_destroy(void* graph);
 #define XPRESS_BF16 0u
 #define XPRESS_F16 1u
 #define XPRESS_F32 2u
+/* Of a cache alone: tensors of bf16 or fp16 go in and come out, 4 bits a value and a scale of 8 bits
+ * for 32 values are held (the microscaling format MXFP4). */
+#define XPRESS_BF16_MX4 16u
+#define XPRESS_F16_MX4 17u
 
 /* A paged cache: a pool of pages of `page` tokens, and `rows` sequences. Sequence r holds len[r]
  * tokens; its token t is line t % page of page table[r*table_ld + t/page] (the same page id in
@@ -312,13 +316,27 @@ xpress_status xpress_graph_destroy(void* graph);
  * page p (0: the page is free). The caller owns every buffer and starts with ref = 0, len = 0 and
  * table = -1; the calls below keep them so.
  * Limits: 1 <= n_layers <= 2^16; 1 <= n_pages <= 2^24; page in {16, 32, 64, 128, 256}; 1 <= Hkv <=
- * 256; D in {64, 128, 256}; 1 <= rows <= 2^20; 1 <= table_ld <= 2^20; dtype XPRESS_BF16 or
- * XPRESS_F16; k and v 16-byte aligned, table, len and ref 4-byte aligned.
+ * 256; D in {64, 128, 256}; 1 <= rows <= 2^20; 1 <= table_ld <= 2^20; dtype XPRESS_BF16, _F16,
+ * _BF16_MX4 or _F16_MX4; k and v 16-byte aligned, table, len and ref 4-byte aligned.
  * Lists of rows (`seq`, `src`, `dst`) are int32 on the device. seq NULL means rows 0..N-1. A row
  * outside [0, rows) is skipped. A row twice in one list is the caller's error (the metadata is
  * then unspecified, counts below 0 among it, which count as 0; nothing outside the buffers is
  * touched, by that call or a later one). A page id outside [0, n_pages) in
- * the used part of a table is too: it is clamped where it is read and never counted. */
+ * the used part of a table is too: it is clamped where it is read and never counted.
+ *
+ * In 4 bits (_MX4) k and v are [n_layers, n_pages, Hkv, page/16, 17*D/2] bytes: 16 tokens of a page and
+ * head are a tile of 8*D bytes of codes, two values each, and D/2 of scales, one of 32 channels of a
+ * token. A value is one of 0, 0.5, 1, 1.5, 2, 3, 4, 6 (its code's low three bits; the fourth is its
+ * sign) times 2^(s - 127) with the scale s. In K channels 2c (low half) and 2c+1 of token t are byte
+ * t*D/2 + c, and the scale of channels 32g.. is byte t*D/32 + g of the scales; in V channels 32g + 2i
+ * and the next of token 4q + j are byte ((16q + i)*D/32 + g)*4 + j, and their scale is byte
+ * (q*D/32 + g)*4 + j of the scales.
+ * An append rounds each value to the nearest of its group's, ties to the even code. The group's scale
+ * is the power of two of which its largest magnitude is 3.5 to 7 times, but 2^-123 at least and 2^125
+ * at most (fp16: 2^-23 and 2^13), so what is held is a value of bf16 (fp16) itself. What is more than 6
+ * scales, infinities too, becomes 6; NaN becomes 0 (the codes have neither). Where a caller writes
+ * the bytes, scales beyond these limits are its error: results of rows that see them, or whose block
+ * holds them, are then unspecified. */
 typedef struct {
   int32_t n_layers, n_pages, page, Hkv, D;
   uint32_t dtype;
@@ -355,7 +373,7 @@ xpress_status xpress_cache_extend(const xpress_cache* c, const int32_t* seq, int
 
 /* Writes K and V of one layer for the last B tokens of each row: token b of list entry i goes to
  * position len[seq[i]] - B + b (skipped where that is negative). k_new, v_new: token i*B + b at
- * element (i*B + b)*ld_new, [Hkv, D] dense, the cache's dtype, 16-byte aligned, ld_new a multiple
+ * element (i*B + b)*ld_new, [Hkv, D] dense, the cache's type, 16-byte aligned, ld_new a multiple
  * of 8 and at least Hkv*D (so slices of a fused projection's output can be passed).
  * N*B*Hkv < 2^26.
  * _append_if: the same, unless *lacking (device, nullable), as an extension wrote it, is not 0 when
@@ -367,6 +385,16 @@ xpress_status xpress_cache_append_if(const xpress_cache* c, const int32_t* lacki
                                      const void* k_new, const void* v_new, int64_t ld_new,
                                      const int32_t* seq, int32_t N, int32_t B,
                                      xpress_stream stream);
+
+/* Reads back K and V of one layer: token b of list entry i is position first[i] + b of row seq[i], for
+ * b < B (first NULL: the row's last B tokens, as an append takes them); positions outside the row, and
+ * rows outside the cache, give 0. From 4 bits the values are those that are held, exactly.
+ * first: [N] int32 on the device, nullable. k_out, v_out: token i*B + b at element (i*B + b)*ld_out,
+ * [Hkv, D] dense, the cache's type, 16-byte aligned, ld_out a multiple of 8 and at least Hkv*D; they
+ * do not overlap. N*B*Hkv < 2^26. */
+xpress_status xpress_cache_read(const xpress_cache* c, int32_t layer, const int32_t* seq, int32_t N,
+                                const int32_t* first, int32_t B, void* k_out, void* v_out,
+                                int64_t ld_out, xpress_stream stream);
 
 /* Freeing: row seq[i] loses its last drop[i] tokens (clamped to [0, len]; drop NULL: all of them);
  * pages that hold none of its tokens any more leave its table and their counts go down.
@@ -392,7 +420,7 @@ xpress_status xpress_cache_compact(const xpress_cache* c, int32_t* live, void* w
  * all: the caller vouches that every row's first min(shared, len) tokens are the same. The result is that of
  * attending over each row alone. A query that sees no token gives 0 (and lse = -inf).
  * q: token i*B + b at element (i*B + b)*q_ld, [Hq, D] dense; out likewise with out_ld; both of the
- * cache's dtype, 16-byte aligned, strides multiples of 8. lse: [N*B, Hq] fp32, nullable, the
+ * cache's type, 16-byte aligned, strides multiples of 8. lse: [N*B, Hq] fp32, nullable, the
  * natural log of the sum of exp(scale * q.k). Scores, their maxima, exponentials and sums have 32 bits;
  * the weights are rounded to the cache's type (16 bits) for the product with v, as the matrix core takes
  * them, and the result once more. Hq a multiple of Hkv; B >= 1; N*B*Hq < 2^26;

@@ -405,7 +405,7 @@ __global__ __launch_bounds__(256) void compact_move_kernel(Pages P, const int32_
 
 Copies copies(const xpress_cache& c, const int32_t* count, const int32_t* from, const int32_t* to) {
   return Copies{count, from, to, static_cast<u32x4*>(c.k), static_cast<u32x4*>(c.v), c.n_layers,
-                c.n_pages, (int64_t)c.Hkv * c.page * c.D * 2 / 16};
+                c.n_pages, cache_page_bytes(c) / 16};
 }
 // Workgroups for `most` page copies.
 unsigned copy_grid(const xpress_cache& c, int64_t most) {
@@ -442,6 +442,8 @@ hipError_t launch_cache_extend(const xpress_cache& c, const int32_t* seq, int N,
 hipError_t launch_cache_append(const xpress_cache& c, const int32_t* lacking, int layer,
                                const void* k_new, const void* v_new, int64_t ld_new,
                                const int32_t* seq, int N, int B, hipStream_t s) {
+  if (cache_in_4_bits(c))
+    return launch_cache_append4(c, lacking, layer, k_new, v_new, ld_new, seq, N, B, s);
   const int64_t n = (int64_t)N * B * (c.Hkv * c.D / 8);
   const int64_t layer_elems = (int64_t)c.n_pages * c.Hkv * c.page * c.D;
   hipLaunchKernelGGL(append_kernel, dim3((unsigned)((n + 255) / 256), 2), dim3(256), 0, s,

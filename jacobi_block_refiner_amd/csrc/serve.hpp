@@ -10,6 +10,14 @@
 
 namespace xpress {
 
+// The type of the tensors that go into a cache and come out of it; whether it holds them in 4 bits;
+// bytes of a page of one layer of K or V.
+inline uint32_t value_type(const xpress_cache& c) { return c.dtype & 15u; }
+inline bool cache_in_4_bits(const xpress_cache& c) { return c.dtype > 15u; }
+inline int64_t cache_page_bytes(const xpress_cache& c) {
+  return (int64_t)c.Hkv * c.page * c.D * (cache_in_4_bits(c) ? 17 : 64) / 32;
+}
+
 size_t cache_scratch_bytes(const xpress_cache& c, int n_max);
 hipError_t launch_cache_fork(const xpress_cache& c, const int32_t* src, const int32_t* dst, int n,
                              hipStream_t s);
@@ -19,6 +27,12 @@ hipError_t launch_cache_extend(const xpress_cache& c, const int32_t* seq, int N,
 hipError_t launch_cache_append(const xpress_cache& c, const int32_t* lacking, int layer,
                                const void* k_new, const void* v_new, int64_t ld_new,
                                const int32_t* seq, int N, int B, hipStream_t s);
+hipError_t launch_cache_append4(const xpress_cache& c, const int32_t* lacking, int layer,
+                                const void* k_new, const void* v_new, int64_t ld_new,
+                                const int32_t* seq, int N, int B, hipStream_t s);
+hipError_t launch_cache_read(const xpress_cache& c, int layer, const int32_t* first, void* k_out,
+                             void* v_out, int64_t ld_out, const int32_t* seq, int N, int B,
+                             hipStream_t s);
 hipError_t launch_cache_trim(const xpress_cache& c, const int32_t* lacking, const int32_t* seq, int N,
                              const int32_t* drop, hipStream_t s);
 hipError_t launch_cache_compact(const xpress_cache& c, int32_t* live, void* ws, hipStream_t s);
@@ -29,6 +43,10 @@ hipError_t launch_block_attention(const xpress_cache& c, int layer, const void* 
                                   const int32_t* seq, int N, int B, int Hq, float scale,
                                   int shared, void* out, int64_t out_ld, float* lse, void* ws,
                                   hipStream_t s);
+
+hipError_t launch_block_attention4(const xpress_cache& c, int layer, const void* q, int64_t q_ld,
+                                   const int32_t* seq, int N, int B, int Hq, float scale, int shared,
+                                   void* out, int64_t out_ld, float* lse, void* ws, hipStream_t s);
 
 size_t verify_scratch_bytes(int N, int B, int64_t V);
 int64_t verify_items(int N, int B, int64_t V);  // workgroups

@@ -38,8 +38,9 @@ xpress_status check_cache(const xpress_cache* c, bool pools, bool tables) {
     return fail(XPRESS_ERR_ARG, "rows=%d outside [1, 2^20]", c->rows);
   if (c->table_ld < 1 || c->table_ld > 1 << 20)
     return fail(XPRESS_ERR_ARG, "table_ld=%d outside [1, 2^20]", c->table_ld);
-  if (c->dtype != XPRESS_BF16 && c->dtype != XPRESS_F16)
-    return fail(XPRESS_ERR_ARG, "dtype=%u is neither XPRESS_BF16 nor XPRESS_F16", c->dtype);
+  if (c->dtype != XPRESS_BF16 && c->dtype != XPRESS_F16 && c->dtype != XPRESS_BF16_MX4 &&
+      c->dtype != XPRESS_F16_MX4)
+    return fail(XPRESS_ERR_ARG, "dtype=%u is not XPRESS_BF16, _F16, _BF16_MX4 or _F16_MX4", c->dtype);
   if (pools) {
     XP_PTR(c->k);
     XP_PTR(c->v);
@@ -56,6 +57,20 @@ xpress_status check_rows(const xpress_cache* c, const int32_t* seq, int32_t N) {
   if (N < 0) return fail(XPRESS_ERR_ARG, "N=%d < 0", N);
   if (N > c->rows) return fail(XPRESS_ERR_ARG, "N=%d > rows=%d", N, c->rows);
   XP_WORDS_OR_NULL(seq);
+  return XPRESS_OK;
+}
+
+// B tokens of each of N rows in one layer, a token every `ld` elements.
+xpress_status check_block(const xpress_cache* c, int32_t layer, int32_t N, int32_t B, int64_t ld,
+                          const char* name) {
+  if (layer < 0 || layer >= c->n_layers)
+    return fail(XPRESS_ERR_ARG, "layer=%d outside [0, %d)", layer, c->n_layers);
+  if (B < 0) return fail(XPRESS_ERR_ARG, "B=%d < 0", B);
+  if ((int64_t)N * B * c->Hkv >= (int64_t)1 << 26)
+    return fail(XPRESS_ERR_ARG, "N*B*Hkv = %d*%d*%d is not below 2^26", N, B, c->Hkv);
+  if (ld < (int64_t)c->Hkv * c->D || ld % 8)
+    return fail(XPRESS_ERR_ARG, "%s=%lld must be >= Hkv*D=%d and a multiple of 8", name, (long long)ld,
+                c->Hkv * c->D);
   return XPRESS_OK;
 }
 
@@ -150,14 +165,8 @@ xpress_status xpress_cache_append_if(const xpress_cache* c, const int32_t* lacki
   if (st != XPRESS_OK) return st;
   st = check_rows(c, seq, N);
   if (st != XPRESS_OK) return st;
-  if (layer < 0 || layer >= c->n_layers)
-    return fail(XPRESS_ERR_ARG, "layer=%d outside [0, %d)", layer, c->n_layers);
-  if (B < 0) return fail(XPRESS_ERR_ARG, "B=%d < 0", B);
-  if ((int64_t)N * B * c->Hkv >= (int64_t)1 << 26)
-    return fail(XPRESS_ERR_ARG, "N*B*Hkv = %d*%d*%d is not below 2^26", N, B, c->Hkv);
-  if (ld_new < (int64_t)c->Hkv * c->D || ld_new % 8)
-    return fail(XPRESS_ERR_ARG, "ld_new=%lld must be >= Hkv*D=%d and a multiple of 8",
-                (long long)ld_new, c->Hkv * c->D);
+  st = check_block(c, layer, N, B, ld_new, "ld_new");
+  if (st != XPRESS_OK) return st;
   XP_WORDS_OR_NULL(lacking);
   if (N == 0 || B == 0) return XPRESS_OK;
   XP_PTR(k_new);
@@ -172,6 +181,25 @@ xpress_status xpress_cache_append(const xpress_cache* c, int32_t layer, const vo
                                   const void* v_new, int64_t ld_new, const int32_t* seq, int32_t N,
                                   int32_t B, xpress_stream stream) {
   return xpress_cache_append_if(c, nullptr, layer, k_new, v_new, ld_new, seq, N, B, stream);
+}
+
+xpress_status xpress_cache_read(const xpress_cache* c, int32_t layer, const int32_t* seq, int32_t N,
+                                const int32_t* first, int32_t B, void* k_out, void* v_out,
+                                int64_t ld_out, xpress_stream stream) {
+  xpress_status st = check_cache(c, true, true);
+  if (st != XPRESS_OK) return st;
+  st = check_rows(c, seq, N);
+  if (st != XPRESS_OK) return st;
+  st = check_block(c, layer, N, B, ld_out, "ld_out");
+  if (st != XPRESS_OK) return st;
+  XP_WORDS_OR_NULL(first);
+  if (N == 0 || B == 0) return XPRESS_OK;
+  XP_PTR(k_out);
+  XP_PTR(v_out);
+  XP_TRY(xpress::launch_cache_read(*c, layer, first, k_out, v_out, ld_out, seq, N, B,
+                                   hip_stream(stream)),
+         "cache read");
+  return XPRESS_OK;
 }
 
 xpress_status xpress_cache_trim_if(const xpress_cache* c, const int32_t* lacking, const int32_t* seq,

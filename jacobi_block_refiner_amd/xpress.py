@@ -97,6 +97,7 @@ def lib() -> ctypes.CDLL:
             "xpress_cache_extend": [C, P, i32, P, i32, P, P, sz, P],
             "xpress_cache_append": [C, i32, P, P, i64, P, i32, i32, P],
             "xpress_cache_append_if": [C, P, i32, P, P, i64, P, i32, i32, P],
+            "xpress_cache_read": [C, i32, P, i32, P, i32, P, P, i64, P],
             "xpress_cache_trim": [C, P, i32, P, P],
             "xpress_cache_trim_if": [C, P, P, i32, P, P],
             "xpress_cache_compact": [C, P, P, sz, P],
@@ -416,6 +417,7 @@ class StepGraph:
 # ------------------------------------------------------------- the target's side of a draft step
 
 BF16, F16, F32 = 0, 1, 2
+MX4 = 16  # of a cache: its values are held in 4 bits
 _DTYPES = {torch.bfloat16: BF16, torch.float16: F16, torch.float32: F32}
 
 
@@ -452,40 +454,50 @@ def _ws(ws):
 class Cache:
     """A paged K/V cache (``xpress_cache``): pools of pages, one table row a sequence, tokens a
     sequence and holders a page. The caller owns the tensors; the struct is built with the object, and
-    anew when one of its tensors is replaced."""
+    anew when one of its tensors is replaced. Pools of bytes hold values of 4 bits."""
 
-    k: torch.Tensor  # [n_layers, n_pages, Hkv, page, D] bf16 or fp16
-    v: torch.Tensor
+    k: torch.Tensor  # [n_layers, n_pages, Hkv, page, D] bf16 or fp16, or
+    v: torch.Tensor  # [n_layers, n_pages, Hkv, page/16, 17*D/2] uint8
     table: torch.Tensor  # [rows, table_ld] int32, -1 past a row's pages
     length: torch.Tensor  # [rows] int32
     ref: torch.Tensor  # [n_pages] int32
+    dtype: torch.dtype | None = None  # of the values; None: the pools' (bytes: bf16)
 
     def __post_init__(self):
         if self.k.dim() != 5 or self.v.shape != self.k.shape:
             raise ValueError("k and v must be [n_layers, n_pages, Hkv, page, D]")
+        mx4 = self.k.dtype == torch.uint8
+        if mx4 and self.k.shape[4] % 17:
+            raise ValueError("k and v of 4 bits must be [n_layers, n_pages, Hkv, page/16, 17*D/2]")
         if self.table.dim() != 2 or self.length.shape != self.table.shape[:1]:
             raise ValueError("table must be [rows, table_ld] and length [rows]")
         if self.ref.shape != self.k.shape[1:2]:
             raise ValueError("ref must be [n_pages]")
-        if self.k.dtype not in (torch.bfloat16, torch.float16):
-            raise TypeError("k must be bfloat16 or float16")
+        if self.k.dtype not in (torch.bfloat16, torch.float16, torch.uint8):
+            raise TypeError("k must be bfloat16 or float16, or uint8 for 4 bits")
+        values = self.dtype or (torch.bfloat16 if mx4 else self.k.dtype)
+        if values not in ((torch.bfloat16, torch.float16) if mx4 else (self.k.dtype,)):
+            raise TypeError(f"a cache of {self.k.dtype} pools cannot hold {values}")
         for name, dtype in (("k", self.k.dtype), ("v", self.k.dtype), ("table", torch.int32),
                             ("length", torch.int32), ("ref", torch.int32)):
             t = getattr(self, name)
             if t.dtype != dtype or not t.is_cuda or not t.is_contiguous():
                 raise TypeError(f"{name} must be a contiguous CUDA {dtype} tensor")
         n_layers, n_pages, Hkv, page, D = self.k.shape
+        if mx4:
+            page, D = page * 16, D // 17 * 2
         rows, ld = self.table.shape
-        self._struct = _Cache(n_layers, n_pages, page, Hkv, D, _DTYPES[self.k.dtype], rows, ld,
-                              self.k.data_ptr(), self.v.data_ptr(), self.table.data_ptr(),
+        self._struct = _Cache(n_layers, n_pages, page, Hkv, D, _DTYPES[values] + (MX4 if mx4 else 0),
+                              rows, ld, self.k.data_ptr(), self.v.data_ptr(), self.table.data_ptr(),
                               self.length.data_ptr(), self.ref.data_ptr())
         self._ref = ctypes.byref(self._struct)
-        self._dtype, self._width, self._D = self.k.dtype, Hkv * D, D
+        self._dtype, self._width, self._D, self.page = values, Hkv * D, D, page
 
     def __setattr__(self, name, value):
         before = self.__dict__.get(name)
         object.__setattr__(self, name, value)
-        if isinstance(before, torch.Tensor) and "_ref" in self.__dict__:
+        fields = isinstance(before, torch.Tensor) or name == "dtype"
+        if fields and "_ref" in self.__dict__:
             try:
                 self.__post_init__()
             except Exception:
@@ -494,11 +506,19 @@ class Cache:
 
     @classmethod
     def empty(cls, n_layers: int, n_pages: int, Hkv: int, page: int, D: int, rows: int,
-              table_ld: int, dtype=torch.bfloat16, device="cuda") -> "Cache":
-        """An empty cache: every page free, every row of length 0. The pools are not filled."""
+              table_ld: int, dtype=torch.bfloat16, device="cuda", bits: int = 16) -> "Cache":
+        """An empty cache: every page free, every row of length 0. The pools are not filled. bits 4:
+        values of ``dtype`` go in and come out, and are held in 4 bits and a scale of 8 for 32."""
+        if bits not in (4, 16):
+            raise ValueError("bits must be 4 or 16")
+        if bits == 4 and (page % 16 or D % 32):
+            raise ValueError("a cache of 4 bits takes pages of 16 tokens and heads of 32 channels")
         shape = (n_layers, n_pages, Hkv, page, D)
-        return cls(k=torch.empty(shape, dtype=dtype, device=device),
-                   v=torch.empty(shape, dtype=dtype, device=device),
+        pool = dtype
+        if bits == 4:
+            shape, pool = (n_layers, n_pages, Hkv, page // 16, 17 * D // 2), torch.uint8
+        return cls(k=torch.empty(shape, dtype=pool, device=device),
+                   v=torch.empty(shape, dtype=pool, device=device), dtype=dtype,
                    table=torch.full((rows, table_ld), -1, dtype=torch.int32, device=device),
                    length=torch.zeros(rows, dtype=torch.int32, device=device),
                    ref=torch.zeros(n_pages, dtype=torch.int32, device=device))
@@ -550,6 +570,19 @@ def cache_append(cache: Cache, layer: int, k_new: torch.Tensor, v_new: torch.Ten
     _check(lib().xpress_cache_append_if(cache._ref, _list(lacking, 1, torch.int32, "lacking"), layer,
                                         k_new.data_ptr(), v_new.data_ptr(), ld,
                                         _list(seq, N, torch.int32, "seq"), N, B, _stream()))
+
+
+def cache_read(cache: Cache, layer: int, k_out: torch.Tensor, v_out: torch.Tensor, *, B: int,
+               first: torch.Tensor | None = None, seq=None, N: int | None = None) -> None:
+    """K and V of one layer read back: tokens first[i].. (int32; None: the last B) of each row, into
+    k_out, v_out: [N*B, Hkv*D] views with the same row stride. Positions outside a row give 0."""
+    N = cache._rows(seq, N)
+    ld = _tokens(k_out, N * B, cache._width, cache._dtype, "k_out")
+    if _tokens(v_out, N * B, cache._width, cache._dtype, "v_out") != ld:
+        raise ValueError("k_out and v_out must have the same row stride")
+    _check(lib().xpress_cache_read(cache._ref, layer, _list(seq, N, torch.int32, "seq"), N,
+                                   _list(first, N, torch.int32, "first"), B, k_out.data_ptr(),
+                                   v_out.data_ptr(), ld, _stream()))
 
 
 def cache_trim(cache: Cache, drop=None, *, seq=None, N: int | None = None,
