@@ -294,6 +294,7 @@ xpress_status xpress_graph_destroy(void* graph);
  *   xpress_cache_extend                 room for the block's B tokens (anchor and drafts);
  *   xpress_cache_append_if, xpress_block_attention   once a layer of the target;
  *   xpress_verify_draft                 which drafts stand, and the next token;
+ *   xpress_token_logprobs               (where they are reported) their log probabilities;
  *   xpress_cache_trim_if                gives back the refused drafts' tokens.
  * The conventions above hold (device pointers, stream order, nothing allocated, host-side argument
  * errors, N == 0 is a no-op); the _if calls do nothing where the extension found no room. Page tables,
@@ -465,6 +466,35 @@ xpress_status xpress_verify_draft(const void* logits, uint32_t logits_dtype, int
                                   const float* u, int32_t N, int32_t B, int64_t V, int64_t* out,
                                   int32_t* accepted, int32_t* drop, void* ws, size_t ws_bytes,
                                   xpress_stream stream);
+
+/* Log probabilities of tokens under rows of logits, beside the verification or for a prompt's tokens.
+ * Row i*B + s of logits gives p = softmax(x / temperature[i]), and of it
+ *   logprob[row] = log p(token[row]);
+ *   entropy[row] = -sum p log p, in nats;
+ *   rank[row] = the number of ids with a larger logit than the token's (0: none is more likely);
+ *   top_ids[row, k], top_logprobs[row, k], k < top: the ids with the largest logits (by value, then
+ *   the lowest id) and their log probabilities; past V ids -1 and -inf.
+ * A negative token stands for none (a slot behind the last of a block, as xpress_verify_draft writes
+ * -1): its row is not read, logprob and entropy are 0, rank is -1, its alternatives -1 at -inf. A token
+ * of V or more has logprob -inf and rank -1. token NULL: every row counts, and logprob and rank must be
+ * NULL.
+ * temperature: [N] fp32, nullable (1). At 0, a negative value or NaN all of p is on the first of the
+ * alternatives: its log probability is 0, the others' -inf, the entropy 0.
+ * A logit of -inf or NaN has no weight and is ordered last (by id); at +inf the ids that hold it share
+ * all. In a row without any weight the log probabilities are -inf and the entropy is 0.
+ * token: [N, B] int64. logprob, entropy: [N*B] fp32, rank: [N*B] int32, each nullable. top_ids: [N*B,
+ * top] int64, top_logprobs: [N*B, top] fp32 (top 0: not used). logits: XPRESS_BF16, _F16 or _F32 with
+ * row stride ld >= V in elements, any alignment of the rows to their own elements. 0 <= top <= 64;
+ * 1 <= V < 2^31; N*B*ceil((V+7)/8192) < 2^24. Weights and a chunk's sums have 32 bits, sums of chunks
+ * and logarithms 64. Deterministic. */
+xpress_status xpress_logprobs_workspace_size(int32_t rows_max, int64_t V, int32_t top,
+                                             size_t* bytes);
+xpress_status xpress_token_logprobs(const void* logits, uint32_t logits_dtype, int64_t ld,
+                                    const int64_t* token, const float* temperature, int32_t N,
+                                    int32_t B, int64_t V, int32_t top, float* logprob,
+                                    float* entropy, int32_t* rank, int64_t* top_ids,
+                                    float* top_logprobs, void* ws, size_t ws_bytes,
+                                    xpress_stream stream);
 
 /* Message of the last non-OK status returned on the calling thread ("" if none). */
 const char* xpress_last_error(void);

@@ -56,4 +56,12 @@ hipError_t launch_verify_draft(const void* logits, uint32_t logits_dtype, int64_
                                const float* u, int N, int B, int64_t V, int64_t* out,
                                int32_t* accepted, int32_t* drop, void* ws, hipStream_t s);
 
+constexpr int kMostTop = 64;  // alternatives of a row at most
+size_t logprobs_scratch_bytes(int64_t rows, int64_t V);
+int64_t logprobs_items(int64_t rows, int64_t V);  // workgroups
+hipError_t launch_token_logprobs(const void* logits, uint32_t dtype, int64_t ld, const int64_t* token,
+                                 const float* temperature, int N, int B, int64_t V, int top,
+                                 float* logprob, float* entropy, int32_t* rank, int64_t* top_ids,
+                                 float* top_logprobs, void* ws, hipStream_t s);
+
 }  // namespace xpress

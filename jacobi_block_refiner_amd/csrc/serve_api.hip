@@ -1,5 +1,5 @@
 // C ABI of the target's side of a draft step: argument checks of the paged cache, the block
-// attention and the draft verification. Every entry point validates on the host, then only
+// attention, the draft verification and the log probabilities of tokens. Every entry point validates on the host, then only
 // enqueues kernels on the caller's stream.
 #include "api_common.hpp"
 #include "serve.hpp"
@@ -99,6 +99,18 @@ xpress_status check_verify(int32_t N, int32_t B, int64_t V) {
     return fail(XPRESS_ERR_ARG, "V=%lld outside [1, 2^31)", (long long)V);
   if ((int64_t)N * B >= (int64_t)1 << 24 || xpress::verify_items(N, B, V) >= (int64_t)1 << 24)
     return fail(XPRESS_ERR_ARG, "N=%d, B=%d, V=%lld is too large a launch", N, B, (long long)V);
+  return XPRESS_OK;
+}
+
+xpress_status check_logprobs(int64_t rows, int64_t V, int32_t top) {
+  if (rows < 0) return fail(XPRESS_ERR_ARG, "%lld rows < 0", (long long)rows);
+  if (V < 1 || V >= (int64_t)1 << 31)
+    return fail(XPRESS_ERR_ARG, "V=%lld outside [1, 2^31)", (long long)V);
+  if (top < 0 || top > xpress::kMostTop)
+    return fail(XPRESS_ERR_ARG, "top=%d outside [0, %d]", top, xpress::kMostTop);
+  if (rows >= (int64_t)1 << 24 || xpress::logprobs_items(rows, V) >= (int64_t)1 << 24)
+    return fail(XPRESS_ERR_ARG, "%lld rows of V=%lld are too large a launch", (long long)rows,
+                (long long)V);
   return XPRESS_OK;
 }
 
@@ -314,6 +326,50 @@ xpress_status xpress_verify_draft(const void* logits, uint32_t logits_dtype, int
                                      temperature, u, N, B, V, out, accepted, drop, ws,
                                      hip_stream(stream)),
          "draft verification");
+  return XPRESS_OK;
+}
+
+xpress_status xpress_logprobs_workspace_size(int32_t rows_max, int64_t V, int32_t top,
+                                             size_t* bytes) {
+  if (bytes == nullptr) return fail(XPRESS_ERR_ARG, "bytes is NULL");
+  xpress_status st = check_logprobs(rows_max, V, top);
+  if (st != XPRESS_OK) return st;
+  *bytes = up256(xpress::logprobs_scratch_bytes(rows_max, V));
+  return XPRESS_OK;
+}
+
+xpress_status xpress_token_logprobs(const void* logits, uint32_t logits_dtype, int64_t ld,
+                                    const int64_t* token, const float* temperature, int32_t N,
+                                    int32_t B, int64_t V, int32_t top, float* logprob,
+                                    float* entropy, int32_t* rank, int64_t* top_ids,
+                                    float* top_logprobs, void* ws, size_t ws_bytes,
+                                    xpress_stream stream) {
+  if (N < 0) return fail(XPRESS_ERR_ARG, "N=%d < 0", N);
+  if (B < 1) return fail(XPRESS_ERR_ARG, "B=%d < 1", B);
+  const int64_t rows = (int64_t)N * B;
+  xpress_status st = check_logprobs(rows, V, top);
+  if (st != XPRESS_OK) return st;
+  if (N == 0) return XPRESS_OK;
+  st = check_values(logits, "logits", logits_dtype, ld, V);
+  if (st != XPRESS_OK) return st;
+  if (!aligned_to(token, 8)) return fail(XPRESS_ERR_ARG, "token is not 8-byte aligned");
+  XP_WORDS_OR_NULL(temperature);
+  XP_WORDS_OR_NULL(logprob);
+  XP_WORDS_OR_NULL(entropy);
+  XP_WORDS_OR_NULL(rank);
+  if (token == nullptr && (logprob != nullptr || rank != nullptr))
+    return fail(XPRESS_ERR_ARG, "token is NULL: there is no logprob and no rank without it");
+  if (top > 0) {
+    if (top_ids == nullptr || !aligned_to(top_ids, 8))
+      return fail(XPRESS_ERR_ARG, "top_ids is NULL or not 8-byte aligned");
+    XP_WORDS(top_logprobs);
+  }
+  st = check_ws(ws, ws_bytes, xpress::logprobs_scratch_bytes(rows, V));
+  if (st != XPRESS_OK) return st;
+  XP_TRY(xpress::launch_token_logprobs(logits, logits_dtype, ld, token, temperature, N, B, V, top,
+                                       logprob, entropy, rank, top_ids, top_logprobs, ws,
+                                       hip_stream(stream)),
+         "token log probabilities");
   return XPRESS_OK;
 }
 

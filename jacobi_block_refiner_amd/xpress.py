@@ -107,6 +107,8 @@ def lib() -> ctypes.CDLL:
             "xpress_verify_workspace_size": [i32, i32, i64, ctypes.POINTER(sz)],
             "xpress_verify_draft": [P, u32, i64, P, P, P, u32, i64, P, P, i32, i32, i64, P, P, P,
                                     P, sz, P],
+            "xpress_logprobs_workspace_size": [i32, i64, i32, ctypes.POINTER(sz)],
+            "xpress_token_logprobs": [P, u32, i64, P, P, i32, i32, i64, i32, P, P, P, P, P, P, sz, P],
         }
         for name, args in sig.items():
             fn = getattr(L, name)
@@ -658,3 +660,38 @@ def verify_draft(logits: torch.Tensor, blk: torch.Tensor, *, out: torch.Tensor,
         _list(out, N * B, i64, "out"), _list(accepted, N, i32, "accepted"),
         _list(drop, N, i32, "drop"), ws_ptr, ws_bytes, _stream()))
     return out
+
+
+def logprobs_workspace(rows_max: int, V: int, top: int = 0, device="cuda") -> torch.Tensor:
+    out = ctypes.c_size_t()
+    _check(lib().xpress_logprobs_workspace_size(rows_max, V, top, ctypes.byref(out)))
+    return torch.empty(max(out.value, 256), dtype=torch.uint8, device=device)
+
+
+def token_logprobs(logits: torch.Tensor, token: torch.Tensor | None = None, *, ws: torch.Tensor,
+                   temperature=None, logprob=None, entropy=None, rank=None, top_ids=None,
+                   top_logprobs=None) -> None:
+    """Of tokens [N, B] (negative: none there) under logits [N*B, V]: their log probabilities, the
+    entropy, their ranks, and the most likely alternatives, top_ids and top_logprobs [N*B, top]; each
+    is written where it is given. temperature: [N] float32 (None: 1). token None: [N*B, 1] rows."""
+    rows, V = logits.shape
+    N, B = (rows, 1) if token is None else token.shape
+    if logits.dtype not in _DTYPES:
+        raise TypeError("logits must be bfloat16, float16 or float32")
+    ld = _tokens(logits, N * B, V, logits.dtype, "logits")
+    top = 0
+    if (top_ids is None) != (top_logprobs is None):
+        raise ValueError("top_ids and top_logprobs go together")
+    if top_ids is not None:
+        top = top_ids.shape[-1]
+        if top_ids.shape != top_logprobs.shape or top_ids.dim() != 2:
+            raise ValueError("top_ids and top_logprobs must be [N*B, top]")
+    ws_ptr, ws_bytes = _ws(ws)
+    i64, i32, f32 = torch.int64, torch.int32, torch.float32
+    n = N * B
+    _check(lib().xpress_token_logprobs(
+        logits.data_ptr(), _DTYPES[logits.dtype], ld, _list(token, n, i64, "token"),
+        _list(temperature, N, f32, "temperature"), N, B, V, top, _list(logprob, n, f32, "logprob"),
+        _list(entropy, n, f32, "entropy"), _list(rank, n, i32, "rank"),
+        _list(top_ids, n * top, i64, "top_ids"), _list(top_logprobs, n * top, f32, "top_logprobs"),
+        ws_ptr, ws_bytes, _stream()))
