@@ -6,11 +6,12 @@ runs the target over the block and keeps what the target confirms:
 
     xpress_jacobi_step -> xpress_cache_extend
     -> (xpress_cache_append_if, xpress_block_attention) a layer
-    -> xpress_verify_draft -> xpress_cache_trim_if
+    -> xpress_verify_draft -> xpress_cache_trim_if (-> xpress_token_logprobs)
 
 At the end all samples but one are freed and the pool is compacted.
 
     python -m jacobi_block_refiner_amd.draft_turn [--samples 4] [--turns 8] [--prompt 200] [--greedy]
+                                                [--bits 4] [--logprobs]
 """
 from __future__ import annotations
 
@@ -69,13 +70,22 @@ class Turn:
     u: torch.Tensor  # [N, B]
     out: torch.Tensor  # [N, B]: the accepted drafts, one more token, -1
     accepted: torch.Tensor  # [N]
+    # of the tokens in out, where they are asked for: log probability, entropy and rank [N, B], and the
+    # most likely ids with their log probabilities [N, B, top]
+    logprob: torch.Tensor | None = None
+    entropy: torch.Tensor | None = None
+    rank: torch.Tensor | None = None
+    top_ids: torch.Tensor | None = None
+    top_logprobs: torch.Tensor | None = None
 
 
 class Decoder:
-    """The samples of one prompt: their cache, the refiner's inputs and the buffers of a turn."""
+    """The samples of one prompt: their cache (of 16 or 4 bits), the refiner's inputs and the buffers of
+    a turn. top: with each turn's tokens come their log probabilities and as many alternatives."""
 
     def __init__(self, target: Target, refiner: xpress.Weights, samples: int, *, page: int = 16,
-                 most: int = 512, temperature: float = 1.0, seed: int = 0):
+                 most: int = 512, temperature: float = 1.0, seed: int = 0, bits: int = 16,
+                 top: int | None = None):
         d = refiner.dims
         if (d["H"], d["V"]) != (target.H, target.V):
             raise ValueError("the refiner and the target differ in hidden size or vocabulary")
@@ -85,7 +95,7 @@ class Decoder:
         ld = -(-(most + B) // page)
         # every row's table full, and the prompt's last page while every sample copies it
         self.cache = xpress.Cache.empty(len(target.layers), ld * N + 1, target.Hkv, page, target.D, N,
-                                        ld, device=dev)
+                                        ld, device=dev, bits=bits)
         self.shared = 0
 
         def empty(*shape, dtype=torch.int32):
@@ -99,6 +109,9 @@ class Decoder:
         self.cache_ws = xpress.cache_workspace(self.cache, N)
         self.attention_ws = xpress.attention_workspace(self.cache, N, B, target.Hq)
         self.verify_ws = xpress.verify_workspace(N, B, V, dev)
+        self.top = top
+        if top is not None:
+            self.logprobs_ws = xpress.logprobs_workspace(N * B, V, top, dev)
 
     def _run(self, ids: torch.Tensor, N: int, B: int, ws: torch.Tensor):
         """The target over B more tokens of rows 0..N-1; ids: [N*B]."""
@@ -144,9 +157,19 @@ class Decoder:
         xpress.verify_draft(logits, self.blk, u=u, temperature=self.temperature, out=self.out,
                             accepted=self.accepted, drop=self.drop, ws=self.verify_ws)
         xpress.cache_trim(self.cache, self.drop, N=N, lacking=self.lacking)
+        said = {}
+        if self.top is not None:
+            said = {name: torch.empty(N * B, device=h.device) for name in ("logprob", "entropy")}
+            said["rank"] = torch.empty(N * B, dtype=torch.int32, device=h.device)
+            if self.top:
+                said["top_ids"] = torch.empty(N * B, self.top, dtype=torch.int64, device=h.device)
+                said["top_logprobs"] = torch.empty(N * B, self.top, device=h.device)
+            xpress.token_logprobs(logits, self.out, temperature=self.temperature,
+                                  ws=self.logprobs_ws, **said)
+            said = {name: t.view(N, B, *t.shape[1:]) for name, t in said.items()}
         # tokens of the longest row at most: the host waits for the card only where they might not fit
         self.reach += B
-        if self.reach > self.cache.table.shape[1] * self.cache.k.shape[3]:
+        if self.reach > self.cache.table.shape[1] * self.cache.page:
             self._check_room()
         # the extra token is the next anchor; the state it was drawn from serves the next block
         a = self.accepted.to(torch.int64)[:, None]
@@ -154,7 +177,7 @@ class Decoder:
         self.h = h.view(N, B, -1).gather(1, a[:, :, None].expand(N, 1, h.shape[1])).repeat(1, B, 1)
         base = logits.view(N, B, V).gather(1, a[:, :, None].expand(N, 1, V))
         self.base = base.expand(N, B - 1, V).reshape(N * (B - 1), V).contiguous()
-        return Turn(self.blk.clone(), logits, u, self.out.clone(), self.accepted.clone())
+        return Turn(self.blk.clone(), logits, u, self.out.clone(), self.accepted.clone(), **said)
 
     def keep(self, sample: int) -> int:
         """Frees every sample but one and compacts the pool; the pages that are left."""
@@ -178,21 +201,27 @@ def main(argv=None) -> None:
     p.add_argument("--turns", type=int, default=8)
     p.add_argument("--prompt", type=int, default=200)
     p.add_argument("--greedy", action="store_true")
+    p.add_argument("--bits", type=int, default=16, choices=(4, 16), help="of a value in the cache")
+    p.add_argument("--logprobs", action="store_true", help="of the tokens, summed up a sample")
     a = p.parse_args(argv)
     inp = synth.make_inputs(1).rounded_bf16()
     most = a.prompt + a.turns * inp.wl.B
     target = Target(inp.wl.V, inp.wl.H, most=most + inp.wl.B)
     dec = Decoder(target, upload.weights(inp), a.samples, most=most,
-                  temperature=0.0 if a.greedy else 1.0)
+                  temperature=0.0 if a.greedy else 1.0, bits=a.bits,
+                  top=0 if a.logprobs else None)
     ids = torch.randint(inp.wl.V, (a.prompt,), generator=torch.Generator().manual_seed(1))
     dec.prompt(ids.cuda())
-    text = [[] for _ in range(a.samples)]
+    text, logprob = [[] for _ in range(a.samples)], torch.zeros(a.samples, device="cuda")
     for _ in range(a.turns):
         t = dec.turn()
         for row, new in zip(text, t.out.tolist()):
             row += [x for x in new if x >= 0]
+        if a.logprobs:
+            logprob += t.logprob.sum(1)
     for i, row in enumerate(text):
-        print(f"sample {i}: {len(row)} tokens in {a.turns} turns: {row[:12]}")
+        said = f", log probability {float(logprob[i]):.2f}" if a.logprobs else ""
+        print(f"sample {i}: {len(row)} tokens in {a.turns} turns: {row[:12]}{said}")
     print(f"pages after keeping sample 0: {dec.keep(0)}")
 
 
