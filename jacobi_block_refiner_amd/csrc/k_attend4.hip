@@ -1,16 +1,620 @@
 // Attention of drafted blocks over a paged cache of 4 bits (gfx950).
+//
+// Query rows of the shared part, and of requests with more than 32 of them a head, go to the items of
+// attend_kernel.hpp. The requests' own keys with up to 32 rows a head (plain decoding, short blocks)
+// are HBM's: 2 * 17 D / 32 bytes a key for few operations. few_kernel reads them straight into the
+// matrix core's registers.
+//
+// All (request, head) pairs' tiles of 32 keys form one sequence, which is cut into as many equal parts
+// as there are workgroups on the card, whatever the lengths: a workgroup finds its part from the
+// lengths themselves. A pair that lies in one part is finished there; where it is cut, each part
+// leaves (sums, unit of the weights, their sum) in a slot, and join_kernel joins them.
 #include "attend_kernel.hpp"
 
 namespace xpress {
+
+namespace {
+
+constexpr int kFewTile = 32;   // keys of a step of a wave
+constexpr int kFewLeast = 4;   // tiles of a part at least: one a wave
+constexpr int kFewRequests = 4096;  // more are not cut: a workgroup a pair
+
+// Workgroups of few_kernel on a CU, by its registers.
+constexpr int few_per_cu(int D, int RT) { return D == 256 ? 3 - RT : RT == 1 ? D == 64 ? 4 : 3 : 2; }
+
+// A pair whose keys lie in several parts: it begins in this one.
+struct Cut {
+  int pair, slots;
+  int64_t slot;  // its first; then 2 (w + 1), 2 (w + 2), ..
+};
+
+struct Few {
+  Args a;
+  int parts;  // workgroups, where the sequence is cut; else 0
+  float* po;   // [2 * parts, R, D]
+  float2* pml; // [2 * parts, R]
+  Cut* cut;    // [parts]
+};
+
+typedef float f32x4v __attribute__((ext_vector_type(4)));
+
+template <bool F16>
+__device__ __forceinline__ f32x4v mfma16(const s16x8& a, const s16x8& b, const f32x4v& c) {
+  if constexpr (F16)
+    return __builtin_amdgcn_mfma_f32_16x16x32_f16(__builtin_bit_cast(f16x8, a),
+                                                  __builtin_bit_cast(f16x8, b), c, 0, 0, 0);
+  else
+    return __builtin_amdgcn_mfma_f32_16x16x32_bf16(__builtin_bit_cast(bf16x8, a),
+                                                   __builtin_bit_cast(bf16x8, b), c, 0, 0, 0);
+}
+
+// N words from an address that is aligned to all of them.
+template <int N> __device__ __forceinline__ void load_words(const uint8_t* p, uint32_t (&w)[N]) {
+  if constexpr (N == 2) {
+    const uint2 u = *reinterpret_cast<const uint2*>(p);
+    w[0] = u.x, w[1] = u.y;
+  } else {
+#pragma unroll
+    for (int i = 0; i < N / 4; ++i) {
+      const uint4 u = reinterpret_cast<const uint4*>(p)[i];
+      w[4 * i] = u.x, w[4 * i + 1] = u.y, w[4 * i + 2] = u.z, w[4 * i + 3] = u.w;
+    }
+  }
+}
+
+// A tile of 32 keys as a lane holds it: two tiles of 16 tokens. With lane = 16 q + i: of K, token i,
+// its q-th quarter of the channels (of 256 channels two eighths); of V, the pairs of channels i of all
+// groups, tokens 4q..4q+3.
+template <int D> struct Keys {
+  static constexpr int NG = D / 32;
+  uint32_t kc[2][NG], ks[2][D == 256 ? 2 : 1], vc[2][NG], vs[2][NG];
+};
+
+// A wave's 16 RT query rows against tiles of 32 keys, all in registers. Scores are formed transposed,
+// S^T = K Q^T (16 keys x 16 queries): a lane holds four keys' of one query, and as weights they are the
+// right operand of O^T = V^T P^T as they stand. The lane's bytes of K are eight channels of each of the
+// product's steps, and K's and V's conversion to 16 bits takes one instruction a pair (V one more, to
+// put two tokens of a channel beside each other). 32 keys of 16 queries at D 128 take about 250 vector
+// instructions, 1000 cycles; at 5 TB/s a SIMD has 2000.
+template <bool F16, int D, int RT> struct FewCore {
+  static constexpr int NG = D / 32;
+  static constexpr float kLift = F16 ? 7.f : 0.f;  // as in Core
+  static constexpr float kHuge = 0x1p20f;
+
+  int lane, i, q;
+  float c;
+  s16x8 qf[RT][NG];
+  f32x4v o[RT][NG][2];  // channels 32g + 8q + 2r (and + 1) of query i
+  float m[RT], l[RT], shift[RT];
+  uint64_t huge[RT];
+
+  __device__ __forceinline__ void begin(float scale) {
+    lane = threadIdx.x & 63;
+    i = lane & 15;
+    q = lane >> 4;
+    c = scale;
+  }
+  // Channel of the lane's eight of step s of the product.
+  __device__ __forceinline__ int channel(int s) const {
+    return D == 64 ? 16 * q + 8 * s : s / 4 * 128 + 32 * q + 8 * (s % 4);
+  }
+  __device__ __forceinline__ void take(int rt, const uint16_t* row) {
+#pragma unroll
+    for (int s = 0; s < NG; ++s) qf[rt][s] = *reinterpret_cast<const s16x8*>(row + channel(s));
+#pragma unroll
+    for (int g = 0; g < NG; ++g) o[rt][g][0] = o[rt][g][1] = f32x4v{};
+    m[rt] = -1e30f;
+    l[rt] = 0.f;
+    huge[rt] = ~0ull;
+  }
+
+  // The lane's part of tile x (of 16 tokens) from one tile of K and of V.
+  __device__ __forceinline__ void load(Keys<D>& t, int x, const uint8_t* k, const uint8_t* v) const {
+    if constexpr (D == 256) {
+      const uint4 a = *reinterpret_cast<const uint4*>(k + i * 128 + q * 16);
+      const uint4 b = *reinterpret_cast<const uint4*>(k + i * 128 + 64 + q * 16);
+      t.kc[x][0] = a.x, t.kc[x][1] = a.y, t.kc[x][2] = a.z, t.kc[x][3] = a.w;
+      t.kc[x][4] = b.x, t.kc[x][5] = b.y, t.kc[x][6] = b.z, t.kc[x][7] = b.w;
+      t.ks[x][0] = k[mx4_k_scale(D, i, q)];
+      t.ks[x][1] = k[mx4_k_scale(D, i, 4 + q)];
+    } else {
+      load_words<NG>(k + i * (D / 2) + q * (D / 8), t.kc[x]);
+      t.ks[x][0] = k[mx4_k_scale(D, i, D == 64 ? q / 2 : q)];
+    }
+    load_words<NG>(v + lane * (D / 8), t.vc[x]);
+    load_words<NG>(v + mx4_v_scale(D, 4 * q, 0), t.vs[x]);
+  }
+
+  __device__ __forceinline__ s16x8 k_frag(const Keys<D>& t, int x, int s) const {
+    const float scale = mx4_scale<0>(t.ks[x][D == 256 ? s / 4 : 0]);
+    const uint32_t w = t.kc[x][s];
+    return __builtin_bit_cast(s16x8, make_uint4(mx4_pair<F16, 0>(w, scale), mx4_pair<F16, 1>(w, scale),
+                                                mx4_pair<F16, 2>(w, scale), mx4_pair<F16, 3>(w, scale)));
+  }
+
+  // Query i of row tile rt sees the tile's keys below vis (a lane's are 4q.. and 16 + 4q..).
+  __device__ __forceinline__ void step(Keys<D>& t, const int (&vis)[RT], int end, bool masked) {
+    f32x4v s[RT][2];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int d = 0; d < NG; ++d) {
+        const s16x8 k = k_frag(t, x, d);
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt)
+          s[rt][x] = mfma16<F16>(k, qf[rt][d], d == 0 ? f32x4v{} : s[rt][x]);
+      }
+    __builtin_amdgcn_sched_barrier(0);
+    s16x8 pf[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      if (masked) {
+#pragma unroll
+        for (int x = 0; x < 2; ++x)
+#pragma unroll
+          for (int r = 0; r < 4; ++r)
+            s[rt][x][r] = 16 * x + 4 * q + r < vis[rt] ? s[rt][x][r] : -INFINITY;
+      }
+      rise(rt, s[rt]);
+      float sum[2] = {l[rt], 0.f};
+      uint32_t w[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const float a = __builtin_amdgcn_exp2f(fmaf(s[rt][j / 2][j % 2 * 2], c, shift[rt]));
+        const float b = __builtin_amdgcn_exp2f(fmaf(s[rt][j / 2][j % 2 * 2 + 1], c, shift[rt]));
+        sum[j % 2] += a + b;
+        w[j] = pack2<F16>(a, b);
+      }
+      l[rt] = sum[0] + sum[1];
+      pf[rt] = __builtin_bit_cast(s16x8, make_uint4(w[0], w[1], w[2], w[3]));
+    }
+    if (masked) {
+      // keys past the end: a scale of 1, as what lies there could stand for infinity
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const int n = min(max(end - 16 * x - 4 * q, 0), 4);
+        const uint32_t keep = n == 4 ? ~0u : (1u << 8 * n) - 1;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) t.vs[x][g] = (t.vs[x][g] & keep) | (0x7f7f7f7fu & ~keep);
+      }
+    }
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      __builtin_amdgcn_sched_barrier(0);
+      uint32_t even[4], odd[4];
+#pragma unroll
+      for (int x = 0; x < 2; ++x) {
+        const uint32_t w = t.vc[x][g], e = t.vs[x][g];
+        const uint32_t a = mx4_pair<F16, 0>(w, mx4_scale<0>(e)), b = mx4_pair<F16, 1>(w, mx4_scale<1>(e));
+        const uint32_t d = mx4_pair<F16, 2>(w, mx4_scale<2>(e)), f = mx4_pair<F16, 3>(w, mx4_scale<3>(e));
+        even[2 * x] = low_halves(a, b), even[2 * x + 1] = low_halves(d, f);
+        odd[2 * x] = high_halves(a, b), odd[2 * x + 1] = high_halves(d, f);
+      }
+      const s16x8 ve = __builtin_bit_cast(s16x8, make_uint4(even[0], even[1], even[2], even[3]));
+      const s16x8 vo = __builtin_bit_cast(s16x8, make_uint4(odd[0], odd[1], odd[2], odd[3]));
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        o[rt][g][0] = mfma16<F16>(ve, pf[rt], o[rt][g][0]);
+        o[rt][g][1] = mfma16<F16>(vo, pf[rt], o[rt][g][1]);
+      }
+    }
+  }
+
+  // log2 of the weights' unit.
+  __device__ __forceinline__ float unit(int rt) const { return fmaf(m[rt], c, -kLift); }
+
+  // As Core::rise: the sums are rescaled only where some row's maximum grew by more than 2^8 in weight.
+  // The four lanes of a query have one maximum; they exchange theirs only then.
+  __device__ __forceinline__ void rise(int rt, f32x4v (&s)[2]) {
+    float top = s[0][0];
+#pragma unroll
+    for (int x = 0; x < 2; ++x)
+#pragma unroll
+      for (int r = 0; r < 4; ++r) top = fmaxf(top, s[x][r]);
+    if ((__ballot((top - m[rt]) * c > 8.f) | huge[rt]) != 0) {
+      top = fmaxf(top, __shfl_xor(top, 16));
+      top = fmaxf(top, __shfl_xor(top, 32));
+      raise(rt, fmaxf(m[rt], top));
+      shift[rt] = -unit(rt);
+      huge[rt] = __ballot(fabsf(shift[rt]) > kHuge);
+      if (huge[rt] != 0) {
+        s[0] -= m[rt];
+        s[1] -= m[rt];
+        shift[rt] = kLift;
+      }
+    }
+  }
+  __device__ __forceinline__ void raise(int rt, float to) {
+    const float alpha = __builtin_amdgcn_exp2f((m[rt] - to) * c);
+    l[rt] *= alpha;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+      o[rt][g][0] *= alpha;
+      o[rt][g][1] *= alpha;
+    }
+    m[rt] = to;
+  }
+};
+
+// A value that is the same in all lanes, in a scalar register.
+__device__ __forceinline__ int scalar(int x) { return __builtin_amdgcn_readfirstlane(x); }
+__device__ __forceinline__ int64_t scalar(int64_t x) {
+  const uint32_t lo = __builtin_amdgcn_readfirstlane((int)x);
+  return (int64_t)((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(x >> 32)) << 32 | lo);
+}
+
+// Tiles of a request's own keys (one at least: it writes what the request has without them).
+__device__ __forceinline__ int own_tiles(int len, int first) {
+  return max((len - first + kFewTile - 1) / kFewTile, 1);
+}
+
+template <bool F16, int D, int RT>
+__global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
+  using C = FewCore<F16, D, RT>;
+  constexpr int NG = C::NG, LW = RT * NG * 8;  // sums of a lane
+  const Args& A = F.a;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int R = A.B * A.G;
+  __shared__ float s_sum[2][LW][64];
+  __shared__ float s_m[4][RT][64], s_l[4][RT][64];
+  __shared__ int64_t s_scan[4], s_before;
+  __shared__ int s_request;
+
+  // this workgroup's part of the sequence: tiles [at, end) of all, beginning in a request with `before`
+  // tiles a head in front of it
+  int64_t at, end, before, each = 0;
+  int request;
+  if (F.parts) {
+    // each thread a run of requests
+    const int per = (A.N + 255) / 256, r0 = threadIdx.x * per;
+    int64_t mine = 0;
+    for (int j = 0; j < per; ++j)
+      if (r0 + j < A.N) {
+        const int len = list_len(A, r0 + j);
+        mine += own_tiles(len, own_begin(len, A.B, A.shared));
+      }
+    int64_t x = mine;
+#pragma unroll
+    for (int d = 1; d < 64; d *= 2) {
+      const int64_t y = __shfl_up(x, d);
+      if (lane >= d) x += y;
+    }
+    if (lane == 63) s_scan[wave] = x;
+    __syncthreads();
+    int64_t all = 0;
+    x -= mine;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {
+      x += w < wave ? s_scan[w] : 0;
+      all += s_scan[w];
+    }
+    all = scalar(all) * A.Hkv;
+    each = max((all + F.parts - 1) / F.parts, (int64_t)kFewLeast);
+    at = blockIdx.x * each;
+    end = min(at + each, all);
+    if (at >= all) {
+      if (threadIdx.x == 0) F.cut[blockIdx.x].slots = 0;
+      return;
+    }
+    if (x * A.Hkv <= at && at < (x + mine) * A.Hkv) {  // the thread of the first request
+      for (int j = 0; j < per; ++j) {
+        const int len = list_len(A, r0 + j);
+        const int n = own_tiles(len, own_begin(len, A.B, A.shared));
+        if (at < (x + n) * A.Hkv) {
+          s_request = r0 + j;
+          s_before = x;
+          break;
+        }
+        x += n;
+      }
+    }
+    __syncthreads();
+    request = scalar(s_request);
+    before = scalar(s_before);
+  } else {
+    request = blockIdx.x / A.Hkv;
+    before = 0;
+    at = blockIdx.x % A.Hkv;  // (of the request's pairs)
+    end = at + 1;
+  }
+
+  const int64_t head_bytes = mx4_tiles_bytes(D, A.shift);
+  const int page_mask = (1 << A.shift) - 1;
+  Cut cut{0, 0, 0};
+  bool first_segment = true;
+  C w;
+  w.begin(A.c);
+  for (; at < end && request < A.N; ++request) {
+    const int row = scalar(list_row(A, request));
+    const int len = row < 0 ? 0 : clamp_len(scalar(A.len[row]), A.ld, A.shift);
+    const int first = own_begin(len, A.B, A.shared);
+    const int tiles = own_tiles(len, first);
+    const int32_t* table = A.table + (int64_t)max(row, 0) * A.ld;
+    while (at < end) {
+      int hk, t0, t1;
+      if (F.parts) {
+        const int64_t in = at - before * A.Hkv;  // tiles of this request before `at`
+        if (in >= (int64_t)tiles * A.Hkv) break;
+        hk = (int)(in / tiles);
+        t0 = (int)(in % tiles);
+        t1 = (int)min((int64_t)tiles, t0 + (end - at));
+      } else {
+        hk = (int)at;
+        t0 = 0;
+        t1 = tiles;
+      }
+      const int whole = t0 == 0 && t1 == tiles;
+      // the rows
+      int vis[RT];
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        const int rl = min(rt * 16 + w.i, R - 1);
+        vis[rt] = in_sight(len, A.B, rl / A.G);
+        w.take(rt, A.q + ((int64_t)request * A.B + rl / A.G) * A.q_ld + (int64_t)(hk * A.G + rl % A.G) * D);
+      }
+      const int all_see = in_sight(len, A.B, 0);
+      const uint8_t* k = static_cast<const uint8_t*>(A.k) + hk * head_bytes;
+      const uint8_t* v = static_cast<const uint8_t*>(A.v) + hk * head_bytes;
+      // page ids of this wave's next 64 tiles, a lane each
+      int id0 = 0, id1 = 0, ids_from = -64 * 4;
+      auto load = [&](Keys<D>& x, int t) {
+        t = min(t, t1 - 1);
+        const int pos = first + t * kFewTile;
+        const int nth = (t - ids_from) / 4;
+        const int a = __builtin_amdgcn_readlane(id0, nth), b = __builtin_amdgcn_readlane(id1, nth);
+        const int64_t page = (int64_t)A.Hkv * head_bytes;
+        const int64_t ta = a * page + ((pos & page_mask) >> 4) * mx4_tile_bytes(D);
+        const int next = min(pos + 16, max(len - 1, 0) & ~15);
+        const int64_t tb = b * page + ((next & page_mask) >> 4) * mx4_tile_bytes(D);
+        w.load(x, 0, k + ta, v + ta);
+        w.load(x, 1, k + tb, v + tb);
+      };
+      auto step = [&](Keys<D>& x, int t) {
+        const int pos = first + t * kFewTile;
+        int see[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) see[rt] = vis[rt] - pos;
+        w.step(x, see, len - pos, pos + kFewTile > all_see);
+      };
+      if (len > first) {
+        for (int from = t0 + wave; from < t1; from += 64 * 4) {
+          ids_from = from;
+          const int pos = first + min(from + lane * 4, t1 - 1) * kFewTile;
+          id0 = clamp_page(table[pos >> A.shift], A.n_pages);
+          id1 = clamp_page(table[min(pos + 16, len - 1) >> A.shift], A.n_pages);
+          Keys<D> x, y;
+          load(x, from);
+          load(y, from + 4);
+          const int to = min(from + 64 * 4, t1);
+          for (int t = from; t < to; t += 8) {
+            step(x, t);
+            load(x, min(t + 8, to - 1 - (to - 1 - from) % 4));
+            if (t + 4 < to) {
+              step(y, t + 4);
+              load(y, min(t + 12, to - 1 - (to - 1 - from) % 4));
+            }
+          }
+        }
+      }
+      // the four waves' sums in the first
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) s_m[wave][rt][lane] = w.m[rt];
+      __syncthreads();
+#pragma unroll
+      for (int rt = 0; rt < RT; ++rt) {
+        float top = s_m[0][rt][lane];
+#pragma unroll
+        for (int x = 1; x < 4; ++x) top = fmaxf(top, s_m[x][rt][lane]);
+        w.raise(rt, top);
+        s_l[wave][rt][lane] = w.l[rt];
+      }
+#pragma unroll
+      for (int half = 2; half >= 1; half /= 2) {
+        if (wave >= half && wave < 2 * half)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int x = 0; x < NG * 8; ++x)
+              s_sum[wave - half][rt * NG * 8 + x][lane] = w.o[rt][x / 8][x / 4 % 2][x % 4];
+        __syncthreads();
+        if (wave < half)
+#pragma unroll
+          for (int rt = 0; rt < RT; ++rt)
+#pragma unroll
+            for (int x = 0; x < NG * 8; ++x)
+              w.o[rt][x / 8][x / 4 % 2][x % 4] += s_sum[wave][rt * NG * 8 + x][lane];
+        if (half == 2) __syncthreads();
+      }
+      if (wave == 0) {
+        const int64_t slot = 2 * (int64_t)blockIdx.x + !first_segment;
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) {
+          float l = (s_l[0][rt][lane] + s_l[1][rt][lane]) + (s_l[2][rt][lane] + s_l[3][rt][lane]);
+          l += __shfl_xor(l, 16);
+          l += __shfl_xor(l, 32);
+          const int rl = rt * 16 + w.i;
+          if (rl >= R) continue;
+          float o[NG][8];
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+#pragma unroll
+            for (int x = 0; x < 8; ++x) o[g][x] = l == 0.f ? 0.f : w.o[rt][g][x % 2][x / 2];
+          if (!whole) {
+            float* po = F.po + (slot * R + rl) * D + 8 * w.q;
+#pragma unroll
+            for (int g = 0; g < NG; ++g) {
+              *reinterpret_cast<float4*>(po + 32 * g) = make_float4(o[g][0], o[g][1], o[g][2], o[g][3]);
+              *reinterpret_cast<float4*>(po + 32 * g + 4) =
+                  make_float4(o[g][4], o[g][5], o[g][6], o[g][7]);
+            }
+            if (w.q == 0) F.pml[slot * R + rl] = make_float2(w.unit(rt), l);
+            continue;
+          }
+          const int64_t token = (int64_t)request * A.B + rl / A.G;
+          const int hq = hk * A.G + rl % A.G;
+          const int64_t row = token * A.Hq + hq, rows = (int64_t)A.N * A.B * A.Hq;
+          float m = l == 0.f ? -INFINITY : w.unit(rt);
+          // the shared items' parts of this row, from the launch before this one
+          for (int s = 0; s < A.slots_sh; ++s) {
+            const int64_t from = s * rows + row;
+            const float2 ml = A.pml[from];
+            if (first == 0 || ml.y == 0.f) continue;
+            const float mn = fmaxf(m, ml.x);
+            const float a = __builtin_amdgcn_exp2f(m - mn), b = __builtin_amdgcn_exp2f(ml.x - mn);
+            m = mn;
+            l = l * a + ml.y * b;
+            const float* po = A.po + from * D + 8 * w.q;
+#pragma unroll
+            for (int g = 0; g < NG; ++g)
+#pragma unroll
+              for (int x = 0; x < 8; ++x) o[g][x] = o[g][x] * a + po[32 * g + x] * b;
+          }
+          const float inv = l == 0.f ? 0.f : 1.f / l;
+          uint16_t* out = A.out + token * A.out_ld + (int64_t)hq * D + 8 * w.q;
+#pragma unroll
+          for (int g = 0; g < NG; ++g)
+            *reinterpret_cast<uint4*>(out + 32 * g) = make_uint4(
+                pack2<F16>(o[g][0] * inv, o[g][1] * inv), pack2<F16>(o[g][2] * inv, o[g][3] * inv),
+                pack2<F16>(o[g][4] * inv, o[g][5] * inv), pack2<F16>(o[g][6] * inv, o[g][7] * inv));
+          if (A.lse && w.q == 0) A.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
+        }
+        if (!whole && t0 == 0) {  // cut, and begins here
+          const int64_t g1 = before * A.Hkv + (int64_t)(hk + 1) * tiles;
+          cut = Cut{request * A.Hkv + hk, (int)((g1 - 1) / each - blockIdx.x) + 1, slot};
+        }
+      }
+      __syncthreads();  // the first wave has read the others' sums
+      first_segment = false;
+      at += t1 - t0;
+      if (!F.parts) break;
+    }
+    before += tiles;
+  }
+  if (F.parts && threadIdx.x == 0) F.cut[blockIdx.x] = cut;
+}
+
+// Joins the slots of a pair that was cut, and the shared items' parts: a workgroup a part that such a
+// pair begins in, a row after the other; J groups of threads take every J-th slot.
+template <bool F16, int D> __global__ __launch_bounds__(256) void join_kernel(Few F) {
+  constexpr int LPR = D / 4, J = 256 / LPR;
+  const Args& A = F.a;
+  const Cut cut = F.cut[blockIdx.x];
+  if (cut.slots == 0) return;
+  const int R = A.B * A.G, group = threadIdx.x / LPR, d = threadIdx.x % LPR * 4;
+  const int request = cut.pair / A.Hkv, hk = cut.pair % A.Hkv;
+  const int len = list_len(A, request);
+  const int n_sh = own_begin(len, A.B, A.shared) > 0 ? A.slots_sh : 0;
+  __shared__ Joined s_part[256];
+  for (int r = blockIdx.y; r < R; r += gridDim.y) {
+    const int64_t token = (int64_t)request * A.B + r / A.G;
+    const int hq = hk * A.G + r % A.G;
+    const int64_t row = token * A.Hq + hq, rows = (int64_t)A.N * A.B * A.Hq;
+    Joined all{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+    for (int s0 = group; s0 < cut.slots + n_sh; s0 += 4 * J) {  // four slots' loads in flight
+      float2 ml[4];
+      float4 x[4];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const int s = min(s0 + j * J, cut.slots + n_sh - 1);
+        const int64_t slot = s == 0 ? cut.slot : 2 * ((int64_t)blockIdx.x + s);
+        const int64_t from = (s - cut.slots) * rows + row;
+        ml[j] = s < cut.slots ? F.pml[slot * R + r] : A.pml[from];
+        x[j] = *reinterpret_cast<const float4*>(s < cut.slots ? F.po + (slot * R + r) * D + d
+                                                              : A.po + from * D + d);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (s0 + j * J < cut.slots + n_sh && ml[j].y != 0.f) all.add(ml[j].x, ml[j].y, x[j]);
+    }
+    s_part[threadIdx.x] = all;
+    __syncthreads();
+    if (group == 0) {
+#pragma unroll
+      for (int g = 1; g < J; ++g) {
+        const Joined& p = s_part[threadIdx.x + g * LPR];
+        if (p.l != 0.f) all.add(p.m, p.l, p.o);
+      }
+      const float inv = all.l == 0.f ? 0.f : 1.f / all.l;
+      uint2 w;
+      w.x = pack2<F16>(all.o.x * inv, all.o.y * inv);
+      w.y = pack2<F16>(all.o.z * inv, all.o.w * inv);
+      *reinterpret_cast<uint2*>(A.out + token * A.out_ld + (int64_t)hq * D + d) = w;
+      if (A.lse && d == 0)
+        A.lse[row] = all.l == 0.f ? -INFINITY : (all.m + log2f(all.l)) * 0.69314718056f;
+    }
+    __syncthreads();
+  }
+}
+
+// Slots of few_kernel's parts, of rows that few_kernel takes at all.
+int few_parts(int D, int R) { return kCUs * few_per_cu(D, R <= 16 ? 1 : 2); }
+
+template <bool F16, int D> hipError_t launch_few(Few F, bool wide, hipStream_t s) {
+  Args& A = F.a;
+  const int64_t shared = (int64_t)A.Hkv * A.tiles_sh * A.s_sh;
+  A.slots_sh = A.s_sh;
+  A.step_own = narrow_step(D);
+  A.direct = false;
+  if (shared > 0) {
+    if constexpr (D == 128)
+      if (wide)
+        hipLaunchKernelGGL((attend_kernel<F16, D, kWide, kWideStep, true>), dim3((unsigned)shared),
+                           dim3(kWide * 64), 0, s, A);
+    if (!wide)
+      hipLaunchKernelGGL((attend_kernel<F16, D, kNarrow, narrow_step(D), true>),
+                         dim3((unsigned)shared), dim3(kNarrow * 64), 0, s, A);
+    const hipError_t e = hipGetLastError();
+    if (e != hipSuccess) return e;
+  }
+  const int R = A.B * A.G;
+  const dim3 grid(F.parts ? (unsigned)F.parts : (unsigned)((int64_t)A.N * A.Hkv));
+  if (R <= 16)
+    hipLaunchKernelGGL((few_kernel<F16, D, 1>), grid, dim3(256), 0, s, F);
+  else
+    hipLaunchKernelGGL((few_kernel<F16, D, 2>), grid, dim3(256), 0, s, F);
+  const hipError_t e = hipGetLastError();
+  if (e != hipSuccess || F.parts == 0) return e;
+  hipLaunchKernelGGL((join_kernel<F16, D>), dim3((unsigned)F.parts, (unsigned)R), dim3(256), 0, s, F);
+  return hipGetLastError();
+}
+
+}  // namespace
+
+size_t few_scratch_bytes(const xpress_cache& c, int B, int Hq) {
+  const int R = B * (Hq / c.Hkv);
+  if (R > kFewRows4) return 0;
+  const size_t parts = few_parts(c.D, R);
+  return parts * (2 * (size_t)R * (c.D * sizeof(float) + sizeof(float2)) + sizeof(Cut));
+}
 
 hipError_t launch_block_attention4(const xpress_cache& c, int layer, const void* q, int64_t q_ld,
                                    const int32_t* seq, int N, int B, int Hq, float scale, int shared,
                                    void* out, int64_t out_ld, float* lse, void* ws, hipStream_t s) {
   shared = shared / kTile * kTile;
   const AttendPlan p = plan_of(c, N, B, Hq, shared);
-  const Args A =
-      args_of(c, p, layer, q, q_ld, seq, N, B, Hq, scale, shared, out, out_ld, lse, ws);
-  return launch_values<true>(A, c.D, value_type(c) == XPRESS_F16, p.wide, s);
+  Args A = args_of(c, p, layer, q, q_ld, seq, N, B, Hq, scale, shared, out, out_ld, lse, ws);
+  const bool f16 = value_type(c) == XPRESS_F16;
+  const int R = B * A.G;
+  if (R > kFewRows4) return launch_values<true>(A, c.D, f16, p.wide, s);
+  Few F{A, 0, nullptr, nullptr, nullptr};
+  if (N <= kFewRequests) F.parts = few_parts(c.D, R);
+  // the shared part's slots, then the parts' (the room is attention_scratch_bytes')
+  const size_t rows = (size_t)N * B * Hq;
+  char* at = static_cast<char*>(ws);
+  F.a.po = reinterpret_cast<float*>(at);
+  at += p.s_sh * rows * c.D * sizeof(float);
+  F.a.pml = reinterpret_cast<float2*>(at);
+  at += p.s_sh * rows * sizeof(float2);
+  at = static_cast<char*>(ws) + ((at - static_cast<char*>(ws) + 15) / 16) * 16;
+  F.po = reinterpret_cast<float*>(at);
+  at += 2 * (size_t)F.parts * R * c.D * sizeof(float);
+  F.pml = reinterpret_cast<float2*>(at);
+  F.cut = reinterpret_cast<Cut*>(at + 2 * (size_t)F.parts * R * sizeof(float2));
+  switch (c.D) {
+    case 64: return f16 ? launch_few<true, 64>(F, p.wide, s) : launch_few<false, 64>(F, p.wide, s);
+    case 128: return f16 ? launch_few<true, 128>(F, p.wide, s) : launch_few<false, 128>(F, p.wide, s);
+    default: return f16 ? launch_few<true, 256>(F, p.wide, s) : launch_few<false, 256>(F, p.wide, s);
+  }
 }
 
 }  // namespace xpress

@@ -18,6 +18,8 @@ inline int64_t cache_page_bytes(const xpress_cache& c) {
   return (int64_t)c.Hkv * c.page * c.D * (cache_in_4_bits(c) ? 17 : 64) / 32;
 }
 
+inline size_t up16(size_t x) { return (x + 15) & ~(size_t)15; }
+
 size_t cache_scratch_bytes(const xpress_cache& c, int n_max);
 hipError_t launch_cache_fork(const xpress_cache& c, const int32_t* src, const int32_t* dst, int n,
                              hipStream_t s);
@@ -44,6 +46,8 @@ hipError_t launch_block_attention(const xpress_cache& c, int layer, const void* 
                                   int shared, void* out, int64_t out_ld, float* lse, void* ws,
                                   hipStream_t s);
 
+constexpr int kFewRows4 = 32;  // query rows of a request and head that few_kernel takes
+size_t few_scratch_bytes(const xpress_cache& c, int B, int Hq);
 hipError_t launch_block_attention4(const xpress_cache& c, int layer, const void* q, int64_t q_ld,
                                    const int32_t* seq, int N, int B, int Hq, float scale, int shared,
                                    void* out, int64_t out_ld, float* lse, void* ws, hipStream_t s);
