@@ -7,7 +7,7 @@ namespace xpress {
 size_t attention_scratch_bytes(const xpress_cache& c, int N, int B, int Hq) {
   const size_t slots =
       (size_t)most_row_slots(c, N, B, Hq) * B * Hq * (c.D * sizeof(float) + sizeof(float2));
-  return cache_in_4_bits(c) ? up16(slots) + few_scratch_bytes(c, B, Hq) : slots;
+  return cache_in_4_bits(c) ? up16(slots) + few_scratch_bytes(c, N, B, Hq) : slots;
 }
 
 int64_t attention_items(const xpress_cache& c, int N, int B, int Hq, int shared) {

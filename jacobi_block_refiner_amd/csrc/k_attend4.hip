@@ -8,7 +8,9 @@
 // All (request, head) pairs' tiles of 32 keys form one sequence, which is cut into as many equal parts
 // as there are workgroups on the card, whatever the lengths: a workgroup finds its part from the
 // lengths themselves. A pair that lies in one part is finished there; where it is cut, each part
-// leaves (sums, unit of the weights, their sum) in a slot, and join_kernel joins them.
+// leaves (sums, unit of the weights, their sum) in a slot, and join_kernel joins them. Beside a shared
+// part all pairs leave theirs, and are joined with its items'. (One wave a pair that read the shared
+// slots too took 120 of 133 us at 32 requests behind 4096 tokens.)
 #include "attend_kernel.hpp"
 
 namespace xpress {
@@ -24,8 +26,8 @@ constexpr int few_per_cu(int D, int RT) { return D == 256 ? 3 - RT : RT == 1 ? D
 
 // A pair whose keys lie in several parts: it begins in this one.
 struct Cut {
-  int pair, slots;
-  int64_t slot;  // its first; then 2 (w + 1), 2 (w + 2), ..
+  int pair, slots;  // (0: it is whole, or none begins here)
+  int part, slot;   // where it begins, its slot there; then slots 2 (part + 1), 2 (part + 2), ..
 };
 
 struct Few {
@@ -33,7 +35,7 @@ struct Few {
   int parts;  // workgroups, where the sequence is cut; else 0
   float* po;   // [2 * parts, R, D]
   float2* pml; // [2 * parts, R]
-  Cut* cut;    // [parts]
+  Cut* cut;    // [parts]: the pair that begins there and goes on; beside a shared part [pairs]
 };
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
@@ -62,14 +64,6 @@ template <int N> __device__ __forceinline__ void load_words(const uint8_t* p, ui
   }
 }
 
-// A tile of 32 keys as a lane holds it: two tiles of 16 tokens. With lane = 16 q + i: of K, token i,
-// its q-th quarter of the channels (of 256 channels two eighths); of V, the pairs of channels i of all
-// groups, tokens 4q..4q+3.
-template <int D> struct Keys {
-  static constexpr int NG = D / 32;
-  uint32_t kc[2][NG], ks[2][D == 256 ? 2 : 1], vc[2][NG], vs[2][NG];
-};
-
 // A wave's 16 RT query rows against tiles of 32 keys, all in registers. Scores are formed transposed,
 // S^T = K Q^T (16 keys x 16 queries): a lane holds four keys' of one query, and as weights they are the
 // right operand of O^T = V^T P^T as they stand. The lane's bytes of K are eight channels of each of the
@@ -82,8 +76,15 @@ template <bool F16, int D, int RT> struct FewCore {
   static constexpr float kHuge = 0x1p20f;
 
   int lane, i, q;
+  uint32_t k_at, ks_at, v_at, vs_at;  // the lane's bytes in a tile of 16 tokens
   float c;
+  // A tile of 32 keys as a lane holds it, 16 tokens and 16. With lane = 16 q + i: of K, token i, the
+  // q-th quarter of the channels (of 256 channels two eighths); of V, the pairs of channels i of all
+  // groups, tokens 4q..4q+3.
+  uint32_t kc[2][NG], ks[2][D == 256 ? 2 : 1], vc[2][NG], vs[2][NG];
   s16x8 qf[RT][NG];
+  f32x4v s[RT][2];
+  s16x8 pf[RT];
   f32x4v o[RT][NG][2];  // channels 32g + 8q + 2r (and + 1) of query i
   float m[RT], l[RT], shift[RT];
   uint64_t huge[RT];
@@ -93,6 +94,10 @@ template <bool F16, int D, int RT> struct FewCore {
     i = lane & 15;
     q = lane >> 4;
     c = scale;
+    k_at = i * (D / 2) + q * (D == 256 ? 16 : D / 8);
+    ks_at = mx4_k_scale(D, i, D == 64 ? q / 2 : q);
+    v_at = lane * (D / 8);
+    vs_at = mx4_v_scale(D, 4 * q, 0);
   }
   // Channel of the lane's eight of step s of the product.
   __device__ __forceinline__ int channel(int s) const {
@@ -108,44 +113,52 @@ template <bool F16, int D, int RT> struct FewCore {
     huge[rt] = ~0ull;
   }
 
-  // The lane's part of tile x (of 16 tokens) from one tile of K and of V.
-  __device__ __forceinline__ void load(Keys<D>& t, int x, const uint8_t* k, const uint8_t* v) const {
-    if constexpr (D == 256) {
-      const uint4 a = *reinterpret_cast<const uint4*>(k + i * 128 + q * 16);
-      const uint4 b = *reinterpret_cast<const uint4*>(k + i * 128 + 64 + q * 16);
-      t.kc[x][0] = a.x, t.kc[x][1] = a.y, t.kc[x][2] = a.z, t.kc[x][3] = a.w;
-      t.kc[x][4] = b.x, t.kc[x][5] = b.y, t.kc[x][6] = b.z, t.kc[x][7] = b.w;
-      t.ks[x][0] = k[mx4_k_scale(D, i, q)];
-      t.ks[x][1] = k[mx4_k_scale(D, i, 4 + q)];
-    } else {
-      load_words<NG>(k + i * (D / 2) + q * (D / 8), t.kc[x]);
-      t.ks[x][0] = k[mx4_k_scale(D, i, D == 64 ? q / 2 : q)];
+  // The lane's bytes of tiles of K and of V.
+  __device__ __forceinline__ void load_k(const uint8_t* const (&k)[2]) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      if constexpr (D == 256) {
+        const uint4 a = *reinterpret_cast<const uint4*>(k[x] + k_at);
+        const uint4 b = *reinterpret_cast<const uint4*>(k[x] + (k_at + 64));
+        kc[x][0] = a.x, kc[x][1] = a.y, kc[x][2] = a.z, kc[x][3] = a.w;
+        kc[x][4] = b.x, kc[x][5] = b.y, kc[x][6] = b.z, kc[x][7] = b.w;
+        ks[x][1] = k[x][ks_at + 4];
+      } else {
+        load_words<NG>(k[x] + k_at, kc[x]);
+      }
+      ks[x][0] = k[x][ks_at];
     }
-    load_words<NG>(v + lane * (D / 8), t.vc[x]);
-    load_words<NG>(v + mx4_v_scale(D, 4 * q, 0), t.vs[x]);
+  }
+  __device__ __forceinline__ void load_v(const uint8_t* const (&v)[2]) {
+#pragma unroll
+    for (int x = 0; x < 2; ++x) {
+      load_words<NG>(v[x] + v_at, vc[x]);
+      load_words<NG>(v[x] + vs_at, vs[x]);
+    }
   }
 
-  __device__ __forceinline__ s16x8 k_frag(const Keys<D>& t, int x, int s) const {
-    const float scale = mx4_scale<0>(t.ks[x][D == 256 ? s / 4 : 0]);
-    const uint32_t w = t.kc[x][s];
+  __device__ __forceinline__ s16x8 k_frag(int x, int s) const {
+    const float scale = mx4_scale<0>(ks[x][D == 256 ? s / 4 : 0]);
+    const uint32_t w = kc[x][s];
     return __builtin_bit_cast(s16x8, make_uint4(mx4_pair<F16, 0>(w, scale), mx4_pair<F16, 1>(w, scale),
                                                 mx4_pair<F16, 2>(w, scale), mx4_pair<F16, 3>(w, scale)));
   }
 
-  // Query i of row tile rt sees the tile's keys below vis (a lane's are 4q.. and 16 + 4q..).
-  __device__ __forceinline__ void step(Keys<D>& t, const int (&vis)[RT], int end, bool masked) {
-    f32x4v s[RT][2];
+  // Scores of the tile; weights, where query i of row tile rt sees the keys below vis (a lane's are
+  // 4q.. and 16 + 4q..); their products with its values, `end` keys of which are the row's. Each takes
+  // the tile's bytes out of its registers, and the next tile's loads go there behind it.
+  __device__ __forceinline__ void scores() {
 #pragma unroll
-    for (int x = 0; x < 2; ++x)
+    for (int d = 0; d < NG; ++d)
 #pragma unroll
-      for (int d = 0; d < NG; ++d) {
-        const s16x8 k = k_frag(t, x, d);
+      for (int x = 0; x < 2; ++x) {
+        const s16x8 k = k_frag(x, d);
 #pragma unroll
         for (int rt = 0; rt < RT; ++rt)
           s[rt][x] = mfma16<F16>(k, qf[rt][d], d == 0 ? f32x4v{} : s[rt][x]);
       }
-    __builtin_amdgcn_sched_barrier(0);
-    s16x8 pf[RT];
+  }
+  __device__ __forceinline__ void weights(const int (&vis)[RT], bool masked) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
       if (masked) {
@@ -155,7 +168,7 @@ template <bool F16, int D, int RT> struct FewCore {
           for (int r = 0; r < 4; ++r)
             s[rt][x][r] = 16 * x + 4 * q + r < vis[rt] ? s[rt][x][r] : -INFINITY;
       }
-      rise(rt, s[rt]);
+      rise(rt);
       float sum[2] = {l[rt], 0.f};
       uint32_t w[4];
 #pragma unroll
@@ -168,6 +181,8 @@ template <bool F16, int D, int RT> struct FewCore {
       l[rt] = sum[0] + sum[1];
       pf[rt] = __builtin_bit_cast(s16x8, make_uint4(w[0], w[1], w[2], w[3]));
     }
+  }
+  __device__ __forceinline__ void values(int end, bool masked) {
     if (masked) {
       // keys past the end: a scale of 1, as what lies there could stand for infinity
 #pragma unroll
@@ -175,7 +190,7 @@ template <bool F16, int D, int RT> struct FewCore {
         const int n = min(max(end - 16 * x - 4 * q, 0), 4);
         const uint32_t keep = n == 4 ? ~0u : (1u << 8 * n) - 1;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) t.vs[x][g] = (t.vs[x][g] & keep) | (0x7f7f7f7fu & ~keep);
+        for (int g = 0; g < NG; ++g) vs[x][g] = (vs[x][g] & keep) | (0x7f7f7f7fu & ~keep);
       }
     }
 #pragma unroll
@@ -184,7 +199,7 @@ template <bool F16, int D, int RT> struct FewCore {
       uint32_t even[4], odd[4];
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
-        const uint32_t w = t.vc[x][g], e = t.vs[x][g];
+        const uint32_t w = vc[x][g], e = vs[x][g];
         const uint32_t a = mx4_pair<F16, 0>(w, mx4_scale<0>(e)), b = mx4_pair<F16, 1>(w, mx4_scale<1>(e));
         const uint32_t d = mx4_pair<F16, 2>(w, mx4_scale<2>(e)), f = mx4_pair<F16, 3>(w, mx4_scale<3>(e));
         even[2 * x] = low_halves(a, b), even[2 * x + 1] = low_halves(d, f);
@@ -205,12 +220,12 @@ template <bool F16, int D, int RT> struct FewCore {
 
   // As Core::rise: the sums are rescaled only where some row's maximum grew by more than 2^8 in weight.
   // The four lanes of a query have one maximum; they exchange theirs only then.
-  __device__ __forceinline__ void rise(int rt, f32x4v (&s)[2]) {
-    float top = s[0][0];
+  __device__ __forceinline__ void rise(int rt) {
+    float top = s[rt][0][0];
 #pragma unroll
     for (int x = 0; x < 2; ++x)
 #pragma unroll
-      for (int r = 0; r < 4; ++r) top = fmaxf(top, s[x][r]);
+      for (int r = 0; r < 4; ++r) top = fmaxf(top, s[rt][x][r]);
     if ((__ballot((top - m[rt]) * c > 8.f) | huge[rt]) != 0) {
       top = fmaxf(top, __shfl_xor(top, 16));
       top = fmaxf(top, __shfl_xor(top, 32));
@@ -218,8 +233,8 @@ template <bool F16, int D, int RT> struct FewCore {
       shift[rt] = -unit(rt);
       huge[rt] = __ballot(fabsf(shift[rt]) > kHuge);
       if (huge[rt] != 0) {
-        s[0] -= m[rt];
-        s[1] -= m[rt];
+        s[rt][0] -= m[rt];
+        s[rt][1] -= m[rt];
         shift[rt] = kLift;
       }
     }
@@ -293,7 +308,7 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
     at = blockIdx.x * each;
     end = min(at + each, all);
     if (at >= all) {
-      if (threadIdx.x == 0) F.cut[blockIdx.x].slots = 0;
+      if (threadIdx.x == 0 && A.slots_sh == 0) F.cut[blockIdx.x].slots = 0;
       return;
     }
     if (x * A.Hkv <= at && at < (x + mine) * A.Hkv) {  // the thread of the first request
@@ -320,7 +335,7 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
 
   const int64_t head_bytes = mx4_tiles_bytes(D, A.shift);
   const int page_mask = (1 << A.shift) - 1;
-  Cut cut{0, 0, 0};
+  Cut cut{0, 0, 0, 0};
   bool first_segment = true;
   C w;
   w.begin(A.c);
@@ -356,25 +371,18 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
       const uint8_t* k = static_cast<const uint8_t*>(A.k) + hk * head_bytes;
       const uint8_t* v = static_cast<const uint8_t*>(A.v) + hk * head_bytes;
       // page ids of this wave's next 64 tiles, a lane each
-      int id0 = 0, id1 = 0, ids_from = -64 * 4;
-      auto load = [&](Keys<D>& x, int t) {
-        t = min(t, t1 - 1);
-        const int pos = first + t * kFewTile;
-        const int nth = (t - ids_from) / 4;
-        const int a = __builtin_amdgcn_readlane(id0, nth), b = __builtin_amdgcn_readlane(id1, nth);
+      int id0 = 0, id1 = 0, ids_from = 0;
+      const uint8_t *k_next[2], *v_next[2];
+      auto turn = [&](int t) {
+        const int pos = first + t * kFewTile, nth = (t - ids_from) / 4;
+        const int second = min(pos + 16, (len - 1) & ~15);
         const int64_t page = (int64_t)A.Hkv * head_bytes;
-        const int64_t ta = a * page + ((pos & page_mask) >> 4) * mx4_tile_bytes(D);
-        const int next = min(pos + 16, max(len - 1, 0) & ~15);
-        const int64_t tb = b * page + ((next & page_mask) >> 4) * mx4_tile_bytes(D);
-        w.load(x, 0, k + ta, v + ta);
-        w.load(x, 1, k + tb, v + tb);
-      };
-      auto step = [&](Keys<D>& x, int t) {
-        const int pos = first + t * kFewTile;
-        int see[RT];
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) see[rt] = vis[rt] - pos;
-        w.step(x, see, len - pos, pos + kFewTile > all_see);
+        const int64_t a = __builtin_amdgcn_readlane(id0, nth) * page +
+                          ((pos & page_mask) >> 4) * mx4_tile_bytes(D);
+        const int64_t b = __builtin_amdgcn_readlane(id1, nth) * page +
+                          ((second & page_mask) >> 4) * mx4_tile_bytes(D);
+        k_next[0] = k + a, k_next[1] = k + b;
+        v_next[0] = v + a, v_next[1] = v + b;
       };
       if (len > first) {
         for (int from = t0 + wave; from < t1; from += 64 * 4) {
@@ -382,17 +390,26 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
           const int pos = first + min(from + lane * 4, t1 - 1) * kFewTile;
           id0 = clamp_page(table[pos >> A.shift], A.n_pages);
           id1 = clamp_page(table[min(pos + 16, len - 1) >> A.shift], A.n_pages);
-          Keys<D> x, y;
-          load(x, from);
-          load(y, from + 4);
+          turn(from);
+          w.load_k(k_next);
+          w.load_v(v_next);
           const int to = min(from + 64 * 4, t1);
-          for (int t = from; t < to; t += 8) {
-            step(x, t);
-            load(x, min(t + 8, to - 1 - (to - 1 - from) % 4));
-            if (t + 4 < to) {
-              step(y, t + 4);
-              load(y, min(t + 12, to - 1 - (to - 1 - from) % 4));
-            }
+#pragma unroll 1
+          for (int t = from; t < to; t += 4) {
+            const int at_key = first + t * kFewTile;
+            const bool masked = at_key + kFewTile > all_see;
+            int see[RT];
+#pragma unroll
+            for (int rt = 0; rt < RT; ++rt) see[rt] = vis[rt] - at_key;
+            w.scores();
+            __builtin_amdgcn_sched_barrier(0);
+            turn(t + 4 < to ? t + 4 : t);
+            w.load_k(k_next);
+            __builtin_amdgcn_sched_barrier(0);
+            w.weights(see, masked);
+            w.values(len - at_key, masked);
+            __builtin_amdgcn_sched_barrier(0);
+            w.load_v(v_next);
           }
         }
       }
@@ -439,35 +456,20 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
           for (int g = 0; g < NG; ++g)
 #pragma unroll
             for (int x = 0; x < 8; ++x) o[g][x] = l == 0.f ? 0.f : w.o[rt][g][x % 2][x / 2];
-          if (!whole) {
-            float* po = F.po + (slot * R + rl) * D + 8 * w.q;
+          const int64_t token = (int64_t)request * A.B + rl / A.G;
+          const int hq = hk * A.G + rl % A.G;
+          const int64_t row = token * A.Hq + hq;
+          if (!whole || A.slots_sh) {
+            const int64_t to = whole ? A.slots_sh * (int64_t)A.N * A.B * A.Hq + row : slot * R + rl;
+            float* po = (whole ? A.po : F.po) + to * D + 8 * w.q;
 #pragma unroll
             for (int g = 0; g < NG; ++g) {
               *reinterpret_cast<float4*>(po + 32 * g) = make_float4(o[g][0], o[g][1], o[g][2], o[g][3]);
               *reinterpret_cast<float4*>(po + 32 * g + 4) =
                   make_float4(o[g][4], o[g][5], o[g][6], o[g][7]);
             }
-            if (w.q == 0) F.pml[slot * R + rl] = make_float2(w.unit(rt), l);
+            if (w.q == 0) (whole ? A.pml : F.pml)[to] = make_float2(w.unit(rt), l);
             continue;
-          }
-          const int64_t token = (int64_t)request * A.B + rl / A.G;
-          const int hq = hk * A.G + rl % A.G;
-          const int64_t row = token * A.Hq + hq, rows = (int64_t)A.N * A.B * A.Hq;
-          float m = l == 0.f ? -INFINITY : w.unit(rt);
-          // the shared items' parts of this row, from the launch before this one
-          for (int s = 0; s < A.slots_sh; ++s) {
-            const int64_t from = s * rows + row;
-            const float2 ml = A.pml[from];
-            if (first == 0 || ml.y == 0.f) continue;
-            const float mn = fmaxf(m, ml.x);
-            const float a = __builtin_amdgcn_exp2f(m - mn), b = __builtin_amdgcn_exp2f(ml.x - mn);
-            m = mn;
-            l = l * a + ml.y * b;
-            const float* po = A.po + from * D + 8 * w.q;
-#pragma unroll
-            for (int g = 0; g < NG; ++g)
-#pragma unroll
-              for (int x = 0; x < 8; ++x) o[g][x] = o[g][x] * a + po[32 * g + x] * b;
           }
           const float inv = l == 0.f ? 0.f : 1.f / l;
           uint16_t* out = A.out + token * A.out_ld + (int64_t)hq * D + 8 * w.q;
@@ -476,11 +478,18 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
             *reinterpret_cast<uint4*>(out + 32 * g) = make_uint4(
                 pack2<F16>(o[g][0] * inv, o[g][1] * inv), pack2<F16>(o[g][2] * inv, o[g][3] * inv),
                 pack2<F16>(o[g][4] * inv, o[g][5] * inv), pack2<F16>(o[g][6] * inv, o[g][7] * inv));
-          if (A.lse && w.q == 0) A.lse[row] = l == 0.f ? -INFINITY : (m + log2f(l)) * 0.69314718056f;
+          if (A.lse && w.q == 0)
+            A.lse[row] = l == 0.f ? -INFINITY : (w.unit(rt) + log2f(l)) * 0.69314718056f;
         }
-        if (!whole && t0 == 0) {  // cut, and begins here
+        if (F.parts && t0 == 0) {  // the pair begins here
           const int64_t g1 = before * A.Hkv + (int64_t)(hk + 1) * tiles;
-          cut = Cut{request * A.Hkv + hk, (int)((g1 - 1) / each - blockIdx.x) + 1, slot};
+          const int pair = request * A.Hkv + hk, part = blockIdx.x;
+          const Cut c{pair, whole ? 0 : (int)((g1 - 1) / each - part) + 1, part, (int)slot};
+          if (A.slots_sh) {
+            if (lane == 0) F.cut[pair] = c;
+          } else if (!whole) {
+            cut = c;
+          }
         }
       }
       __syncthreads();  // the first wave has read the others' sums
@@ -490,41 +499,46 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
     }
     before += tiles;
   }
-  if (F.parts && threadIdx.x == 0) F.cut[blockIdx.x] = cut;
+  if (F.parts && A.slots_sh == 0 && threadIdx.x == 0) F.cut[blockIdx.x] = cut;
 }
 
-// Joins the slots of a pair that was cut, and the shared items' parts: a workgroup a part that such a
-// pair begins in, a row after the other; J groups of threads take every J-th slot.
+// Joins the slots of a pair that was cut, a workgroup a part that such a pair begins in; beside a shared
+// part those of every pair and its items'. A row after the other; J groups of threads take every J-th
+// slot.
 template <bool F16, int D> __global__ __launch_bounds__(256) void join_kernel(Few F) {
   constexpr int LPR = D / 4, J = 256 / LPR;
   const Args& A = F.a;
-  const Cut cut = F.cut[blockIdx.x];
-  if (cut.slots == 0) return;
+  Cut cut{(int)blockIdx.x, 0, 0, 0};
+  if (F.parts) cut = F.cut[blockIdx.x];
+  if (cut.slots == 0 && A.slots_sh == 0) return;
   const int R = A.B * A.G, group = threadIdx.x / LPR, d = threadIdx.x % LPR * 4;
   const int request = cut.pair / A.Hkv, hk = cut.pair % A.Hkv;
   const int len = list_len(A, request);
   const int n_sh = own_begin(len, A.B, A.shared) > 0 ? A.slots_sh : 0;
+  const int n = n_sh + max(cut.slots, 1);
+  const int64_t rows = (int64_t)A.N * A.B * A.Hq;
   __shared__ Joined s_part[256];
   for (int r = blockIdx.y; r < R; r += gridDim.y) {
     const int64_t token = (int64_t)request * A.B + r / A.G;
     const int hq = hk * A.G + r % A.G;
-    const int64_t row = token * A.Hq + hq, rows = (int64_t)A.N * A.B * A.Hq;
+    const int64_t row = token * A.Hq + hq;
     Joined all{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int s0 = group; s0 < cut.slots + n_sh; s0 += 4 * J) {  // four slots' loads in flight
+    for (int s0 = group; s0 < n; s0 += 4 * J) {  // four slots' loads in flight
       float2 ml[4];
       float4 x[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const int s = min(s0 + j * J, cut.slots + n_sh - 1);
-        const int64_t slot = s == 0 ? cut.slot : 2 * ((int64_t)blockIdx.x + s);
-        const int64_t from = (s - cut.slots) * rows + row;
-        ml[j] = s < cut.slots ? F.pml[slot * R + r] : A.pml[from];
-        x[j] = *reinterpret_cast<const float4*>(s < cut.slots ? F.po + (slot * R + r) * D + d
-                                                              : A.po + from * D + d);
+        const int s = min(s0 + j * J, n - 1), own = s - n_sh;
+        const bool part = own >= 0 && cut.slots;
+        const int64_t from =
+            part ? (own == 0 ? cut.slot : 2 * ((int64_t)cut.part + own)) * R + r
+                 : (own >= 0 ? A.slots_sh : s) * rows + row;
+        ml[j] = (part ? F.pml : A.pml)[from];
+        x[j] = *reinterpret_cast<const float4*>((part ? F.po : A.po) + from * D + d);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
-        if (s0 + j * J < cut.slots + n_sh && ml[j].y != 0.f) all.add(ml[j].x, ml[j].y, x[j]);
+        if (s0 + j * J < n && ml[j].y != 0.f) all.add(ml[j].x, ml[j].y, x[j]);
     }
     s_part[threadIdx.x] = all;
     __syncthreads();
@@ -573,18 +587,19 @@ template <bool F16, int D> hipError_t launch_few(Few F, bool wide, hipStream_t s
   else
     hipLaunchKernelGGL((few_kernel<F16, D, 2>), grid, dim3(256), 0, s, F);
   const hipError_t e = hipGetLastError();
-  if (e != hipSuccess || F.parts == 0) return e;
-  hipLaunchKernelGGL((join_kernel<F16, D>), dim3((unsigned)F.parts, (unsigned)R), dim3(256), 0, s, F);
+  if (e != hipSuccess || (F.parts == 0 && shared == 0)) return e;
+  const int64_t joined = shared ? (int64_t)A.N * A.Hkv : F.parts;
+  hipLaunchKernelGGL((join_kernel<F16, D>), dim3((unsigned)joined, (unsigned)R), dim3(256), 0, s, F);
   return hipGetLastError();
 }
 
 }  // namespace
 
-size_t few_scratch_bytes(const xpress_cache& c, int B, int Hq) {
+size_t few_scratch_bytes(const xpress_cache& c, int N, int B, int Hq) {
   const int R = B * (Hq / c.Hkv);
   if (R > kFewRows4) return 0;
-  const size_t parts = few_parts(c.D, R);
-  return parts * (2 * (size_t)R * (c.D * sizeof(float) + sizeof(float2)) + sizeof(Cut));
+  const size_t parts = few_parts(c.D, R), pairs = (size_t)std::min(N, kFewRequests) * c.Hkv;
+  return parts * 2 * R * (c.D * sizeof(float) + sizeof(float2)) + std::max(parts, pairs) * sizeof(Cut);
 }
 
 hipError_t launch_block_attention4(const xpress_cache& c, int layer, const void* q, int64_t q_ld,
@@ -598,18 +613,15 @@ hipError_t launch_block_attention4(const xpress_cache& c, int layer, const void*
   if (R > kFewRows4) return launch_values<true>(A, c.D, f16, p.wide, s);
   Few F{A, 0, nullptr, nullptr, nullptr};
   if (N <= kFewRequests) F.parts = few_parts(c.D, R);
-  // the shared part's slots, then the parts' (the room is attention_scratch_bytes')
-  const size_t rows = (size_t)N * B * Hq;
-  char* at = static_cast<char*>(ws);
-  F.a.po = reinterpret_cast<float*>(at);
-  at += p.s_sh * rows * c.D * sizeof(float);
-  F.a.pml = reinterpret_cast<float2*>(at);
-  at += p.s_sh * rows * sizeof(float2);
-  at = static_cast<char*>(ws) + ((at - static_cast<char*>(ws) + 15) / 16) * 16;
-  F.po = reinterpret_cast<float*>(at);
-  at += 2 * (size_t)F.parts * R * c.D * sizeof(float);
-  F.pml = reinterpret_cast<float2*>(at);
-  F.cut = reinterpret_cast<Cut*>(at + 2 * (size_t)F.parts * R * sizeof(float2));
+  // the shared part's slots and one of every row, then the parts' (attention_scratch_bytes has room)
+  const size_t rows = (size_t)N * B * Hq, slots = rows * (p.s_sh ? p.s_sh + 1 : 0);
+  F.a.po = static_cast<float*>(ws);
+  F.a.pml = reinterpret_cast<float2*>(F.a.po + slots * c.D);
+  F.po = reinterpret_cast<float*>(static_cast<char*>(ws) +
+                                  up16(slots * (c.D * sizeof(float) + sizeof(float2))));
+  F.cut = reinterpret_cast<Cut*>(F.po + 2 * (size_t)F.parts * R * c.D);
+  const size_t cuts = p.s_sh ? (size_t)N * c.Hkv : F.parts;
+  F.pml = reinterpret_cast<float2*>(F.cut + (F.parts ? cuts : 0));
   switch (c.D) {
     case 64: return f16 ? launch_few<true, 64>(F, p.wide, s) : launch_few<false, 64>(F, p.wide, s);
     case 128: return f16 ? launch_few<true, 128>(F, p.wide, s) : launch_few<false, 128>(F, p.wide, s);
