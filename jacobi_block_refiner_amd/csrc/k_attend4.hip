@@ -6,8 +6,8 @@
 // matrix core's registers.
 //
 // All (request, head) pairs' tiles of 32 keys form one sequence, which is cut into as many equal parts
-// as there are workgroups on the card, whatever the lengths: a workgroup finds its part from the
-// lengths themselves. A pair that lies in one part is finished there; where it is cut, each part
+// as there are waves on the card, whatever the lengths: a wave finds its part from the lengths
+// themselves. A pair that lies in one part is finished there; where it is cut, each part
 // leaves (sums, unit of the weights, their sum) in a slot, and join_kernel joins them. Beside a shared
 // part all pairs leave theirs, and are joined with its items'. (One wave a pair that read the shared
 // slots too took 120 of 133 us at 32 requests behind 4096 tokens.)
@@ -18,8 +18,8 @@ namespace xpress {
 namespace {
 
 constexpr int kFewTile = 32;   // keys of a step of a wave
-constexpr int kFewLeast = 4;   // tiles of a part at least: one a wave
-constexpr int kFewRequests = 4096;  // more are not cut: a workgroup a pair
+constexpr int kFewLeast = 2;   // tiles of a part at least
+constexpr int kFewRequests = 4096;  // more are not cut: a wave a pair
 
 // Workgroups of few_kernel on a CU, by its registers.
 constexpr int few_per_cu(int D, int RT) { return D == 256 ? 3 - RT : RT == 1 ? D == 64 ? 4 : 3 : 2; }
@@ -32,7 +32,7 @@ struct Cut {
 
 struct Few {
   Args a;
-  int parts;  // workgroups, where the sequence is cut; else 0
+  int parts;  // waves, where the sequence is cut; else 0
   float* po;   // [2 * parts, R, D]
   float2* pml; // [2 * parts, R]
   Cut* cut;    // [parts]: the pair that begins there and goes on; beside a shared part [pairs]
@@ -259,35 +259,29 @@ __device__ __forceinline__ int64_t scalar(int64_t x) {
 }
 
 // Tiles of a request's own keys (one at least: it writes what the request has without them).
-__device__ __forceinline__ int own_tiles(int len, int first) {
-  return max((len - first + kFewTile - 1) / kFewTile, 1);
+__device__ __forceinline__ int own_tiles(const Args& A, int len) {
+  return max((len - own_begin(len, A.B, A.shared) + kFewTile - 1) / kFewTile, 1);
 }
 
 template <bool F16, int D, int RT>
 __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
-  using C = FewCore<F16, D, RT>;
-  constexpr int NG = C::NG, LW = RT * NG * 8;  // sums of a lane
+  constexpr int NG = D / 32;
   const Args& A = F.a;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), lane = threadIdx.x & 63;
+  const int wave = scalar((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int R = A.B * A.G;
-  __shared__ float s_sum[2][LW][64];
-  __shared__ float s_m[4][RT][64], s_l[4][RT][64];
-  __shared__ int64_t s_scan[4], s_before;
-  __shared__ int s_request;
 
-  // this workgroup's part of the sequence: tiles [at, end) of all, beginning in a request with `before`
+  // this wave's part of the sequence: tiles [at, end) of all, beginning in a request with `before`
   // tiles a head in front of it
-  int64_t at, end, before, each = 0;
+  const int part = blockIdx.x * 4 + wave;
+  int64_t at, end, before = 0, each = 0;
   int request;
   if (F.parts) {
+    __shared__ int64_t s_scan[4], s_before[4];
+    __shared__ int s_request[4];
     // each thread a run of requests
     const int per = (A.N + 255) / 256, r0 = threadIdx.x * per;
     int64_t mine = 0;
-    for (int j = 0; j < per; ++j)
-      if (r0 + j < A.N) {
-        const int len = list_len(A, r0 + j);
-        mine += own_tiles(len, own_begin(len, A.B, A.shared));
-      }
+    for (int r = r0; r < min(r0 + per, A.N); ++r) mine += own_tiles(A, list_len(A, r));
     int64_t x = mine;
 #pragma unroll
     for (int d = 1; d < 64; d *= 2) {
@@ -305,97 +299,91 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
     }
     all = scalar(all) * A.Hkv;
     each = max((all + F.parts - 1) / F.parts, (int64_t)kFewLeast);
-    at = blockIdx.x * each;
-    end = min(at + each, all);
-    if (at >= all) {
-      if (threadIdx.x == 0 && A.slots_sh == 0) F.cut[blockIdx.x].slots = 0;
-      return;
-    }
-    if (x * A.Hkv <= at && at < (x + mine) * A.Hkv) {  // the thread of the first request
-      for (int j = 0; j < per; ++j) {
-        const int len = list_len(A, r0 + j);
-        const int n = own_tiles(len, own_begin(len, A.B, A.shared));
-        if (at < (x + n) * A.Hkv) {
-          s_request = r0 + j;
-          s_before = x;
-          break;
-        }
-        x += n;
+#pragma unroll
+    for (int w = 0; w < 4; ++w) {  // the thread of the request in which wave w's part begins
+      const int64_t from = (blockIdx.x * 4 + w) * each;
+      if (from < x * A.Hkv || from >= (x + mine) * A.Hkv) continue;
+      int r = r0;
+      int64_t y = x;
+      for (;; ++r) {
+        const int n = own_tiles(A, list_len(A, r));
+        if (from < (y + n) * A.Hkv) break;
+        y += n;
       }
+      s_request[w] = r;
+      s_before[w] = y;
     }
     __syncthreads();
-    request = scalar(s_request);
-    before = scalar(s_before);
+    at = part * each;
+    end = min(at + each, all);
+    if (at >= all) {
+      if (lane == 0 && A.slots_sh == 0) F.cut[part].slots = 0;
+      return;
+    }
+    request = scalar(s_request[wave]);
+    before = scalar(s_before[wave]);
   } else {
-    request = blockIdx.x / A.Hkv;
-    before = 0;
-    at = blockIdx.x % A.Hkv;  // (of the request's pairs)
+    if (part >= (int64_t)A.N * A.Hkv) return;
+    request = part / A.Hkv;
+    at = part % A.Hkv;  // (of the request's pairs)
     end = at + 1;
   }
 
-  const int64_t head_bytes = mx4_tiles_bytes(D, A.shift);
+  const int64_t head_bytes = mx4_tiles_bytes(D, A.shift), page_bytes = A.Hkv * head_bytes;
   const int page_mask = (1 << A.shift) - 1;
   Cut cut{0, 0, 0, 0};
-  bool first_segment = true;
-  C w;
+  int slot = 2 * part;  // of the first pair here, then of the others (whole ones leave it alone)
+  FewCore<F16, D, RT> w;
   w.begin(A.c);
   for (; at < end && request < A.N; ++request) {
     const int row = scalar(list_row(A, request));
     const int len = row < 0 ? 0 : clamp_len(scalar(A.len[row]), A.ld, A.shift);
-    const int first = own_begin(len, A.B, A.shared);
-    const int tiles = own_tiles(len, first);
+    const int first = own_begin(len, A.B, A.shared), tiles = own_tiles(A, len);
+    const int all_see = in_sight(len, A.B, 0);
     const int32_t* table = A.table + (int64_t)max(row, 0) * A.ld;
     while (at < end) {
-      int hk, t0, t1;
+      int hk = (int)at, t0 = 0, t1 = tiles;
       if (F.parts) {
-        const int64_t in = at - before * A.Hkv;  // tiles of this request before `at`
+        const int64_t in = at - before * A.Hkv;  // tiles of this request in front
         if (in >= (int64_t)tiles * A.Hkv) break;
         hk = (int)(in / tiles);
         t0 = (int)(in % tiles);
         t1 = (int)min((int64_t)tiles, t0 + (end - at));
-      } else {
-        hk = (int)at;
-        t0 = 0;
-        t1 = tiles;
       }
-      const int whole = t0 == 0 && t1 == tiles;
-      // the rows
+      const bool whole = t0 == 0 && t1 == tiles;
       int vis[RT];
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
         const int rl = min(rt * 16 + w.i, R - 1);
         vis[rt] = in_sight(len, A.B, rl / A.G);
-        w.take(rt, A.q + ((int64_t)request * A.B + rl / A.G) * A.q_ld + (int64_t)(hk * A.G + rl % A.G) * D);
+        w.take(rt, A.q + ((int64_t)request * A.B + rl / A.G) * A.q_ld +
+                       (int64_t)(hk * A.G + rl % A.G) * D);
       }
-      const int all_see = in_sight(len, A.B, 0);
       const uint8_t* k = static_cast<const uint8_t*>(A.k) + hk * head_bytes;
       const uint8_t* v = static_cast<const uint8_t*>(A.v) + hk * head_bytes;
-      // page ids of this wave's next 64 tiles, a lane each
-      int id0 = 0, id1 = 0, ids_from = 0;
+      // page ids of the next 64 tiles, a lane each
+      int id0 = 0, id1 = 0;
       const uint8_t *k_next[2], *v_next[2];
-      auto turn = [&](int t) {
-        const int pos = first + t * kFewTile, nth = (t - ids_from) / 4;
-        const int second = min(pos + 16, (len - 1) & ~15);
-        const int64_t page = (int64_t)A.Hkv * head_bytes;
-        const int64_t a = __builtin_amdgcn_readlane(id0, nth) * page +
+      auto turn = [&](int t, int nth) {
+        const int pos = first + t * kFewTile, second = min(pos + 16, (len - 1) & ~15);
+        const int64_t a = __builtin_amdgcn_readlane(id0, nth) * page_bytes +
                           ((pos & page_mask) >> 4) * mx4_tile_bytes(D);
-        const int64_t b = __builtin_amdgcn_readlane(id1, nth) * page +
+        const int64_t b = __builtin_amdgcn_readlane(id1, nth) * page_bytes +
                           ((second & page_mask) >> 4) * mx4_tile_bytes(D);
         k_next[0] = k + a, k_next[1] = k + b;
         v_next[0] = v + a, v_next[1] = v + b;
       };
       if (len > first) {
-        for (int from = t0 + wave; from < t1; from += 64 * 4) {
-          ids_from = from;
-          const int pos = first + min(from + lane * 4, t1 - 1) * kFewTile;
+        for (int from = t0; from < t1; from += 64) {
+          const int pos = first + min(from + lane, t1 - 1) * kFewTile;
           id0 = clamp_page(table[pos >> A.shift], A.n_pages);
           id1 = clamp_page(table[min(pos + 16, len - 1) >> A.shift], A.n_pages);
-          turn(from);
+          const int to = min(from + 64, t1);
+          turn(from, 0);
           w.load_k(k_next);
           w.load_v(v_next);
-          const int to = min(from + 64 * 4, t1);
 #pragma unroll 1
-          for (int t = from; t < to; t += 4) {
+          for (int t = from; t < to; ++t) {
             const int at_key = first + t * kFewTile;
             const bool masked = at_key + kFewTile > all_see;
             int see[RT];
@@ -403,7 +391,8 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
             for (int rt = 0; rt < RT; ++rt) see[rt] = vis[rt] - at_key;
             w.scores();
             __builtin_amdgcn_sched_barrier(0);
-            turn(t + 4 < to ? t + 4 : t);
+            const int next = min(t + 1, to - 1);
+            turn(next, next - from);
             w.load_k(k_next);
             __builtin_amdgcn_sched_barrier(0);
             w.weights(see, masked);
@@ -413,93 +402,61 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
           }
         }
       }
-      // the four waves' sums in the first
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) s_m[wave][rt][lane] = w.m[rt];
-      __syncthreads();
 #pragma unroll
       for (int rt = 0; rt < RT; ++rt) {
-        float top = s_m[0][rt][lane];
+        float l = w.l[rt];
+        l += __shfl_xor(l, 16);
+        l += __shfl_xor(l, 32);
+        const int rl = rt * 16 + w.i;
+        if (rl >= R) continue;
+        float o[NG][8];
 #pragma unroll
-        for (int x = 1; x < 4; ++x) top = fmaxf(top, s_m[x][rt][lane]);
-        w.raise(rt, top);
-        s_l[wave][rt][lane] = w.l[rt];
-      }
+        for (int g = 0; g < NG; ++g)
 #pragma unroll
-      for (int half = 2; half >= 1; half /= 2) {
-        if (wave >= half && wave < 2 * half)
+          for (int x = 0; x < 8; ++x) o[g][x] = l == 0.f ? 0.f : w.o[rt][g][x % 2][x / 2];
+        const int64_t token = (int64_t)request * A.B + rl / A.G;
+        const int hq = hk * A.G + rl % A.G;
+        const int64_t out_row = token * A.Hq + hq;
+        if (!whole || A.slots_sh) {
+          const int64_t to = whole ? A.slots_sh * (int64_t)A.N * A.B * A.Hq + out_row
+                                   : (int64_t)slot * R + rl;
+          float* po = (whole ? A.po : F.po) + to * D + 8 * w.q;
 #pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int x = 0; x < NG * 8; ++x)
-              s_sum[wave - half][rt * NG * 8 + x][lane] = w.o[rt][x / 8][x / 4 % 2][x % 4];
-        __syncthreads();
-        if (wave < half)
-#pragma unroll
-          for (int rt = 0; rt < RT; ++rt)
-#pragma unroll
-            for (int x = 0; x < NG * 8; ++x)
-              w.o[rt][x / 8][x / 4 % 2][x % 4] += s_sum[wave][rt * NG * 8 + x][lane];
-        if (half == 2) __syncthreads();
-      }
-      if (wave == 0) {
-        const int64_t slot = 2 * (int64_t)blockIdx.x + !first_segment;
-#pragma unroll
-        for (int rt = 0; rt < RT; ++rt) {
-          float l = (s_l[0][rt][lane] + s_l[1][rt][lane]) + (s_l[2][rt][lane] + s_l[3][rt][lane]);
-          l += __shfl_xor(l, 16);
-          l += __shfl_xor(l, 32);
-          const int rl = rt * 16 + w.i;
-          if (rl >= R) continue;
-          float o[NG][8];
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-#pragma unroll
-            for (int x = 0; x < 8; ++x) o[g][x] = l == 0.f ? 0.f : w.o[rt][g][x % 2][x / 2];
-          const int64_t token = (int64_t)request * A.B + rl / A.G;
-          const int hq = hk * A.G + rl % A.G;
-          const int64_t row = token * A.Hq + hq;
-          if (!whole || A.slots_sh) {
-            const int64_t to = whole ? A.slots_sh * (int64_t)A.N * A.B * A.Hq + row : slot * R + rl;
-            float* po = (whole ? A.po : F.po) + to * D + 8 * w.q;
-#pragma unroll
-            for (int g = 0; g < NG; ++g) {
-              *reinterpret_cast<float4*>(po + 32 * g) = make_float4(o[g][0], o[g][1], o[g][2], o[g][3]);
-              *reinterpret_cast<float4*>(po + 32 * g + 4) =
-                  make_float4(o[g][4], o[g][5], o[g][6], o[g][7]);
-            }
-            if (w.q == 0) (whole ? A.pml : F.pml)[to] = make_float2(w.unit(rt), l);
-            continue;
+          for (int g = 0; g < NG; ++g) {
+            *reinterpret_cast<float4*>(po + 32 * g) = make_float4(o[g][0], o[g][1], o[g][2], o[g][3]);
+            *reinterpret_cast<float4*>(po + 32 * g + 4) =
+                make_float4(o[g][4], o[g][5], o[g][6], o[g][7]);
           }
-          const float inv = l == 0.f ? 0.f : 1.f / l;
-          uint16_t* out = A.out + token * A.out_ld + (int64_t)hq * D + 8 * w.q;
-#pragma unroll
-          for (int g = 0; g < NG; ++g)
-            *reinterpret_cast<uint4*>(out + 32 * g) = make_uint4(
-                pack2<F16>(o[g][0] * inv, o[g][1] * inv), pack2<F16>(o[g][2] * inv, o[g][3] * inv),
-                pack2<F16>(o[g][4] * inv, o[g][5] * inv), pack2<F16>(o[g][6] * inv, o[g][7] * inv));
-          if (A.lse && w.q == 0)
-            A.lse[row] = l == 0.f ? -INFINITY : (w.unit(rt) + log2f(l)) * 0.69314718056f;
+          if (w.q == 0) (whole ? A.pml : F.pml)[to] = make_float2(w.unit(rt), l);
+          continue;
         }
-        if (F.parts && t0 == 0) {  // the pair begins here
-          const int64_t g1 = before * A.Hkv + (int64_t)(hk + 1) * tiles;
-          const int pair = request * A.Hkv + hk, part = blockIdx.x;
-          const Cut c{pair, whole ? 0 : (int)((g1 - 1) / each - part) + 1, part, (int)slot};
-          if (A.slots_sh) {
-            if (lane == 0) F.cut[pair] = c;
-          } else if (!whole) {
-            cut = c;
-          }
+        const float inv = l == 0.f ? 0.f : 1.f / l;
+        uint16_t* out = A.out + token * A.out_ld + (int64_t)hq * D + 8 * w.q;
+#pragma unroll
+        for (int g = 0; g < NG; ++g)
+          *reinterpret_cast<uint4*>(out + 32 * g) = make_uint4(
+              pack2<F16>(o[g][0] * inv, o[g][1] * inv), pack2<F16>(o[g][2] * inv, o[g][3] * inv),
+              pack2<F16>(o[g][4] * inv, o[g][5] * inv), pack2<F16>(o[g][6] * inv, o[g][7] * inv));
+        if (A.lse && w.q == 0)
+          A.lse[out_row] = l == 0.f ? -INFINITY : (w.unit(rt) + log2f(l)) * 0.69314718056f;
+      }
+      if (F.parts && t0 == 0) {  // the pair begins here
+        const int64_t g1 = before * A.Hkv + (int64_t)(hk + 1) * tiles;
+        const int pair = request * A.Hkv + hk;
+        const Cut c{pair, whole ? 0 : (int)((g1 - 1) / each - part) + 1, part, slot};
+        if (A.slots_sh) {
+          if (lane == 0) F.cut[pair] = c;
+        } else if (!whole) {
+          cut = c;
         }
       }
-      __syncthreads();  // the first wave has read the others' sums
-      first_segment = false;
+      slot = 2 * part + 1;
       at += t1 - t0;
       if (!F.parts) break;
     }
     before += tiles;
   }
-  if (F.parts && A.slots_sh == 0 && threadIdx.x == 0) F.cut[blockIdx.x] = cut;
+  if (F.parts && A.slots_sh == 0 && lane == 0) F.cut[part] = cut;
 }
 
 // Joins the slots of a pair that was cut, a workgroup a part that such a pair begins in; beside a shared
@@ -561,7 +518,7 @@ template <bool F16, int D> __global__ __launch_bounds__(256) void join_kernel(Fe
 }
 
 // Slots of few_kernel's parts, of rows that few_kernel takes at all.
-int few_parts(int D, int R) { return kCUs * few_per_cu(D, R <= 16 ? 1 : 2); }
+int few_parts(int D, int R) { return kCUs * 4 * few_per_cu(D, R <= 16 ? 1 : 2); }
 
 template <bool F16, int D> hipError_t launch_few(Few F, bool wide, hipStream_t s) {
   Args& A = F.a;
@@ -581,7 +538,7 @@ template <bool F16, int D> hipError_t launch_few(Few F, bool wide, hipStream_t s
     if (e != hipSuccess) return e;
   }
   const int R = A.B * A.G;
-  const dim3 grid(F.parts ? (unsigned)F.parts : (unsigned)((int64_t)A.N * A.Hkv));
+  const dim3 grid((unsigned)(F.parts ? F.parts / 4 : ((int64_t)A.N * A.Hkv + 3) / 4));
   if (R <= 16)
     hipLaunchKernelGGL((few_kernel<F16, D, 1>), grid, dim3(256), 0, s, F);
   else
