@@ -507,9 +507,8 @@ template <int N, bool MX4> __device__ __forceinline__ void feed() {
 // 20480 rows a head, 16384 keys, 8 heads: 1310 to 1400 us, 1.0 PFLOP/s at 1.9 to 2.0 GHz (the power
 // limit takes the rest of 2.3), the matrix core busy 47% of the cycles; 2560 rows, 8192 keys: 104 us, 0.8
 // PFLOP/s on 240 CUs.
-template <bool F16, int D, int NW, int KT, bool MX4 = false>
-__global__ __launch_bounds__(NW * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void attend_kernel(
-    Args A) {
+template <bool F16, int D, int NW, int KT, bool MX4>
+__device__ __forceinline__ void attend_item(const Args& A, int id) {
   constexpr bool WIDE = NW == kWide;
   using C = Core<F16, D, KT, MX4>;
   using S = std::conditional_t<MX4, Source4<F16, D, KT, NW, WIDE>, Source<D, KT, NW>>;
@@ -524,7 +523,6 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void atte
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
 
   // the item
-  int id = blockIdx.x;
   const int n_sh = A.Hkv * A.tiles_sh * A.s_sh;
   const bool is_shared = WIDE || id < n_sh;
   int hk, tile, slot, req, kbeg, kend, nrows;
@@ -818,6 +816,13 @@ __global__ __launch_bounds__(NW * 64, D == 256 ? 1 : D == 128 ? 2 : 3) void atte
       *reinterpret_cast<float4*>(op + dt * 32 + 8 * i) =
           make_float4(w.o[dt][4 * i], w.o[dt][4 * i + 1], w.o[dt][4 * i + 2], w.o[dt][4 * i + 3]);
   if (h == 0) A.pml[at] = make_float2(w.unit(), l);
+}
+
+constexpr int narrow_per_cu(int D) { return D == 256 ? 1 : D == 128 ? 2 : 3; }
+
+template <bool F16, int D, int NW, int KT, bool MX4 = false>
+__global__ __launch_bounds__(NW * 64, narrow_per_cu(D)) void attend_kernel(Args A) {
+  attend_item<F16, D, NW, KT, MX4>(A, blockIdx.x);
 }
 
 // Joins a row's items: weights relative to the largest maximum. J groups of threads take every J-th

@@ -22,7 +22,7 @@ constexpr int kFewLeast = 2;   // tiles of a part at least
 constexpr int kFewRequests = 4096;  // more are not cut: a wave a pair
 
 // Workgroups of few_kernel on a CU, by its registers.
-constexpr int few_per_cu(int D, int RT) { return D == 256 ? 3 - RT : RT == 1 ? D == 64 ? 4 : 3 : 2; }
+constexpr int few_per_cu(int D, int RT) { return D == 256 ? 3 - RT : 2; }
 
 // A pair whose keys lie in several parts: it begins in this one.
 struct Cut {
@@ -33,9 +33,10 @@ struct Cut {
 struct Few {
   Args a;
   int parts;  // waves, where the sequence is cut; else 0
+  bool by_pair;  // cut[] is of the pairs; else of the parts: of the pair that begins there and goes on
   float* po;   // [2 * parts, R, D]
   float2* pml; // [2 * parts, R]
-  Cut* cut;    // [parts]: the pair that begins there and goes on; beside a shared part [pairs]
+  Cut* cut;
 };
 
 typedef float f32x4v __attribute__((ext_vector_type(4)));
@@ -113,8 +114,14 @@ template <bool F16, int D, int RT> struct FewCore {
     huge[rt] = ~0ull;
   }
 
-  // The lane's bytes of tiles of K and of V.
+  // The lane's bytes of tiles of K and of V. (A scalar base and a 32-bit offset of the lane, as long as
+  // the compiler does not widen the offset ahead of the loop.)
+  static __device__ __forceinline__ uint32_t here(uint32_t offset) {
+    asm volatile("" : "+v"(offset));
+    return offset;
+  }
   __device__ __forceinline__ void load_k(const uint8_t* const (&k)[2]) {
+    const uint32_t k_at = here(this->k_at), ks_at = here(this->ks_at);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       if constexpr (D == 256) {
@@ -130,6 +137,7 @@ template <bool F16, int D, int RT> struct FewCore {
     }
   }
   __device__ __forceinline__ void load_v(const uint8_t* const (&v)[2]) {
+    const uint32_t v_at = here(this->v_at), vs_at = here(this->vs_at);
 #pragma unroll
     for (int x = 0; x < 2; ++x) {
       load_words<NG>(v[x] + v_at, vc[x]);
@@ -149,7 +157,8 @@ template <bool F16, int D, int RT> struct FewCore {
   // the tile's bytes out of its registers, and the next tile's loads go there behind it.
   __device__ __forceinline__ void scores() {
 #pragma unroll
-    for (int d = 0; d < NG; ++d)
+    for (int d = 0; d < NG; ++d) {
+      __builtin_amdgcn_sched_barrier(0);
 #pragma unroll
       for (int x = 0; x < 2; ++x) {
         const s16x8 k = k_frag(x, d);
@@ -157,6 +166,7 @@ template <bool F16, int D, int RT> struct FewCore {
         for (int rt = 0; rt < RT; ++rt)
           s[rt][x] = mfma16<F16>(k, qf[rt][d], d == 0 ? f32x4v{} : s[rt][x]);
       }
+    }
   }
   __device__ __forceinline__ void weights(const int (&vis)[RT], bool masked) {
 #pragma unroll
@@ -264,7 +274,7 @@ __device__ __forceinline__ int own_tiles(const Args& A, int len) {
 }
 
 template <bool F16, int D, int RT>
-__global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
+__device__ __forceinline__ void few_part(const Few& F, int block) {
   constexpr int NG = D / 32;
   const Args& A = F.a;
   const int wave = scalar((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
@@ -272,7 +282,7 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
 
   // this wave's part of the sequence: tiles [at, end) of all, beginning in a request with `before`
   // tiles a head in front of it
-  const int part = blockIdx.x * 4 + wave;
+  const int part = block * 4 + wave;
   int64_t at, end, before = 0, each = 0;
   int request;
   if (F.parts) {
@@ -301,7 +311,7 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
     each = max((all + F.parts - 1) / F.parts, (int64_t)kFewLeast);
 #pragma unroll
     for (int w = 0; w < 4; ++w) {  // the thread of the request in which wave w's part begins
-      const int64_t from = (blockIdx.x * 4 + w) * each;
+      const int64_t from = (block * 4 + w) * each;
       if (from < x * A.Hkv || from >= (x + mine) * A.Hkv) continue;
       int r = r0;
       int64_t y = x;
@@ -317,7 +327,7 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
     at = part * each;
     end = min(at + each, all);
     if (at >= all) {
-      if (lane == 0 && A.slots_sh == 0) F.cut[part].slots = 0;
+      if (lane == 0 && !F.by_pair) F.cut[part].slots = 0;
       return;
     }
     request = scalar(s_request[wave]);
@@ -444,7 +454,7 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
         const int64_t g1 = before * A.Hkv + (int64_t)(hk + 1) * tiles;
         const int pair = request * A.Hkv + hk;
         const Cut c{pair, whole ? 0 : (int)((g1 - 1) / each - part) + 1, part, slot};
-        if (A.slots_sh) {
+        if (F.by_pair) {
           if (lane == 0) F.cut[pair] = c;
         } else if (!whole) {
           cut = c;
@@ -456,12 +466,27 @@ __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
     }
     before += tiles;
   }
-  if (F.parts && A.slots_sh == 0 && lane == 0) F.cut[part] = cut;
+  if (F.parts && !F.by_pair && lane == 0) F.cut[part] = cut;
 }
 
-// Joins the slots of a pair that was cut, a workgroup a part that such a pair begins in; beside a shared
-// part those of every pair and its items'. A row after the other; J groups of threads take every J-th
-// slot.
+template <bool F16, int D, int RT>
+__global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
+  few_part<F16, D, RT>(F, blockIdx.x);
+}
+
+// The shared part's narrow items beside them.
+template <bool F16, int D, int RT>
+__global__ __launch_bounds__(256, narrow_per_cu(D)) void beside_kernel(Few F) {
+  const int items = F.a.Hkv * F.a.tiles_sh * F.a.s_sh;
+  if ((int)blockIdx.x < items)
+    attend_item<F16, D, kNarrow, narrow_step(D), true>(F.a, blockIdx.x);
+  else
+    few_part<F16, D, RT>(F, blockIdx.x - items);
+}
+
+// Joins the slots of a pair that was cut, and the shared items' of every pair: a workgroup a row of a
+// pair, or of the pair that begins in a part where there are more pairs than parts (and no shared
+// items). J groups of threads take every J-th slot.
 template <bool F16, int D> __global__ __launch_bounds__(256) void join_kernel(Few F) {
   constexpr int LPR = D / 4, J = 256 / LPR;
   const Args& A = F.a;
@@ -470,8 +495,8 @@ template <bool F16, int D> __global__ __launch_bounds__(256) void join_kernel(Fe
   if (cut.slots == 0 && A.slots_sh == 0) return;
   const int R = A.B * A.G, group = threadIdx.x / LPR, d = threadIdx.x % LPR * 4;
   const int request = cut.pair / A.Hkv, hk = cut.pair % A.Hkv;
-  const int len = list_len(A, request);
-  const int n_sh = own_begin(len, A.B, A.shared) > 0 ? A.slots_sh : 0;
+  const int n_sh =
+      A.slots_sh && own_begin(list_len(A, request), A.B, A.shared) > 0 ? A.slots_sh : 0;
   const int n = n_sh + max(cut.slots, 1);
   const int64_t rows = (int64_t)A.N * A.B * A.Hq;
   __shared__ Joined s_part[256];
@@ -520,32 +545,42 @@ template <bool F16, int D> __global__ __launch_bounds__(256) void join_kernel(Fe
 // Slots of few_kernel's parts, of rows that few_kernel takes at all.
 int few_parts(int D, int R) { return kCUs * 4 * few_per_cu(D, R <= 16 ? 1 : 2); }
 
-template <bool F16, int D> hipError_t launch_few(Few F, bool wide, hipStream_t s) {
+template <bool F16, int D> hipError_t launch_few(Few F, bool wide, bool beside, hipStream_t s) {
   Args& A = F.a;
   const int64_t shared = (int64_t)A.Hkv * A.tiles_sh * A.s_sh;
   A.slots_sh = A.s_sh;
   A.step_own = narrow_step(D);
   A.direct = false;
-  if (shared > 0) {
-    if constexpr (D == 128)
-      if (wide)
-        hipLaunchKernelGGL((attend_kernel<F16, D, kWide, kWideStep, true>), dim3((unsigned)shared),
-                           dim3(kWide * 64), 0, s, A);
-    if (!wide)
-      hipLaunchKernelGGL((attend_kernel<F16, D, kNarrow, narrow_step(D), true>),
-                         dim3((unsigned)shared), dim3(kNarrow * 64), 0, s, A);
-    const hipError_t e = hipGetLastError();
-    if (e != hipSuccess) return e;
-  }
   const int R = A.B * A.G;
-  const dim3 grid((unsigned)(F.parts ? F.parts / 4 : ((int64_t)A.N * A.Hkv + 3) / 4));
-  if (R <= 16)
-    hipLaunchKernelGGL((few_kernel<F16, D, 1>), grid, dim3(256), 0, s, F);
-  else
-    hipLaunchKernelGGL((few_kernel<F16, D, 2>), grid, dim3(256), 0, s, F);
+  const int64_t own = F.parts ? F.parts / 4 : ((int64_t)A.N * A.Hkv + 3) / 4;
+  if (beside) {
+    const dim3 grid((unsigned)(shared + own));
+    if constexpr (D != 256) {
+      if (R <= 16)
+        hipLaunchKernelGGL((beside_kernel<F16, D, 1>), grid, dim3(256), 0, s, F);
+      else
+        hipLaunchKernelGGL((beside_kernel<F16, D, 2>), grid, dim3(256), 0, s, F);
+    }
+  } else {
+    if (shared > 0) {
+      if constexpr (D == 128)
+        if (wide)
+          hipLaunchKernelGGL((attend_kernel<F16, D, kWide, kWideStep, true>), dim3((unsigned)shared),
+                             dim3(kWide * 64), 0, s, A);
+      if (!wide)
+        hipLaunchKernelGGL((attend_kernel<F16, D, kNarrow, narrow_step(D), true>),
+                           dim3((unsigned)shared), dim3(kNarrow * 64), 0, s, A);
+      const hipError_t e = hipGetLastError();
+      if (e != hipSuccess) return e;
+    }
+    if (R <= 16)
+      hipLaunchKernelGGL((few_kernel<F16, D, 1>), dim3((unsigned)own), dim3(256), 0, s, F);
+    else
+      hipLaunchKernelGGL((few_kernel<F16, D, 2>), dim3((unsigned)own), dim3(256), 0, s, F);
+  }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (F.parts == 0 && shared == 0)) return e;
-  const int64_t joined = shared ? (int64_t)A.N * A.Hkv : F.parts;
+  const int64_t joined = F.parts == 0 || F.by_pair ? (int64_t)A.N * A.Hkv : F.parts;
   hipLaunchKernelGGL((join_kernel<F16, D>), dim3((unsigned)joined, (unsigned)R), dim3(256), 0, s, F);
   return hipGetLastError();
 }
@@ -568,8 +603,13 @@ hipError_t launch_block_attention4(const xpress_cache& c, int layer, const void*
   const bool f16 = value_type(c) == XPRESS_F16;
   const int R = B * A.G;
   if (R > kFewRows4) return launch_values<true>(A, c.D, f16, p.wide, s);
-  Few F{A, 0, nullptr, nullptr, nullptr};
-  if (N <= kFewRequests) F.parts = few_parts(c.D, R);
+  Few F{A, 0, false, nullptr, nullptr, nullptr};
+  const bool beside = p.s_sh && !p.wide && c.D != 256;
+  if (N <= kFewRequests) {
+    const int items = c.Hkv * p.tiles_sh * p.s_sh;
+    F.parts = beside ? 4 * std::max(kCUs, kCUs * narrow_per_cu(c.D) - items) : few_parts(c.D, R);
+    F.by_pair = p.s_sh || N * c.Hkv <= F.parts;
+  }
   // the shared part's slots and one of every row, then the parts' (attention_scratch_bytes has room)
   const size_t rows = (size_t)N * B * Hq, slots = rows * (p.s_sh ? p.s_sh + 1 : 0);
   F.a.po = static_cast<float*>(ws);
@@ -577,12 +617,18 @@ hipError_t launch_block_attention4(const xpress_cache& c, int layer, const void*
   F.po = reinterpret_cast<float*>(static_cast<char*>(ws) +
                                   up16(slots * (c.D * sizeof(float) + sizeof(float2))));
   F.cut = reinterpret_cast<Cut*>(F.po + 2 * (size_t)F.parts * R * c.D);
-  const size_t cuts = p.s_sh ? (size_t)N * c.Hkv : F.parts;
+  const size_t cuts = F.by_pair ? (size_t)N * c.Hkv : F.parts;
   F.pml = reinterpret_cast<float2*>(F.cut + (F.parts ? cuts : 0));
   switch (c.D) {
-    case 64: return f16 ? launch_few<true, 64>(F, p.wide, s) : launch_few<false, 64>(F, p.wide, s);
-    case 128: return f16 ? launch_few<true, 128>(F, p.wide, s) : launch_few<false, 128>(F, p.wide, s);
-    default: return f16 ? launch_few<true, 256>(F, p.wide, s) : launch_few<false, 256>(F, p.wide, s);
+    case 64:
+      return f16 ? launch_few<true, 64>(F, p.wide, beside, s)
+                 : launch_few<false, 64>(F, p.wide, beside, s);
+    case 128:
+      return f16 ? launch_few<true, 128>(F, p.wide, beside, s)
+                 : launch_few<false, 128>(F, p.wide, beside, s);
+    default:
+      return f16 ? launch_few<true, 256>(F, p.wide, beside, s)
+                 : launch_few<false, 256>(F, p.wide, beside, s);
   }
 }
 
