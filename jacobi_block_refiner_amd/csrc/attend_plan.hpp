@@ -2,6 +2,7 @@
 // Plain integer functions, so they compile for the host alone too.
 #pragma once
 
+#include "cache_index.hpp"
 #include "xpress.h"
 
 #include <algorithm>
@@ -103,6 +104,16 @@ inline int64_t most_row_slots(const xpress_cache& c, int n, int B, int Hq) {
   const int64_t sh = std::min(
       ceil_div((int64_t)kWideItems * kWide * 32, (int64_t)c.Hkv * B * G) + n, n * fits);
   return std::max<int64_t>(own, n * ids) + std::max<int64_t>(sh, n * ids);
+}
+
+// A wave holds the page ids of 64 tiles, from `from` on, and finds each tile's addresses while it works
+// on the one before. At tile t of those up to t1: whether the next tile's ids have to be read first, and
+// up to where it can then go on (past t, always).
+inline constexpr int kFewIds = 64;
+XP_HD bool few_ids_wanted(int t, int from, int t1) { return t + 1 < t1 && t + 1 - from >= kFewIds; }
+XP_HD int few_run_end(int t, int from, int t1) {
+  const int known = from + kFewIds - 1;  // the last tile whose ids are held
+  return t + 1 < t1 && known < t1 ? known : t1;
 }
 
 }  // namespace xpress

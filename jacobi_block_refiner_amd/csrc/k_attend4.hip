@@ -22,7 +22,7 @@ constexpr int kFewLeast = 2;   // tiles of a part at least
 constexpr int kFewRequests = 4096;  // more are not cut: a wave a pair
 
 // Workgroups of few_kernel on a CU, by its registers.
-constexpr int few_per_cu(int D, int RT) { return D == 256 ? 3 - RT : 2; }
+constexpr int few_per_cu(int D, int RT) { return D == 256 ? 3 - RT : D == 64 ? 3 : 2; }
 
 // A pair whose keys lie in several parts: it begins in this one.
 struct Cut {
@@ -78,6 +78,7 @@ template <bool F16, int D, int RT> struct FewCore {
 
   int lane, i, q;
   uint32_t k_at, ks_at, v_at, vs_at;  // the lane's bytes in a tile of 16 tokens
+  uint32_t ks_bit;                    // of its scale in the four bytes at ks_at
   float c;
   // A tile of 32 keys as a lane holds it, 16 tokens and 16. With lane = 16 q + i: of K, token i, the
   // q-th quarter of the channels (of 256 channels two eighths); of V, the pairs of channels i of all
@@ -96,7 +97,9 @@ template <bool F16, int D, int RT> struct FewCore {
     q = lane >> 4;
     c = scale;
     k_at = i * (D / 2) + q * (D == 256 ? 16 : D / 8);
-    ks_at = mx4_k_scale(D, i, D == 64 ? q / 2 : q);
+    const uint32_t at = mx4_k_scale(D, i, D == 64 ? q / 2 : q);
+    ks_at = at & ~3u;
+    ks_bit = at % 4 * 8;
     v_at = lane * (D / 8);
     vs_at = mx4_v_scale(D, 4 * q, 0);
   }
@@ -107,11 +110,16 @@ template <bool F16, int D, int RT> struct FewCore {
   __device__ __forceinline__ void take(int rt, const uint16_t* row) {
 #pragma unroll
     for (int s = 0; s < NG; ++s) qf[rt][s] = *reinterpret_cast<const s16x8*>(row + channel(s));
+  }
+  __device__ __forceinline__ void clear() {
 #pragma unroll
-    for (int g = 0; g < NG; ++g) o[rt][g][0] = o[rt][g][1] = f32x4v{};
-    m[rt] = -1e30f;
-    l[rt] = 0.f;
-    huge[rt] = ~0ull;
+    for (int rt = 0; rt < RT; ++rt) {
+#pragma unroll
+      for (int g = 0; g < NG; ++g) o[rt][g][0] = o[rt][g][1] = f32x4v{};
+      m[rt] = -1e30f;
+      l[rt] = 0.f;
+      huge[rt] = ~0ull;
+    }
   }
 
   // The lane's bytes of tiles of K and of V. (A scalar base and a 32-bit offset of the lane, as long as
@@ -129,11 +137,11 @@ template <bool F16, int D, int RT> struct FewCore {
         const uint4 b = *reinterpret_cast<const uint4*>(k[x] + (k_at + 64));
         kc[x][0] = a.x, kc[x][1] = a.y, kc[x][2] = a.z, kc[x][3] = a.w;
         kc[x][4] = b.x, kc[x][5] = b.y, kc[x][6] = b.z, kc[x][7] = b.w;
-        ks[x][1] = k[x][ks_at + 4];
+        ks[x][1] = *reinterpret_cast<const uint32_t*>(k[x] + (ks_at + 4));
       } else {
         load_words<NG>(k[x] + k_at, kc[x]);
       }
-      ks[x][0] = k[x][ks_at];
+      ks[x][0] = *reinterpret_cast<const uint32_t*>(k[x] + ks_at);
     }
   }
   __device__ __forceinline__ void load_v(const uint8_t* const (&v)[2]) {
@@ -146,7 +154,7 @@ template <bool F16, int D, int RT> struct FewCore {
   }
 
   __device__ __forceinline__ s16x8 k_frag(int x, int s) const {
-    const float scale = mx4_scale<0>(ks[x][D == 256 ? s / 4 : 0]);
+    const float scale = mx4_scale<0>(ks[x][D == 256 ? s / 4 : 0] >> ks_bit);
     const uint32_t w = kc[x][s];
     return __builtin_bit_cast(s16x8, make_uint4(mx4_pair<F16, 0>(w, scale), mx4_pair<F16, 1>(w, scale),
                                                 mx4_pair<F16, 2>(w, scale), mx4_pair<F16, 3>(w, scale)));
@@ -317,7 +325,7 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
       int64_t y = x;
       for (;; ++r) {
         const int n = own_tiles(A, list_len(A, r));
-        if (from < (y + n) * A.Hkv) break;
+        if (from < (y + n) * A.Hkv || r + 1 >= min(r0 + per, A.N)) break;
         y += n;
       }
       s_request[w] = r;
@@ -342,129 +350,175 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
   const int64_t head_bytes = mx4_tiles_bytes(D, A.shift), page_bytes = A.Hkv * head_bytes;
   const int page_mask = (1 << A.shift) - 1;
   Cut cut{0, 0, 0, 0};
-  int slot = 2 * part;  // of the first pair here, then of the others (whole ones leave it alone)
+  int slot = 2 * part;  // of the first pair here; then of the last
   FewCore<F16, D, RT> w;
   w.begin(A.c);
-  for (; at < end && request < A.N; ++request) {
-    const int row = scalar(list_row(A, request));
-    const int len = row < 0 ? 0 : clamp_len(scalar(A.len[row]), A.ld, A.shift);
-    const int first = own_begin(len, A.B, A.shared), tiles = own_tiles(A, len);
-    const int all_see = in_sight(len, A.B, 0);
-    const int32_t* table = A.table + (int64_t)max(row, 0) * A.ld;
-    while (at < end) {
-      int hk = (int)at, t0 = 0, t1 = tiles;
-      if (F.parts) {
-        const int64_t in = at - before * A.Hkv;  // tiles of this request in front
-        if (in >= (int64_t)tiles * A.Hkv) break;
-        hk = (int)(in / tiles);
-        t0 = (int)(in % tiles);
-        t1 = (int)min((int64_t)tiles, t0 + (end - at));
-      }
-      const bool whole = t0 == 0 && t1 == tiles;
-      int vis[RT];
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        const int rl = min(rt * 16 + w.i, R - 1);
-        vis[rt] = in_sight(len, A.B, rl / A.G);
-        w.take(rt, A.q + ((int64_t)request * A.B + rl / A.G) * A.q_ld +
-                       (int64_t)(hk * A.G + rl % A.G) * D);
-      }
-      const uint8_t* k = static_cast<const uint8_t*>(A.k) + hk * head_bytes;
-      const uint8_t* v = static_cast<const uint8_t*>(A.v) + hk * head_bytes;
-      // page ids of the next 64 tiles, a lane each
-      int id0 = 0, id1 = 0;
-      const uint8_t *k_next[2], *v_next[2];
-      auto turn = [&](int t, int nth) {
-        const int pos = first + t * kFewTile, second = min(pos + 16, (len - 1) & ~15);
-        const int64_t a = __builtin_amdgcn_readlane(id0, nth) * page_bytes +
-                          ((pos & page_mask) >> 4) * mx4_tile_bytes(D);
-        const int64_t b = __builtin_amdgcn_readlane(id1, nth) * page_bytes +
-                          ((second & page_mask) >> 4) * mx4_tile_bytes(D);
-        k_next[0] = k + a, k_next[1] = k + b;
-        v_next[0] = v + a, v_next[1] = v + b;
-      };
-      if (len > first) {
-        for (int from = t0; from < t1; from += 64) {
-          const int pos = first + min(from + lane, t1 - 1) * kFewTile;
-          id0 = clamp_page(table[pos >> A.shift], A.n_pages);
-          id1 = clamp_page(table[min(pos + 16, len - 1) >> A.shift], A.n_pages);
-          const int to = min(from + 64, t1);
-          turn(from, 0);
-          w.load_k(k_next);
-          w.load_v(v_next);
-#pragma unroll 1
-          for (int t = from; t < to; ++t) {
-            const int at_key = first + t * kFewTile;
-            const bool masked = at_key + kFewTile > all_see;
-            int see[RT];
-#pragma unroll
-            for (int rt = 0; rt < RT; ++rt) see[rt] = vis[rt] - at_key;
-            w.scores();
-            __builtin_amdgcn_sched_barrier(0);
-            const int next = min(t + 1, to - 1);
-            turn(next, next - from);
-            w.load_k(k_next);
-            __builtin_amdgcn_sched_barrier(0);
-            w.weights(see, masked);
-            w.values(len - at_key, masked);
-            __builtin_amdgcn_sched_barrier(0);
-            w.load_v(v_next);
-          }
-        }
-      }
-#pragma unroll
-      for (int rt = 0; rt < RT; ++rt) {
-        float l = w.l[rt];
-        l += __shfl_xor(l, 16);
-        l += __shfl_xor(l, 32);
-        const int rl = rt * 16 + w.i;
-        if (rl >= R) continue;
-        float o[NG][8];
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-#pragma unroll
-          for (int x = 0; x < 8; ++x) o[g][x] = l == 0.f ? 0.f : w.o[rt][g][x % 2][x / 2];
-        const int64_t token = (int64_t)request * A.B + rl / A.G;
-        const int hq = hk * A.G + rl % A.G;
-        const int64_t out_row = token * A.Hq + hq;
-        if (!whole || A.slots_sh) {
-          const int64_t to = whole ? A.slots_sh * (int64_t)A.N * A.B * A.Hq + out_row
-                                   : (int64_t)slot * R + rl;
-          float* po = (whole ? A.po : F.po) + to * D + 8 * w.q;
-#pragma unroll
-          for (int g = 0; g < NG; ++g) {
-            *reinterpret_cast<float4*>(po + 32 * g) = make_float4(o[g][0], o[g][1], o[g][2], o[g][3]);
-            *reinterpret_cast<float4*>(po + 32 * g + 4) =
-                make_float4(o[g][4], o[g][5], o[g][6], o[g][7]);
-          }
-          if (w.q == 0) (whole ? A.pml : F.pml)[to] = make_float2(w.unit(rt), l);
-          continue;
-        }
-        const float inv = l == 0.f ? 0.f : 1.f / l;
-        uint16_t* out = A.out + token * A.out_ld + (int64_t)hq * D + 8 * w.q;
-#pragma unroll
-        for (int g = 0; g < NG; ++g)
-          *reinterpret_cast<uint4*>(out + 32 * g) = make_uint4(
-              pack2<F16>(o[g][0] * inv, o[g][1] * inv), pack2<F16>(o[g][2] * inv, o[g][3] * inv),
-              pack2<F16>(o[g][4] * inv, o[g][5] * inv), pack2<F16>(o[g][6] * inv, o[g][7] * inv));
-        if (A.lse && w.q == 0)
-          A.lse[out_row] = l == 0.f ? -INFINITY : (w.unit(rt) + log2f(l)) * 0.69314718056f;
-      }
-      if (F.parts && t0 == 0) {  // the pair begins here
-        const int64_t g1 = before * A.Hkv + (int64_t)(hk + 1) * tiles;
-        const int pair = request * A.Hkv + hk;
-        const Cut c{pair, whole ? 0 : (int)((g1 - 1) / each - part) + 1, part, slot};
-        if (F.by_pair) {
-          if (lane == 0) F.cut[pair] = c;
-        } else if (!whole) {
-          cut = c;
-        }
-      }
-      slot = 2 * part + 1;
-      at += t1 - t0;
-      if (!F.parts) break;
+
+  // The tiles of one pair in this part. While it is worked on, the next one's page ids are on their
+  // way, and behind its last scores the next one's first tile.
+  struct Segment {
+    int request, hk, len, first, tiles, t0, t1;
+    const int32_t* table;
+    int id0, id1;  // page ids of its tiles from `ids_from` on (of their two halves), a lane each
+    int ids_from;
+  };
+  // First key of the row's last tile of 16.
+  auto last_tile = [&](const Segment& g) { return max(g.len - 1, 0) & ~15; };
+  auto ask_ids = [&](Segment& g, int from) {
+    g.ids_from = from;
+    const int pos = g.first + min(from + lane, g.t1 - 1) * kFewTile, last = last_tile(g);
+    g.id0 = g.table[min(pos, last) >> A.shift];
+    g.id1 = g.table[min(pos + 16, last) >> A.shift];
+  };
+  int len_ahead = 0;  // of the request behind the last one opened, as it was read
+  auto read_len = [&](int r) {
+    const int row = r < A.N ? list_row(A, r) : -1;
+    return row < 0 ? 0 : A.len[row];
+  };
+  // The pair that begins at `from` (tile t0 of head hk of the request).
+  auto open = [&](Segment& g, int r, int hk, int t0, bool other_request) {
+    if (other_request) {
+      const int row = scalar(list_row(A, r));
+      g.request = r;
+      g.len = row < 0 ? 0 : clamp_len(scalar(len_ahead), A.ld, A.shift);
+      g.first = own_begin(g.len, A.B, A.shared);
+      g.tiles = own_tiles(A, g.len);
+      g.table = A.table + (int64_t)max(row, 0) * A.ld;
+      len_ahead = read_len(r + 1);
     }
-    before += tiles;
+    g.hk = hk;
+    g.t0 = t0;
+    g.t1 = F.parts ? (int)min((int64_t)g.tiles, t0 + (end - at)) : g.tiles;
+    ask_ids(g, t0);
+  };
+  const uint8_t *k_next[2], *v_next[2];
+  auto turn = [&](const Segment& g, int t) {
+    const int pos = g.first + t * kFewTile, last = last_tile(g), nth = t - g.ids_from;
+    const int p0 = min(pos, last), p1 = min(pos + 16, last);
+    const int i0 = clamp_page(__builtin_amdgcn_readlane(g.id0, nth), A.n_pages);
+    const int i1 = clamp_page(__builtin_amdgcn_readlane(g.id1, nth), A.n_pages);
+    const int64_t a = i0 * page_bytes + g.hk * head_bytes + ((p0 & page_mask) >> 4) * mx4_tile_bytes(D);
+    const int64_t b = i1 * page_bytes + g.hk * head_bytes + ((p1 & page_mask) >> 4) * mx4_tile_bytes(D);
+    k_next[0] = static_cast<const uint8_t*>(A.k) + a, k_next[1] = static_cast<const uint8_t*>(A.k) + b;
+    v_next[0] = static_cast<const uint8_t*>(A.v) + a, v_next[1] = static_cast<const uint8_t*>(A.v) + b;
+  };
+  auto take = [&](const Segment& g) {
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      const int rl = min(rt * 16 + w.i, R - 1);
+      w.take(rt, A.q + ((int64_t)g.request * A.B + rl / A.G) * A.q_ld +
+                     (int64_t)(g.hk * A.G + rl % A.G) * D);
+    }
+  };
+
+  Segment g;
+  {
+    len_ahead = read_len(request);
+    const int row = scalar(list_row(A, request));
+    const int tiles = own_tiles(A, row < 0 ? 0 : clamp_len(scalar(len_ahead), A.ld, A.shift));
+    const int64_t in = F.parts ? at - before * A.Hkv : at * tiles;  // tiles of the request in front
+    // (where another stream changes lengths meanwhile, results are unspecified, but inside the cache)
+    open(g, request, (int)min(in / tiles, (int64_t)A.Hkv - 1), (int)(in % tiles), true);
+  }
+  take(g);
+  turn(g, g.t0);
+  w.load_k(k_next);
+  w.load_v(v_next);
+  while (true) {
+    const int64_t g0 = before * A.Hkv + (int64_t)g.hk * g.tiles;  // the pair's first tile of all
+    const int all_see = in_sight(g.len, A.B, 0);
+    at += g.t1 - g.t0;
+    const bool other = g.hk + 1 == A.Hkv;
+    const bool more = F.parts && at < end && !(other && g.request + 1 >= A.N);
+    Segment next = g;
+    if (more) {
+      open(next, other ? g.request + 1 : g.request, other ? 0 : g.hk + 1, 0, other);
+    }
+    int vis[RT];
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) vis[rt] = in_sight(g.len, A.B, min(rt * 16 + w.i, R - 1) / A.G);
+    w.clear();
+    for (int t = g.t0; t < g.t1;) {
+      if (few_ids_wanted(t, g.ids_from, g.t1)) ask_ids(g, t + 1);
+      // the page ids are in: a load that may be under way where the loop begins makes the compiler wait
+      // for all loads in every round of it
+      asm volatile("" : "+v"(g.id0), "+v"(g.id1));
+      const int to = few_run_end(t, g.ids_from, g.t1);
+#pragma unroll 1
+      for (; t < to; ++t) {
+        const int at_key = g.first + t * kFewTile;
+        const bool masked = at_key + kFewTile > all_see;
+        int see[RT];
+#pragma unroll
+        for (int rt = 0; rt < RT; ++rt) see[rt] = vis[rt] - at_key;
+        w.scores();
+        __builtin_amdgcn_sched_barrier(0);
+        if (t + 1 < g.t1)
+          turn(g, t + 1);
+        else if (more)
+          turn(next, 0);
+        w.load_k(k_next);
+        __builtin_amdgcn_sched_barrier(0);
+        w.weights(see, masked);
+        w.values(g.len - at_key, masked);
+        __builtin_amdgcn_sched_barrier(0);
+        w.load_v(v_next);
+      }
+    }
+    if (RT == 1 && more) take(next);  // (two row tiles' queries have no registers beside the sums)
+
+    const bool whole = g.t0 == 0 && g.t1 == g.tiles;
+#pragma unroll
+    for (int rt = 0; rt < RT; ++rt) {
+      float l = w.l[rt];
+      l += __shfl_xor(l, 16);
+      l += __shfl_xor(l, 32);
+      const int rl = rt * 16 + w.i;
+      if (rl >= R) continue;
+      float o[NG][8];
+#pragma unroll
+      for (int c = 0; c < NG; ++c)
+#pragma unroll
+        for (int x = 0; x < 8; ++x) o[c][x] = l == 0.f ? 0.f : w.o[rt][c][x % 2][x / 2];
+      const int64_t token = (int64_t)g.request * A.B + rl / A.G;
+      const int hq = g.hk * A.G + rl % A.G;
+      const int64_t out_row = token * A.Hq + hq;
+      if (!whole || A.slots_sh) {
+        const int64_t to = whole ? A.slots_sh * (int64_t)A.N * A.B * A.Hq + out_row
+                                 : (int64_t)slot * R + rl;
+        float* po = (whole ? A.po : F.po) + to * D + 8 * w.q;
+#pragma unroll
+        for (int c = 0; c < NG; ++c) {
+          *reinterpret_cast<float4*>(po + 32 * c) = make_float4(o[c][0], o[c][1], o[c][2], o[c][3]);
+          *reinterpret_cast<float4*>(po + 32 * c + 4) = make_float4(o[c][4], o[c][5], o[c][6], o[c][7]);
+        }
+        if (w.q == 0) (whole ? A.pml : F.pml)[to] = make_float2(w.unit(rt), l);
+        continue;
+      }
+      const float inv = l == 0.f ? 0.f : 1.f / l;
+      uint16_t* out = A.out + token * A.out_ld + (int64_t)hq * D + 8 * w.q;
+#pragma unroll
+      for (int c = 0; c < NG; ++c)
+        *reinterpret_cast<uint4*>(out + 32 * c) = make_uint4(
+            pack2<F16>(o[c][0] * inv, o[c][1] * inv), pack2<F16>(o[c][2] * inv, o[c][3] * inv),
+            pack2<F16>(o[c][4] * inv, o[c][5] * inv), pack2<F16>(o[c][6] * inv, o[c][7] * inv));
+      if (A.lse && w.q == 0)
+        A.lse[out_row] = l == 0.f ? -INFINITY : (w.unit(rt) + log2f(l)) * 0.69314718056f;
+    }
+    if (F.parts && g.t0 == 0) {  // the pair begins here
+      const int pair = g.request * A.Hkv + g.hk;
+      const Cut c{pair, whole ? 0 : (int)((g0 + g.tiles - 1) / each - part) + 1, part, slot};
+      if (F.by_pair) {
+        if (lane == 0) F.cut[pair] = c;
+      } else if (!whole) {
+        cut = c;
+      }
+    }
+    if (!more) break;
+    if (RT != 1) take(next);
+    slot = 2 * part + 1;
+    if (next.request != g.request) before += g.tiles;
+    g = next;
   }
   if (F.parts && !F.by_pair && lane == 0) F.cut[part] = cut;
 }
@@ -484,62 +538,60 @@ __global__ __launch_bounds__(256, narrow_per_cu(D)) void beside_kernel(Few F) {
     few_part<F16, D, RT>(F, blockIdx.x - items);
 }
 
-// Joins the slots of a pair that was cut, and the shared items' of every pair: a workgroup a row of a
-// pair, or of the pair that begins in a part where there are more pairs than parts (and no shared
-// items). J groups of threads take every J-th slot.
-template <bool F16, int D> __global__ __launch_bounds__(256) void join_kernel(Few F) {
-  constexpr int LPR = D / 4, J = 256 / LPR;
+// Joins the slots of a pair that was cut, and the shared items' of every pair, in rows of the pairs (or
+// of those that begin in a part and go on, where there are more pairs than parts and no shared items).
+// J groups of threads take every J-th slot of a row; a workgroup has 256 / (J D / 4) rows at a time, or
+// with J = 4096 / D one and 1024 threads, where a few pairs were cut into very many slots.
+template <bool F16, int D, int J>
+__global__ __launch_bounds__(J * D > 1024 ? 1024 : 256) void join_kernel(Few F) {
+  constexpr int LPR = D / 4, RPB = J * D > 1024 ? 1 : 256 / (LPR * J);
   const Args& A = F.a;
   Cut cut{(int)blockIdx.x, 0, 0, 0};
   if (F.parts) cut = F.cut[blockIdx.x];
   if (cut.slots == 0 && A.slots_sh == 0) return;
-  const int R = A.B * A.G, group = threadIdx.x / LPR, d = threadIdx.x % LPR * 4;
+  const int R = A.B * A.G, d = threadIdx.x % LPR * 4;
+  const int group = threadIdx.x / LPR % J, r = blockIdx.y * RPB + threadIdx.x / (LPR * J);
   const int request = cut.pair / A.Hkv, hk = cut.pair % A.Hkv;
   const int n_sh =
       A.slots_sh && own_begin(list_len(A, request), A.B, A.shared) > 0 ? A.slots_sh : 0;
-  const int n = n_sh + max(cut.slots, 1);
+  const int n = r < R ? n_sh + max(cut.slots, 1) : 0;
   const int64_t rows = (int64_t)A.N * A.B * A.Hq;
-  __shared__ Joined s_part[256];
-  for (int r = blockIdx.y; r < R; r += gridDim.y) {
-    const int64_t token = (int64_t)request * A.B + r / A.G;
-    const int hq = hk * A.G + r % A.G;
-    const int64_t row = token * A.Hq + hq;
-    Joined all{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
-    for (int s0 = group; s0 < n; s0 += 4 * J) {  // four slots' loads in flight
-      float2 ml[4];
-      float4 x[4];
+  const int64_t token = (int64_t)request * A.B + r / A.G;
+  const int hq = hk * A.G + r % A.G;
+  const int64_t row = token * A.Hq + hq;
+  Joined all{-INFINITY, 0.f, make_float4(0.f, 0.f, 0.f, 0.f)};
+  for (int s0 = group; s0 < n; s0 += 4 * J) {  // four slots' loads in flight
+    float2 ml[4];
+    float4 x[4];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        const int s = min(s0 + j * J, n - 1), own = s - n_sh;
-        const bool part = own >= 0 && cut.slots;
-        const int64_t from =
-            part ? (own == 0 ? cut.slot : 2 * ((int64_t)cut.part + own)) * R + r
-                 : (own >= 0 ? A.slots_sh : s) * rows + row;
-        ml[j] = (part ? F.pml : A.pml)[from];
-        x[j] = *reinterpret_cast<const float4*>((part ? F.po : A.po) + from * D + d);
-      }
-#pragma unroll
-      for (int j = 0; j < 4; ++j)
-        if (s0 + j * J < n && ml[j].y != 0.f) all.add(ml[j].x, ml[j].y, x[j]);
+    for (int j = 0; j < 4; ++j) {
+      const int s = min(s0 + j * J, n - 1), own = s - n_sh;
+      const bool part = own >= 0 && cut.slots;
+      const int64_t from = part ? (own == 0 ? cut.slot : 2 * ((int64_t)cut.part + own)) * R + r
+                                : (own >= 0 ? A.slots_sh : s) * rows + row;
+      ml[j] = (part ? F.pml : A.pml)[from];
+      x[j] = *reinterpret_cast<const float4*>((part ? F.po : A.po) + from * D + d);
     }
-    s_part[threadIdx.x] = all;
-    __syncthreads();
-    if (group == 0) {
 #pragma unroll
-      for (int g = 1; g < J; ++g) {
-        const Joined& p = s_part[threadIdx.x + g * LPR];
-        if (p.l != 0.f) all.add(p.m, p.l, p.o);
-      }
-      const float inv = all.l == 0.f ? 0.f : 1.f / all.l;
-      uint2 w;
-      w.x = pack2<F16>(all.o.x * inv, all.o.y * inv);
-      w.y = pack2<F16>(all.o.z * inv, all.o.w * inv);
-      *reinterpret_cast<uint2*>(A.out + token * A.out_ld + (int64_t)hq * D + d) = w;
-      if (A.lse && d == 0)
-        A.lse[row] = all.l == 0.f ? -INFINITY : (all.m + log2f(all.l)) * 0.69314718056f;
-    }
-    __syncthreads();
+    for (int j = 0; j < 4; ++j)
+      if (s0 + j * J < n && ml[j].y != 0.f) all.add(ml[j].x, ml[j].y, x[j]);
   }
+  __shared__ Joined s_part[RPB * J * LPR];
+  s_part[threadIdx.x] = all;
+  __syncthreads();
+  if (group || r >= R) return;
+#pragma unroll 8
+  for (int g = 1; g < J; ++g) {
+    const Joined& p = s_part[threadIdx.x + g * LPR];
+    if (p.l != 0.f) all.add(p.m, p.l, p.o);
+  }
+  const float inv = all.l == 0.f ? 0.f : 1.f / all.l;
+  uint2 w;
+  w.x = pack2<F16>(all.o.x * inv, all.o.y * inv);
+  w.y = pack2<F16>(all.o.z * inv, all.o.w * inv);
+  *reinterpret_cast<uint2*>(A.out + token * A.out_ld + (int64_t)hq * D + d) = w;
+  if (A.lse && d == 0)
+    A.lse[row] = all.l == 0.f ? -INFINITY : (all.m + log2f(all.l)) * 0.69314718056f;
 }
 
 // Slots of few_kernel's parts, of rows that few_kernel takes at all.
@@ -581,7 +633,15 @@ template <bool F16, int D> hipError_t launch_few(Few F, bool wide, bool beside, 
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (F.parts == 0 && shared == 0)) return e;
   const int64_t joined = F.parts == 0 || F.by_pair ? (int64_t)A.N * A.Hkv : F.parts;
-  hipLaunchKernelGGL((join_kernel<F16, D>), dim3((unsigned)joined, (unsigned)R), dim3(256), 0, s, F);
+  // few rows have many slots each
+  if (joined * R <= kCUs) {
+    hipLaunchKernelGGL((join_kernel<F16, D, 4096 / D>), dim3((unsigned)joined, (unsigned)R), dim3(1024),
+                       0, s, F);
+  } else {
+    constexpr int J = 2, RPB = 1024 / (D * J);
+    hipLaunchKernelGGL((join_kernel<F16, D, J>), dim3((unsigned)joined, (unsigned)ceil_div(R, RPB)),
+                       dim3(256), 0, s, F);
+  }
   return hipGetLastError();
 }
 

@@ -403,6 +403,44 @@ def test_many_short_requests():
         x.check(x.run(x.cache()), what=f"{len(lengths)} requests, D {D}")
 
 
+@pytest.mark.parametrize("N,B,G,shared", [(4100, 1, 2, 0), (4100, 1, 2, 64), (5, 1, 2, 0)])
+def test_rows_of_whole_runs_of_tiles(N, B, G, shared):
+    """Rows of exactly 64 and 128 tiles of 32 tokens, and one token more or less, which one wave walks
+    through where there are very many requests; among them as many short ones as it takes."""
+    Hkv, D, page = 2, 64, 64
+    long = [2048, 2049, 2047, 4096, 4097]
+    at = [0, 1, N // 2, N - 2, N - 1] if N > 5 else range(5)
+    lengths = [(7 * i) % 4 + shared for i in range(N)]
+    for r, n in zip(at, long):
+        lengths[r] = n + shared
+    log(f"rows of whole runs of tiles, {N} requests, shared {shared}")
+    g = torch.Generator().manual_seed(2)
+    pages = -(-(4097 + shared) // page)
+    shape = (1, pages, Hkv, page, D)
+    pools = [mx4.pool_of(torch.randn(shape, generator=g), torch.bfloat16, v) for v in (False, True)]
+    k, v = (mx4.pool_values(p, D, is_v).float() for p, is_v in zip(pools, (False, True)))
+    # every row's tokens are the first of the same pages
+    c = xpress.Cache(k=pools[0].cuda(), v=pools[1].cuda(), length=i32(lengths), ref=i32(np.ones(pages)),
+                     table=torch.arange(pages, dtype=torch.int32, device="cuda").repeat(N, 1))
+    q = torch.randn(N * B, Hkv * G * D, generator=g).bfloat16()
+    out = torch.empty(N * B, Hkv * G * D, dtype=torch.bfloat16, device="cuda")
+    lse = torch.empty(N * B, Hkv * G, device="cuda")
+    ws = xpress.attention_workspace(c, N, B, Hkv * G)
+    ws.fill_(0xFF)
+    xpress.block_attention(c, 0, q.cuda(), B=B, Hq=Hkv * G, N=N, out=out, lse=lse, shared=shared, ws=ws)
+    rows = sorted({*at, *range(0, N, max(1, N // 40))})
+    pick = [r * B + b for r in rows for b in range(B)]
+    want, wl, mass, size = attention(k[0], v[0], np.tile(np.arange(pages), (N, 1)), lengths, page,
+                                     q[pick], rows, B, Hkv * G, D ** -0.5)
+    bound, lse_bound = attention_bounds(want, mass, size, 4200, D, torch.bfloat16)
+    got = out.cpu().double().view(N * B, Hkv * G, D)
+    assert bool(((got[pick] - want).abs() <= bound).all())
+    sees = wl > -math.inf
+    assert bool((lse.cpu()[pick][~sees] == -math.inf).all())
+    assert bool(((lse.cpu()[pick].double() - wl).abs() <= lse_bound + wl.abs() * 2.0 ** -22)[sees].all())
+    assert not bool(got.isnan().any())
+
+
 def test_long_row_in_a_big_pool():
     """Pages past byte 2^32 of a layer, written and attended to."""
     n_pages, Hkv, page, D = 140000, 8, 64, 128

@@ -152,3 +152,40 @@ def test_the_oracle_on_cases_with_known_answers():
         assert torch.equal(mx4.unpack(mx4.pack(code, e, v), 64, v), mx4.values(code, e))
         far = (mx4.values(code, e) - y.double()).abs().unflatten(-1, (-1, 32))
         assert bool((far <= torch.pow(2.0, e.double())[..., None]).all())  # a scale at most
+
+
+RUNS = r"""
+#include "attend_plan.hpp"
+#include <cstdio>
+using namespace xpress;
+int main() {
+  // a wave's walk over the tiles of a pair: every tile once, in order, with its page ids held
+  for (int t0 : {0, 1, 5, 63, 64, 1000})
+    for (int n = 1; n < 400; ++n) {
+      const int t1 = t0 + n;
+      int from = t0, seen = t0, rounds = 0;
+      for (int t = t0; t < t1;) {
+        if (++rounds > n + 1) return 1;  // no way on
+        if (few_ids_wanted(t, from, t1)) from = t + 1;
+        const int to = few_run_end(t, from, t1);
+        if (to <= t || to > t1) return 2;
+        for (; t < to; ++t) {
+          if (t != seen++) return 3;
+          if (t + 1 < t1 && (t + 1 < from || t + 1 - from >= kFewIds)) return 4;
+        }
+      }
+      if (seen != t1) return 5;
+      if (rounds > n / (kFewIds - 1) + 2) return 6;
+    }
+  return 0;
+}
+"""
+
+
+def test_a_wave_comes_to_the_end_of_its_tiles(tmp_path):
+    src = tmp_path / "runs.cpp"
+    src.write_text(RUNS)
+    exe = tmp_path / "runs"
+    subprocess.run(["g++", "-std=c++17", "-O1", "-fsanitize=undefined", "-fno-sanitize-recover",
+                    f"-I{build.CSRC}", f"-I{build.INCLUDE}", str(src), "-o", str(exe)], check=True)
+    assert subprocess.run([str(exe)], timeout=60).returncode == 0
