@@ -1,13 +1,14 @@
 // Attention of drafted blocks over a paged cache of 4 bits (gfx950).
 //
-// Query rows of the shared part, and of requests with more than 32 of them a head, go to the items of
-// attend_kernel.hpp. The requests' own keys with up to 32 rows a head (plain decoding, short blocks)
-// are HBM's: 2 * 17 D / 32 bytes a key for few operations. few_kernel reads them straight into the
-// matrix core's registers.
+// Query rows of the shared part, and of requests with many of them a head, go to the items of
+// attend_kernel.hpp. The requests' own keys with up to 32 rows a head (decoding, short blocks; up to 64
+// over long contexts) are HBM's: 2 * 17 D / 32 bytes a key for few operations. few_kernel reads them
+// straight into the matrix core's registers, a wave 16 or 32 rows; one, two or four waves of a workgroup
+// take a request's rows and read the same keys, from HBM once.
 //
 // All (request, head) pairs' tiles of 32 keys form one sequence, which is cut into as many equal parts
-// as there are waves on the card, whatever the lengths: a wave finds its part from the lengths
-// themselves. A pair that lies in one part is finished there; where it is cut, each part
+// as there are waves (or such groups of them) on the card, whatever the lengths: a wave finds its part
+// from the lengths themselves. A pair that lies in one part is finished there; where it is cut, each part
 // leaves (sums, unit of the weights, their sum) in a slot, and join_kernel joins them. Beside a shared
 // part all pairs leave theirs, and are joined with its items'. (One wave a pair that read the shared
 // slots too took 120 of 133 us at 32 requests behind 4096 tokens.)
@@ -18,11 +19,10 @@ namespace xpress {
 namespace {
 
 constexpr int kFewTile = 32;   // keys of a step of a wave
-constexpr int kFewLeast = 2;   // tiles of a part at least
-constexpr int kFewRequests = 4096;  // more are not cut: a wave a pair
+constexpr int kFewRequests = 4096;  // more are not cut: a part a pair
 
 // Workgroups of few_kernel on a CU, by its registers.
-constexpr int few_per_cu(int D, int RT) { return D == 256 ? 3 - RT : D == 64 ? 3 : 2; }
+constexpr int few_per_cu(int D, int RT) { return D == 64 ? 3 : 2; }
 
 // A pair whose keys lie in several parts: it begins in this one.
 struct Cut {
@@ -32,7 +32,9 @@ struct Cut {
 
 struct Few {
   Args a;
-  int parts;  // waves, where the sequence is cut; else 0
+  int parts;  // of the sequence, where it is cut; else 0
+  int least;  // tiles of a part at least
+  int waves;  // of a part, with 16 RT rows each: 1, 2 or 4
   bool by_pair;  // cut[] is of the pairs; else of the parts: of the pair that begins there and goes on
   float* po;   // [2 * parts, R, D]
   float2* pml; // [2 * parts, R]
@@ -287,15 +289,15 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
   const Args& A = F.a;
   const int wave = scalar((int)threadIdx.x >> 6), lane = threadIdx.x & 63;
   const int R = A.B * A.G;
-
-  // this wave's part of the sequence: tiles [at, end) of all, beginning in a request with `before`
-  // tiles a head in front of it
-  const int part = block * 4 + wave;
+  // this wave's rows, and its part of the sequence: tiles [at, end) of all, beginning in a request with
+  // `before` tiles a head in front of it
+  const int per_block = 4 / F.waves, part = block * per_block + wave / F.waves;
+  const int row0 = wave % F.waves * 16 * RT;
   int64_t at, end, before = 0, each = 0;
-  int request;
+  int request, row, len;
   if (F.parts) {
     __shared__ int64_t s_scan[4], s_before[4];
-    __shared__ int s_request[4];
+    __shared__ int s_request[4], s_row[4], s_len[4];
     // each thread a run of requests
     const int per = (A.N + 255) / 256, r0 = threadIdx.x * per;
     int64_t mine = 0;
@@ -316,10 +318,10 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
       all += s_scan[w];
     }
     all = scalar(all) * A.Hkv;
-    each = max((all + F.parts - 1) / F.parts, (int64_t)kFewLeast);
-#pragma unroll
-    for (int w = 0; w < 4; ++w) {  // the thread of the request in which wave w's part begins
-      const int64_t from = (block * 4 + w) * each;
+    each = all < (int64_t)1 << 31 ? (uint32_t)all / (uint32_t)F.parts : all / F.parts;
+    each = max(each + (each * F.parts < all), (int64_t)F.least);
+    for (int w = 0; w < per_block; ++w) {  // the thread of the request in which the part begins
+      const int64_t from = (block * per_block + w) * each;
       if (from < x * A.Hkv || from >= (x + mine) * A.Hkv) continue;
       int r = r0;
       int64_t y = x;
@@ -330,19 +332,26 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
       }
       s_request[w] = r;
       s_before[w] = y;
+      s_row[w] = list_row(A, r);
+      s_len[w] = list_len(A, r);
     }
     __syncthreads();
     at = part * each;
     end = min(at + each, all);
     if (at >= all) {
-      if (lane == 0 && !F.by_pair) F.cut[part].slots = 0;
+      if (lane == 0 && row0 == 0 && !F.by_pair) F.cut[part].slots = 0;
       return;
     }
-    request = scalar(s_request[wave]);
-    before = scalar(s_before[wave]);
+    if (row0 >= R) return;
+    request = scalar(s_request[wave / F.waves]);
+    before = scalar(s_before[wave / F.waves]);
+    row = scalar(s_row[wave / F.waves]);
+    len = scalar(s_len[wave / F.waves]);
   } else {
-    if (part >= (int64_t)A.N * A.Hkv) return;
+    if (part >= (int64_t)A.N * A.Hkv || row0 >= R) return;
     request = part / A.Hkv;
+    row = scalar(list_row(A, request));
+    len = row < 0 ? 0 : clamp_len(scalar(A.len[row]), A.ld, A.shift);
     at = part % A.Hkv;  // (of the request's pairs)
     end = at + 1;
   }
@@ -375,17 +384,16 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
     const int row = r < A.N ? list_row(A, r) : -1;
     return row < 0 ? 0 : A.len[row];
   };
-  // The pair that begins at `from` (tile t0 of head hk of the request).
-  auto open = [&](Segment& g, int r, int hk, int t0, bool other_request) {
-    if (other_request) {
-      const int row = scalar(list_row(A, r));
-      g.request = r;
-      g.len = row < 0 ? 0 : clamp_len(scalar(len_ahead), A.ld, A.shift);
-      g.first = own_begin(g.len, A.B, A.shared);
-      g.tiles = own_tiles(A, g.len);
-      g.table = A.table + (int64_t)max(row, 0) * A.ld;
-      len_ahead = read_len(r + 1);
-    }
+  auto set_request = [&](Segment& g, int r, int row, int len) {
+    g.request = r;
+    g.len = len;
+    g.first = own_begin(len, A.B, A.shared);
+    g.tiles = own_tiles(A, len);
+    g.table = A.table + (int64_t)max(row, 0) * A.ld;
+    len_ahead = read_len(r + 1);
+  };
+  // The part's tiles of the request's head hk from t0 on.
+  auto open = [&](Segment& g, int hk, int t0) {
     g.hk = hk;
     g.t0 = t0;
     g.t1 = F.parts ? (int)min((int64_t)g.tiles, t0 + (end - at)) : g.tiles;
@@ -405,20 +413,19 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
   auto take = [&](const Segment& g) {
 #pragma unroll
     for (int rt = 0; rt < RT; ++rt) {
-      const int rl = min(rt * 16 + w.i, R - 1);
+      const int rl = min(row0 + rt * 16 + w.i, R - 1);
       w.take(rt, A.q + ((int64_t)g.request * A.B + rl / A.G) * A.q_ld +
                      (int64_t)(g.hk * A.G + rl % A.G) * D);
     }
   };
 
   Segment g;
+  set_request(g, request, row, len);
   {
-    len_ahead = read_len(request);
-    const int row = scalar(list_row(A, request));
-    const int tiles = own_tiles(A, row < 0 ? 0 : clamp_len(scalar(len_ahead), A.ld, A.shift));
-    const int64_t in = F.parts ? at - before * A.Hkv : at * tiles;  // tiles of the request in front
-    // (where another stream changes lengths meanwhile, results are unspecified, but inside the cache)
-    open(g, request, (int)min(in / tiles, (int64_t)A.Hkv - 1), (int)(in % tiles), true);
+    // tiles of the request in front (below 2^31, as a table holds 2^28 tokens; where another stream
+    // changes lengths meanwhile, results are unspecified, but inside the cache)
+    const uint32_t in = F.parts ? (uint32_t)(at - before * A.Hkv) : (uint32_t)at * g.tiles;
+    open(g, min((int)(in / g.tiles), A.Hkv - 1), (int)(in % g.tiles));
   }
   take(g);
   turn(g, g.t0);
@@ -432,11 +439,16 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
     const bool more = F.parts && at < end && !(other && g.request + 1 >= A.N);
     Segment next = g;
     if (more) {
-      open(next, other ? g.request + 1 : g.request, other ? 0 : g.hk + 1, 0, other);
+      if (other) {
+        const int row = scalar(list_row(A, g.request + 1));
+        const int len = scalar(len_ahead);
+        set_request(next, g.request + 1, row, row < 0 ? 0 : clamp_len(len, A.ld, A.shift));
+      }
+      open(next, other ? 0 : g.hk + 1, 0);
     }
     int vis[RT];
 #pragma unroll
-    for (int rt = 0; rt < RT; ++rt) vis[rt] = in_sight(g.len, A.B, min(rt * 16 + w.i, R - 1) / A.G);
+    for (int rt = 0; rt < RT; ++rt) vis[rt] = in_sight(g.len, A.B, min(row0 + rt * 16 + w.i, R - 1) / A.G);
     w.clear();
     for (int t = g.t0; t < g.t1;) {
       if (few_ids_wanted(t, g.ids_from, g.t1)) ask_ids(g, t + 1);
@@ -473,7 +485,7 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
       float l = w.l[rt];
       l += __shfl_xor(l, 16);
       l += __shfl_xor(l, 32);
-      const int rl = rt * 16 + w.i;
+      const int rl = row0 + rt * 16 + w.i;
       if (rl >= R) continue;
       float o[NG][8];
 #pragma unroll
@@ -509,7 +521,7 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
       const int pair = g.request * A.Hkv + g.hk;
       const Cut c{pair, whole ? 0 : (int)((g0 + g.tiles - 1) / each - part) + 1, part, slot};
       if (F.by_pair) {
-        if (lane == 0) F.cut[pair] = c;
+        if (lane == 0 && row0 == 0) F.cut[pair] = c;
       } else if (!whole) {
         cut = c;
       }
@@ -520,7 +532,7 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
     if (next.request != g.request) before += g.tiles;
     g = next;
   }
-  if (F.parts && !F.by_pair && lane == 0) F.cut[part] = cut;
+  if (F.parts && !F.by_pair && lane == 0 && row0 == 0) F.cut[part] = cut;
 }
 
 template <bool F16, int D, int RT>
@@ -594,8 +606,16 @@ __global__ __launch_bounds__(J * D > 1024 ? 1024 : 256) void join_kernel(Few F) 
     A.lse[row] = all.l == 0.f ? -INFINITY : (all.m + log2f(all.l)) * 0.69314718056f;
 }
 
-// Slots of few_kernel's parts, of rows that few_kernel takes at all.
-int few_parts(int D, int R) { return kCUs * 4 * few_per_cu(D, R <= 16 ? 1 : 2); }
+// Row tiles of a wave, waves of a part, and parts of the sequence. At D 256 two row tiles would have a
+// SIMD to themselves and no registers left.
+int few_row_tiles(int D, int R) { return R <= 16 || D == 256 ? 1 : 2; }
+int few_waves(int D, int R) {
+  const int n = (R - 1) / (16 * few_row_tiles(D, R));
+  return n == 0 ? 1 : n == 1 ? 2 : 4;
+}
+int few_parts(int D, int R) {
+  return kCUs * few_per_cu(D, few_row_tiles(D, R)) * 4 / few_waves(D, R);
+}
 
 template <bool F16, int D> hipError_t launch_few(Few F, bool wide, bool beside, hipStream_t s) {
   Args& A = F.a;
@@ -604,11 +624,12 @@ template <bool F16, int D> hipError_t launch_few(Few F, bool wide, bool beside, 
   A.step_own = narrow_step(D);
   A.direct = false;
   const int R = A.B * A.G;
-  const int64_t own = F.parts ? F.parts / 4 : ((int64_t)A.N * A.Hkv + 3) / 4;
+  const int64_t own = ceil_div(F.parts ? F.parts : (int64_t)A.N * A.Hkv, 4 / F.waves);
+  const bool one = few_row_tiles(D, R) == 1;
   if (beside) {
     const dim3 grid((unsigned)(shared + own));
     if constexpr (D != 256) {
-      if (R <= 16)
+      if (one)
         hipLaunchKernelGGL((beside_kernel<F16, D, 1>), grid, dim3(256), 0, s, F);
       else
         hipLaunchKernelGGL((beside_kernel<F16, D, 2>), grid, dim3(256), 0, s, F);
@@ -625,17 +646,21 @@ template <bool F16, int D> hipError_t launch_few(Few F, bool wide, bool beside, 
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
     }
-    if (R <= 16)
+    if (one)
       hipLaunchKernelGGL((few_kernel<F16, D, 1>), dim3((unsigned)own), dim3(256), 0, s, F);
-    else
+    else if constexpr (D != 256)
       hipLaunchKernelGGL((few_kernel<F16, D, 2>), dim3((unsigned)own), dim3(256), 0, s, F);
   }
   const hipError_t e = hipGetLastError();
   if (e != hipSuccess || (F.parts == 0 && shared == 0)) return e;
   const int64_t joined = F.parts == 0 || F.by_pair ? (int64_t)A.N * A.Hkv : F.parts;
-  // few rows have many slots each
-  if (joined * R <= kCUs) {
+  // few rows may have many slots each
+  const int64_t tiles = ceil_div((int64_t)A.ld << A.shift, kFewTile);
+  if (joined * R <= kCUs && tiles / F.least > 32) {
     hipLaunchKernelGGL((join_kernel<F16, D, 4096 / D>), dim3((unsigned)joined, (unsigned)R), dim3(1024),
+                       0, s, F);
+  } else if (joined * R <= 8 * kCUs) {
+    hipLaunchKernelGGL((join_kernel<F16, D, 1024 / D>), dim3((unsigned)joined, (unsigned)R), dim3(256),
                        0, s, F);
   } else {
     constexpr int J = 2, RPB = 1024 / (D * J);
@@ -646,6 +671,18 @@ template <bool F16, int D> hipError_t launch_few(Few F, bool wide, bool beside, 
 }
 
 }  // namespace
+
+// Whether few_kernel takes the own keys of N requests with R query rows a head. Up to 32: always, and up
+// to 64 over long contexts (by what the tables hold), where the items' meetings cost more than reading
+// codes in several waves: 16 tokens of 4 heads a head, us a call, few_kernel and items: D 128: 64
+// requests of up to 4000 own keys 93 and 130, of up to 300 37 and 34; 8 of up to 4000 31 and 34, of up
+// to 1000 23 and 20; one 21 and 18. D 64: 64 of up to 4000 56 and 67, of up to 1000 34 and 31. D 256:
+// 64 of up to 300 58 and 61, 8 of up to 1000 34 and 29. (65 to 128 rows, 64 requests of up to 4000: 154
+// and 146.)
+bool few_rows(const xpress_cache& c, int N, int R, int shared) {
+  const int64_t keys = (int64_t)N * c.Hkv * ((int64_t)c.table_ld * c.page - shared);
+  return R <= 32 || (R <= kFewRows4 && keys * c.D * c.D >= (int64_t)1 << 32);
+}
 
 size_t few_scratch_bytes(const xpress_cache& c, int N, int B, int Hq) {
   const int R = B * (Hq / c.Hkv);
@@ -662,12 +699,14 @@ hipError_t launch_block_attention4(const xpress_cache& c, int layer, const void*
   Args A = args_of(c, p, layer, q, q_ld, seq, N, B, Hq, scale, shared, out, out_ld, lse, ws);
   const bool f16 = value_type(c) == XPRESS_F16;
   const int R = B * A.G;
-  if (R > kFewRows4) return launch_values<true>(A, c.D, f16, p.wide, s);
-  Few F{A, 0, false, nullptr, nullptr, nullptr};
+  if (!few_rows(c, N, R, shared)) return launch_values<true>(A, c.D, f16, p.wide, s);
+  Few F{A, 0, 2, few_waves(c.D, R), false, nullptr, nullptr, nullptr};
   const bool beside = p.s_sh && !p.wide && c.D != 256;
   if (N <= kFewRequests) {
     const int items = c.Hkv * p.tiles_sh * p.s_sh;
-    F.parts = beside ? 4 * std::max(kCUs, kCUs * narrow_per_cu(c.D) - items) : few_parts(c.D, R);
+    F.parts = few_parts(c.D, R);
+    if (beside)
+      F.parts = 4 / F.waves * std::max(kCUs, kCUs * narrow_per_cu(c.D) - items);
     F.by_pair = p.s_sh || N * c.Hkv <= F.parts;
   }
   // the shared part's slots and one of every row, then the parts' (attention_scratch_bytes has room)

@@ -403,6 +403,25 @@ def test_many_short_requests():
         x.check(x.run(x.cache()), what=f"{len(lengths)} requests, D {D}")
 
 
+@pytest.mark.parametrize("D,ld", [(64, 2048), (128, 2048), (256, 512)])
+@pytest.mark.parametrize("B,G,shared", [(16, 4, 0), (16, 3, 0), (13, 3, 100), (33, 1, 70), (2, 2, 0)])
+def test_blocks_under_tables_for_long_contexts(D, ld, B, G, shared):
+    """Requests of 17 to 64 query rows a head in several waves, where the tables could hold much more
+    than they do."""
+    N, Hkv = 8, 4
+    lengths = [shared + n for n in (1, 40, 0, 33, 300, 97, 64, 31)]
+    lengths[2] = 0
+    x = Case4(lengths=lengths, shared=shared, B=B, Hkv=Hkv, G=G, D=D, page=16, seed=80)
+    wide = np.full((N, ld), -1, np.int32)
+    wide[:, :x.table.shape[1]] = x.table
+    x.table = wide
+    c = x.cache()
+    x.check(x.run(c), what=f"D {D}, {B * G} rows")
+    x.check(x.run(c, shared=0), what="not shared")
+    order = [6, 1, 4]
+    x.check(x.run(c, seq=i32(order), rows=order), rows=order, what="a list")
+
+
 @pytest.mark.parametrize("N,B,G,shared", [(4100, 1, 2, 0), (4100, 1, 2, 64), (5, 1, 2, 0)])
 def test_rows_of_whole_runs_of_tiles(N, B, G, shared):
     """Rows of exactly 64 and 128 tiles of 32 tokens, and one token more or less, which one wave walks
