@@ -23,6 +23,8 @@ constexpr int kThreads = 256;
 constexpr int kChunk = 8192;          // ids of a chunk: 32 a thread
 constexpr int kGroup = 32;            // ids of a group
 constexpr int kGroups = kChunk / kGroup;
+constexpr int kWaves = kThreads / 64;  // of a chunk, each with sums of its own
+constexpr int kFinish = 6;            // workgroups of finish_kernel on a CU
 constexpr int kList = kMostTop * kGroup;  // keys whose places are counted, at most
 
 struct Part {
@@ -40,18 +42,18 @@ struct Args {
   int32_t* rank;
   int64_t* top_ids;
   float* top_logprobs;
-  Part* part;    // [rows, chunks]
+  Part* part;    // [rows, chunks, kWaves]
   void* groups;  // [rows, chunks, kGroups], of the logits' type
 };
 
 // What a row's temperature makes of its logits.
 struct Scale {
-  double inverse;  // 1 / T, 0 for greedy; without temperatures 1
-  float c;         // log2(e) / T
+  float t;  // 0 for greedy; without temperatures 1
+  float c;  // log2(e) / t
   __device__ __forceinline__ Scale(const Args& A, int64_t row) {
-    const float t = A.temperature ? A.temperature[row / A.B] : 1.f;
-    inverse = t > 0.f ? fmax(1.0 / (double)t, 1e-300) : 0.0;
-    c = (float)fmin(inverse * 1.4426950408889634, 1e37);
+    t = A.temperature ? A.temperature[(uint32_t)row / (uint32_t)A.B] : 1.f;  // (below 2^24 rows)
+    t = t > 0.f ? t : 0.f;
+    c = fminf(1.44269504f / t, 1e37f);
   }
   // Whether exponents are x c - unit in one operation, with the unit m c rounded: what its rounding is
   // off by is the same for all, and the sums' unit is what it was rounded to. Where m c is large, or c at
@@ -77,21 +79,48 @@ __device__ __forceinline__ uint64_t key_of(uint32_t order, int index) {
 }
 __device__ __forceinline__ int index_of(uint64_t key) { return (int)(0xffffffffu - (uint32_t)key); }
 
-// Lanes d away (d a power of two) inside groups of eight, without the LDS's help.
-template <int D> __device__ __forceinline__ float lane_xor(float x) {
-  constexpr int P = D == 1 ? 0xB1 : D == 2 ? 0x4E : 0x141;  // quad_perm [1,0,3,2], [2,3,0,1]; half mirror
+// Maxima of numbers. (fmaxf quiets what could be a signalling NaN first, an operation more for each.)
+__device__ __forceinline__ float max_of(float a, float b) {
+  float r;
+  asm("v_max_f32 %0, %1, %2" : "=v"(r) : "v"(a), "v"(b));
+  return r;
+}
+__device__ __forceinline__ float max_of(float a, float b, float c) {
+  float r;
+  asm("v_max3_f32 %0, %1, %2, %3" : "=v"(r) : "v"(a), "v"(b), "v"(c));
+  return r;
+}
+// A neighbouring lane's value, without the LDS's help.
+template <int P> __device__ __forceinline__ float lane_by(float x) {
   return __uint_as_float(__builtin_amdgcn_update_dpp(0, __float_as_uint(x), P, 0xf, 0xf, false));
 }
-// The maximum over N = 4 or 8 neighbouring lanes (of eight the second four, mirrored, have one value).
+// The maximum over N = 4 or 8 neighbouring lanes.
 template <int N> __device__ __forceinline__ float max_of_group(float x) {
-  x = fmaxf(x, lane_xor<1>(x));
-  x = fmaxf(x, lane_xor<2>(x));
-  return N == 4 ? x : fmaxf(x, lane_xor<4>(x));
+  x = max_of(x, lane_by<0xB1>(x));                        // quad_perm 1 0 3 2
+  x = max_of(x, lane_by<0x4E>(x));                        // quad_perm 2 3 0 1
+  return N == 4 ? x : max_of(x, lane_by<0x141>(x));  // half mirror
 }
-template <int FROM> __device__ __forceinline__ float max_of_lanes(float x) {
-#pragma unroll
-  for (int d = FROM; d < 64; d *= 2) x = fmaxf(x, __shfl_xor(x, d));
-  return x;
+// f(x, y) of all lanes: neighbours by DPP, whole rows of 16 through the LDS's crossbar.
+template <class F> __device__ __forceinline__ uint32_t of_wave(uint32_t x, F&& f) {
+  x = f(x, (uint32_t)__builtin_amdgcn_update_dpp(0, x, 0xB1, 0xf, 0xf, false));   // quad_perm 1 0 3 2
+  x = f(x, (uint32_t)__builtin_amdgcn_update_dpp(0, x, 0x4E, 0xf, 0xf, false));   // quad_perm 2 3 0 1
+  x = f(x, (uint32_t)__builtin_amdgcn_update_dpp(0, x, 0x141, 0xf, 0xf, false));  // half mirror
+  x = f(x, (uint32_t)__builtin_amdgcn_update_dpp(0, x, 0x140, 0xf, 0xf, false));  // mirror
+  x = f(x, (uint32_t)__shfl_xor((int)x, 16));
+  return f(x, (uint32_t)__shfl_xor((int)x, 32));
+}
+__device__ __forceinline__ float wave_max(float x) {
+  return __uint_as_float(of_wave(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(max_of(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+__device__ __forceinline__ float wave_sum(float x) {
+  return __uint_as_float(of_wave(__float_as_uint(x), [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+__device__ __forceinline__ int wave_sum(int x) {
+  return (int)of_wave((uint32_t)x, [](uint32_t a, uint32_t b) { return a + b; });
 }
 
 template <class T> __device__ __forceinline__ T narrow(float x);
@@ -99,8 +128,12 @@ template <> __device__ __forceinline__ uint16_t narrow(float x) { return __float
 template <> __device__ __forceinline__ _Float16 narrow(float x) { return (_Float16)x; }
 template <> __device__ __forceinline__ float narrow(float x) { return x; }
 
-// Bound by HBM: 16 KiB of 16-bit logits a workgroup, eight workgroups a CU.
-template <class T> __global__ __launch_bounds__(kThreads, 8) void chunks_kernel(Args A) {
+// One chunk of one row, 16 KiB of 16-bit logits; each wave leaves sums of its own. Bound by HBM, close to
+// the vector unit's 280 operations a wave (with 430, of which quieted maxima, a join of the waves and
+// bounds checks of every piece were the rest, 2048 rows of 151,936 ids took 158 us instead of 144). Six
+// workgroups a CU: with eight the careful path spills (222 us). Workgroups that go on from chunk to chunk
+// and ask for the next one's logits ahead were slower (224 us and more).
+template <class T> __global__ __launch_bounds__(kThreads, 6) void chunks_kernel(Args A) {
   constexpr int E = Row<T>::E, K = kChunk / kThreads / E;  // K loads; as many lanes hold a group
   static_assert(K * E == kGroup, "a thread's ids are as many as a group's");
   const int c = blockIdx.x % A.chunks, t = threadIdx.x;
@@ -109,87 +142,92 @@ template <class T> __global__ __launch_bounds__(kThreads, 8) void chunks_kernel(
   if (token < 0) return;
   const Row<T> row(static_cast<const T*>(A.logits) + r * A.ld, A.V);
   const float mine = A.token && token < A.V ? ordered(to_f32<T>(row.x[token])) : INFINITY;
+  Piece<T> p[K];
+  const int64_t first = (int64_t)c * kChunk - row.off;
+  if (first >= 0 && first + kChunk <= A.V) {
+    const uint4* from = reinterpret_cast<const uint4*>(row.x + first) + t;
+#pragma unroll
+    for (int k = 0; k < K; ++k) p[k] = __builtin_bit_cast(Piece<T>, from[k * kThreads]);
+  } else {
+#pragma unroll
+    for (int k = 0; k < K; ++k) p[k] = row.load((int64_t)c * (kChunk / E) + k * kThreads + t);
+  }
   float x[K][E];
 #pragma unroll
-  for (int k = 0; k < K; ++k) {
-    const Piece<T> p = row.load((int64_t)c * (kChunk / E) + k * kThreads + t);
+  for (int k = 0; k < K; ++k)
 #pragma unroll
     for (int e = 0; e < E; ++e) {
-      x[k][e] = p[e];
+      x[k][e] = p[k][e];
       asm("" : "+v"(x[k][e]));  // (fp16: or both the halves and their values stay live, and spill)
     }
-  }
-  int above = 0;
-  float best = -INFINITY, m = -INFINITY;
-#pragma unroll
-  for (int k = 0; k < K; ++k) {
-    float g = -INFINITY;
-#pragma unroll
-    for (int e = 0; e < E; ++e) g = fmaxf(g, x[k][e]);
-    if (__ballot(g > mine)) {  // (most pieces hold no id above a likely token)
-#pragma unroll
-      for (int e = 0; e < E; ++e) above += x[k][e] > mine ? 1 : 0;
-    }
-    g = max_of_group<K>(g);
-    m = fmaxf(m, g);
-    best = t % K == k ? g : best;
-  }
-  static_cast<T*>(A.groups)[(r * A.chunks + c) * kGroups + t % K * (kGroups / K) + t / K] =
-      narrow<T>(best);
-  m = max_of_lanes<K>(m);
   const Scale scale(A, r);
-  float sum = 0.f, zsum = 0.f;
-  if (m == INFINITY) {  // the ids that hold it share all
+  int above;
+  float m, sum, zsum;
+  // What the chunk leaves, of x as it is: numbers.
+  auto maxima = [&] {
+    above = 0;
+    m = -INFINITY;
+    float best = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < K; ++k) {
+      float g = max_of(x[k][0], x[k][1]);
+#pragma unroll
+      for (int e = 2; e < E; e += 2) g = max_of(g, x[k][e], x[k][e + 1]);
+      if (__ballot(g > mine)) {  // (most pieces hold no id above a likely token)
+#pragma unroll
+        for (int e = 0; e < E; ++e) above += x[k][e] > mine ? 1 : 0;
+      }
+      g = max_of_group<K>(g);
+      m = max_of(m, g);
+      best = t % K == k ? g : best;
+    }
+    static_cast<T*>(A.groups)[(r * A.chunks + c) * kGroups + t % K * (kGroups / K) + t / K] =
+        narrow<T>(best);
+    m = wave_max(m);
+  };
+  auto sums = [&](auto exponent) {
+    sum = zsum = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
-      for (int e = 0; e < E; ++e) sum += x[k][e] == m ? 1.f : 0.f;
-  } else if (m > -INFINITY && scale.inverse != 0.0) {
-    // (the maximum with -1e30 turns NaN and -inf into no weight)
-    auto add = [&](auto exponent) {
+      for (int e = 0; e < E; ++e) {
+        const float z = exponent(x[k][e]), w = __builtin_amdgcn_exp2f(z);
+        sum += w;
+        zsum = fmaf(w, z, zsum);
+      }
+  };
+  maxima();
+  {
+    const float unit = m * scale.c;
+    sums([&](float v) { return fmaf(v, scale.c, -unit); });
+  }
+  // NaN, and infinities (products of 0 and -inf), make a sum NaN: then, and where the scale asks for it,
+  // once more with care.
+  if (__ballot(!(zsum <= 0.f)) || !scale.plain(m) || scale.t == 0.f) {
+#pragma unroll
+    for (int k = 0; k < K; ++k)
+#pragma unroll
+      for (int e = 0; e < E; ++e) x[k][e] = ordered(x[k][e]);
+    maxima();
+    sum = zsum = 0.f;
+    if (m == INFINITY) {  // the ids that hold it share all
 #pragma unroll
       for (int k = 0; k < K; ++k)
 #pragma unroll
-        for (int e = 0; e < E; ++e) {
-          const float z = fmaxf(exponent(x[k][e]), -1e30f), w = __builtin_amdgcn_exp2f(z);
-          sum += w;
-          zsum = fmaf(w, z, zsum);
-        }
-    };
-    if (scale.plain(m)) {
+        for (int e = 0; e < E; ++e) sum += x[k][e] == m ? 1.f : 0.f;
+    } else if (m > -INFINITY && scale.t != 0.f) {
       const float unit = m * scale.c;
-      add([&](float v) { return fmaf(v, scale.c, -unit); });
-    } else {
-      add([&](float v) { return (v - m) * scale.c; });
+      // (the maximum with -1e30: no weight, and no NaN of it)
+      if (scale.plain(m))
+        sums([&](float v) { return fmaxf(fmaf(v, scale.c, -unit), -1e30f); });
+      else
+        sums([&](float v) { return fmaxf((v - m) * scale.c, -1e30f); });
     }
   }
-#pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    sum += __shfl_xor(sum, d);
-    zsum += __shfl_xor(zsum, d);
-    above += __shfl_xor(above, d);
-  }
-  __shared__ Part s_part[kThreads / 64];
-  if ((t & 63) == 0) s_part[t >> 6] = Part{m, sum, zsum, above};
-  __syncthreads();
-  if (t != 0) return;
-  Part all = s_part[0];
-#pragma unroll
-  for (int i = 1; i < kThreads / 64; ++i) all.m = fmaxf(all.m, s_part[i].m);
-  all.sum = all.zsum = 0.f;
-  all.above = 0;
-#pragma unroll
-  for (int i = 0; i < kThreads / 64; ++i) {
-    const Part& p = s_part[i];
-    all.above += p.above;
-    if (p.m == -INFINITY || (all.m == INFINITY && p.m != INFINITY)) continue;
-    const float z =
-        p.m == all.m ? 0.f : fmaxf((float)(scale.unit(p.m) - scale.unit(all.m)), -1e30f);
-    const float f = __builtin_amdgcn_exp2f(z);
-    all.sum += f * p.sum;
-    all.zsum += f * fmaf(z, p.sum, p.zsum);
-  }
-  A.part[r * A.chunks + c] = all;
+  sum = wave_sum(sum);
+  zsum = wave_sum(zsum);
+  above = wave_sum(above);
+  if (t % 64 == 0) A.part[(r * A.chunks + c) * kWaves + t / 64] = Part{m, sum, zsum, above};
 }
 
 // Places of the n keys in `list` (all different); take(place, key) for the first `count` of them.
@@ -198,26 +236,16 @@ __device__ __forceinline__ void in_order(const uint64_t* list, int n, int count,
   for (int i = threadIdx.x; i < n; i += kThreads) {
     const uint64_t key = list[i];
     int place = 0;
-#pragma unroll 8
+#pragma unroll 4
     for (int j = 0; j < n; ++j) place += list[j] > key ? 1 : 0;
     if (place < count) take(place, key);
   }
 }
 
-// A 16-byte piece of the groups' maxima, E of them; past the last -inf's order and below all keys: 0.
-template <class T> struct Best {
-  static constexpr int E = Row<T>::E;
-  uint32_t o[E];
-  __device__ __forceinline__ void load(const void* groups, int64_t piece, int n) {
-    const Piece<T> p =
-        __builtin_bit_cast(Piece<T>, static_cast<const uint4*>(groups)[piece]);
-#pragma unroll
-    for (int e = 0; e < E; ++e) o[e] = piece * E + e < n ? order_of(p[e]) : 0u;
-  }
-};
-
-template <class T> __global__ __launch_bounds__(kThreads) void finish_kernel(Args A) {
-  constexpr int E = Row<T>::E, HOLD = 32 / E;  // pieces that stay in a thread's registers
+// A row's end: dependent loads and meetings of 10 us, so few registers and many rows at a time. One row
+// of 151,936 ids with 20 alternatives 9.7 us, 2048 rows with 5 each 20.
+template <class T> __global__ __launch_bounds__(kThreads, kFinish) void finish_kernel(Args A) {
+  constexpr int E = Row<T>::E;
   const int64_t r = blockIdx.x;
   const int t = threadIdx.x, lane = t & 63;
   const int64_t token = A.token ? A.token[r] : 0;
@@ -235,26 +263,23 @@ template <class T> __global__ __launch_bounds__(kThreads) void finish_kernel(Arg
   }
   const Row<T> row(static_cast<const T*>(A.logits) + r * A.ld, A.V);
   const Scale scale(A, r);
-  const bool greedy = scale.inverse == 0.0;
+  const bool greedy = scale.t == 0.f;
   const int n_groups = (int)(((int64_t)A.V + row.off + kGroup - 1) / kGroup);
   const int count = min(max(A.top, greedy ? 1 : 0), A.V), of_groups = min(count, n_groups);
   const int pieces = (n_groups + E - 1) / E;
-  const T* groups = static_cast<const T*>(A.groups) + r * A.chunks * kGroups;
-  Best<T> held[HOLD];
-  if (count > 0) {
-#pragma unroll
-    for (int i = 0; i < HOLD; ++i) held[i].load(groups, min(t + i * kThreads, pieces - 1), n_groups);
-  }
+  const uint4* groups = reinterpret_cast<const uint4*>(static_cast<const T*>(A.groups) +
+                                                       r * A.chunks * kGroups);
   // the row's sums, in every wave
   const float given = A.token && token < A.V ? ordered(to_f32<T>(row.x[token])) : -INFINITY;
   float m = -INFINITY;
   double sum = 0, zsum = 0;
   int above = 0;
-  const Part* part = A.part + r * A.chunks;
-  const Part mine = lane < A.chunks ? part[lane] : Part{-INFINITY, 0.f, 0.f, 0};
-  for (int i = lane; i < A.chunks; i += 64) m = fmaxf(m, i == lane ? mine.m : part[i].m);
-  m = max_of_lanes<1>(m);
-  for (int i = lane; i < A.chunks; i += 64) {
+  const Part* part = A.part + r * A.chunks * kWaves;
+  const int parts = A.chunks * kWaves;
+  const Part mine = lane < parts ? part[lane] : Part{-INFINITY, 0.f, 0.f, 0};
+  for (int i = lane; i < parts; i += 64) m = fmaxf(m, i == lane ? mine.m : part[i].m);
+  m = wave_max(m);
+  for (int i = lane; i < parts; i += 64) {
     const Part p = i == lane ? mine : part[i];
     above += p.above;
     if (p.m == -INFINITY || (m == INFINITY && p.m != INFINITY)) continue;
@@ -266,8 +291,8 @@ template <class T> __global__ __launch_bounds__(kThreads) void finish_kernel(Arg
   for (int d = 32; d; d >>= 1) {
     sum += __shfl_xor(sum, d);
     zsum += __shfl_xor(zsum, d);
-    above += __shfl_xor(above, d);
   }
+  above = wave_sum(above);
   const double log_sum = log(sum);
   // of the sum relative to the maximum's own weight
   const double log_top =
@@ -276,7 +301,7 @@ template <class T> __global__ __launch_bounds__(kThreads) void finish_kernel(Arg
   // log p of a logit (greedy: of one that is not the first best)
   auto logp = [&](float x) {
     if (greedy || m == -INFINITY || x == -INFINITY || (m == INFINITY && x != m)) return -INFINITY;
-    return (float)((x == m ? 0.0 : ((double)x - (double)m) * scale.inverse) - log_top);
+    return (float)((x == m ? 0.0 : ((double)x - (double)m) / scale.t) - log_top);
   };
 
   __shared__ uint64_t s_list[kList];
@@ -286,17 +311,20 @@ template <class T> __global__ __launch_bounds__(kThreads) void finish_kernel(Arg
   __shared__ int s_n, s_first;
   if (count > 0) {
     // all of this thread's maxima: f(order, index) of each
+    auto piece = [&](const uint4& u, int i, auto&& f) {
+      const Piece<T> p = __builtin_bit_cast(Piece<T>, u);
+#pragma unroll
+      for (int e = 0; e < E; ++e)
+        if (i * E + e < n_groups) f(order_of(p[e]), i * E + e);
+    };
     auto each = [&](auto&& f) {
+      for (int i0 = t; i0 < pieces; i0 += 4 * kThreads) {  // four loads in flight
+        uint4 u[4];
 #pragma unroll
-      for (int i = 0; i < HOLD; ++i)
-        if (t + i * kThreads < pieces)
+        for (int i = 0; i < 4; ++i) u[i] = groups[min(i0 + i * kThreads, pieces - 1)];
 #pragma unroll
-          for (int e = 0; e < E; ++e) f(held[i].o[e], (t + i * kThreads) * E + e);
-      for (int i = t + HOLD * kThreads; i < pieces; i += kThreads) {
-        Best<T> b;
-        b.load(groups, i, n_groups);
-#pragma unroll
-        for (int e = 0; e < E; ++e) f(b.o[e], i * E + e);
+        for (int i = 0; i < 4; ++i)
+          if (i0 + i * kThreads < pieces) piece(u[i], i0 + i * kThreads, f);
       }
     };
     uint32_t top = 0;
@@ -321,7 +349,7 @@ template <class T> __global__ __launch_bounds__(kThreads) void finish_kernel(Arg
       }
     }
     each([&](uint32_t o, int g) {
-      if (o < least || o == 0) return;
+      if (o < least) return;
       const int at = atomicAdd(&s_n, 1);
       if (at < kList) s_list[at] = key_of(o, g);
     });
@@ -337,7 +365,7 @@ template <class T> __global__ __launch_bounds__(kThreads) void finish_kernel(Arg
       for (int k = 0; k < of_groups; ++k) {
         uint64_t best = 0;
         each([&](uint32_t o, int g) {
-          const uint64_t key = o ? key_of(o, g) : 0;
+          const uint64_t key = key_of(o, g);
           if (key < last) best = max(best, key);
         });
         __syncthreads();
@@ -417,7 +445,7 @@ int64_t chunks_of(int64_t V) { return (V + 7 + kChunk - 1) / kChunk; }
 int64_t logprobs_items(int64_t rows, int64_t V) { return rows * chunks_of(V); }
 
 size_t logprobs_scratch_bytes(int64_t rows, int64_t V) {
-  return (size_t)(rows * chunks_of(V)) * (sizeof(Part) + kGroups * sizeof(float));  // (of any type)
+  return (size_t)(rows * chunks_of(V)) * (kWaves * sizeof(Part) + kGroups * sizeof(float));  // (of any type)
 }
 
 hipError_t launch_token_logprobs(const void* logits, uint32_t dtype, int64_t ld, const int64_t* token,
@@ -427,7 +455,7 @@ hipError_t launch_token_logprobs(const void* logits, uint32_t dtype, int64_t ld,
   const int rows = N * B;
   Args A{logits, ld, token, temperature, B, (int)V, top, (int)chunks_of(V), logprob, entropy, rank,
          top_ids, top_logprobs, static_cast<Part*>(ws), nullptr};
-  A.groups = A.part + (size_t)rows * A.chunks;
+  A.groups = A.part + (size_t)rows * A.chunks * kWaves;
   switch (dtype) {
     case XPRESS_BF16: return launch_t<uint16_t>(A, rows, s);
     case XPRESS_F16: return launch_t<_Float16>(A, rows, s);
