@@ -24,7 +24,7 @@ constexpr int kChunk = 8192;          // ids of a chunk: 32 a thread
 constexpr int kGroup = 32;            // ids of a group
 constexpr int kGroups = kChunk / kGroup;
 constexpr int kWaves = kThreads / 64;  // of a chunk, each with sums of its own
-constexpr int kFinish = 6;            // workgroups of finish_kernel on a CU
+constexpr int kFinish = 8;            // workgroups of finish_kernel on a CU
 constexpr int kList = kMostTop * kGroup;  // keys whose places are counted, at most
 
 struct Part {
@@ -130,7 +130,7 @@ template <> __device__ __forceinline__ float narrow(float x) { return x; }
 
 // One chunk of one row, 16 KiB of 16-bit logits; each wave leaves sums of its own. Bound by HBM, close to
 // the vector unit's 280 operations a wave (with 430, of which quieted maxima, a join of the waves and
-// bounds checks of every piece were the rest, 2048 rows of 151,936 ids took 158 us instead of 144). Six
+// bounds checks of every piece were the rest, 2048 rows of 151,936 ids took 158 us in all instead of 144). Six
 // workgroups a CU: with eight the careful path spills (222 us). Workgroups that go on from chunk to chunk
 // and ask for the next one's logits ahead were slower (224 us and more).
 template <class T> __global__ __launch_bounds__(kThreads, 6) void chunks_kernel(Args A) {
@@ -230,20 +230,26 @@ template <class T> __global__ __launch_bounds__(kThreads, 6) void chunks_kernel(
   if (t % 64 == 0) A.part[(r * A.chunks + c) * kWaves + t / 64] = Part{m, sum, zsum, above};
 }
 
-// Places of the n keys in `list` (all different); take(place, key) for the first `count` of them.
+// Places of the n keys in `list` (all different); take(place, key) for the first `count` of them. Four
+// threads a key.
 template <class F>
 __device__ __forceinline__ void in_order(const uint64_t* list, int n, int count, F&& take) {
-  for (int i = threadIdx.x; i < n; i += kThreads) {
+  const int part = threadIdx.x & 3;
+  for (int i = threadIdx.x >> 2; i < n; i += kThreads / 4) {
     const uint64_t key = list[i];
     int place = 0;
 #pragma unroll 4
-    for (int j = 0; j < n; ++j) place += list[j] > key ? 1 : 0;
-    if (place < count) take(place, key);
+    for (int j = part; j < n; j += 4) place += list[j] > key ? 1 : 0;
+    place += __builtin_amdgcn_update_dpp(0, place, 0xB1, 0xf, 0xf, false);  // quad_perm 1 0 3 2
+    place += __builtin_amdgcn_update_dpp(0, place, 0x4E, 0xf, 0xf, false);  // quad_perm 2 3 0 1
+    if (part == 0 && place < count) take(place, key);
   }
 }
 
-// A row's end: dependent loads and meetings of 10 us, so few registers and many rows at a time. One row
-// of 151,936 ids with 20 alternatives 9.7 us, 2048 rows with 5 each 20.
+// A row's end: dependent loads and meetings of about 9 us, so few registers, for many rows at a time. The
+// sums, in 64 bits, are one wave's work beside the search of another (in every wave, before the search:
+// 9.7 us instead of 9.3 for one row of 151,936 ids with 20 alternatives, 20 instead of 17.6 for 2048 rows
+// with 5). The maxima held in registers between their two uses spill: 24 us for the 2048 rows.
 template <class T> __global__ __launch_bounds__(kThreads, kFinish) void finish_kernel(Args A) {
   constexpr int E = Row<T>::E;
   const int64_t r = blockIdx.x;
@@ -269,46 +275,56 @@ template <class T> __global__ __launch_bounds__(kThreads, kFinish) void finish_k
   const int pieces = (n_groups + E - 1) / E;
   const uint4* groups = reinterpret_cast<const uint4*>(static_cast<const T*>(A.groups) +
                                                        r * A.chunks * kGroups);
-  // the row's sums, in every wave
   const float given = A.token && token < A.V ? ordered(to_f32<T>(row.x[token])) : -INFINITY;
-  float m = -INFINITY;
-  double sum = 0, zsum = 0;
-  int above = 0;
-  const Part* part = A.part + r * A.chunks * kWaves;
-  const int parts = A.chunks * kWaves;
-  const Part mine = lane < parts ? part[lane] : Part{-INFINITY, 0.f, 0.f, 0};
-  for (int i = lane; i < parts; i += 64) m = fmaxf(m, i == lane ? mine.m : part[i].m);
-  m = wave_max(m);
-  for (int i = lane; i < parts; i += 64) {
-    const Part p = i == lane ? mine : part[i];
-    above += p.above;
-    if (p.m == -INFINITY || (m == INFINITY && p.m != INFINITY)) continue;
-    const double z = p.m == m ? 0.0 : scale.unit(p.m) - scale.unit(m), f = exp2(z);
-    sum += f * p.sum;
-    if (f > 0) zsum += f * (z * p.sum + p.zsum);
-  }
+  __shared__ double s_sums[3];  // maximum, log of the sum, entropy
+  __shared__ int s_above;
+  // The row's sums, by the second wave (while the first looks for the best groups).
+  auto join = [&] {
+    const Part* part = A.part + r * A.chunks * kWaves;
+    const int parts = A.chunks * kWaves;
+    const Part mine = lane < parts ? part[lane] : Part{-INFINITY, 0.f, 0.f, 0};
+    float m = -INFINITY;
+    double sum = 0, zsum = 0;
+    int above = 0;
+    for (int i = lane; i < parts; i += 64) m = fmaxf(m, i == lane ? mine.m : part[i].m);
+    m = wave_max(m);
+    for (int i = lane; i < parts; i += 64) {
+      const Part p = i == lane ? mine : part[i];
+      above += p.above;
+      if (p.m == -INFINITY || (m == INFINITY && p.m != INFINITY)) continue;
+      const double z = p.m == m ? 0.0 : scale.unit(p.m) - scale.unit(m), f = exp2(z);
+      sum += f * p.sum;
+      if (f > 0) zsum += f * (z * p.sum + p.zsum);
+    }
 #pragma unroll
-  for (int d = 32; d; d >>= 1) {
-    sum += __shfl_xor(sum, d);
-    zsum += __shfl_xor(zsum, d);
-  }
-  above = wave_sum(above);
-  const double log_sum = log(sum);
-  // of the sum relative to the maximum's own weight
-  const double log_top =
-      m == INFINITY ? log_sum
+    for (int d = 32; d; d >>= 1) {
+      sum += __shfl_xor(sum, d);
+      zsum += __shfl_xor(zsum, d);
+    }
+    above = wave_sum(above);
+    if (lane) return;
+    const double log_sum = log(sum);
+    s_sums[0] = m;
+    // of the sum relative to the maximum's own weight
+    s_sums[1] = m == INFINITY
+                    ? log_sum
                     : log_sum - ((double)m * scale.c - scale.unit(m)) * 0.69314718055994531;
+    s_sums[2] = log_sum - zsum / sum * 0.69314718055994531;
+    s_above = above;
+  };
   // log p of a logit (greedy: of one that is not the first best)
   auto logp = [&](float x) {
+    const float m = (float)s_sums[0];
     if (greedy || m == -INFINITY || x == -INFINITY || (m == INFINITY && x != m)) return -INFINITY;
-    return (float)((x == m ? 0.0 : ((double)x - (double)m) / scale.t) - log_top);
+    return (float)((x == m ? 0.0 : ((double)x - (double)m) / scale.t) - s_sums[1]);
   };
 
   __shared__ uint64_t s_list[kList];
   __shared__ uint32_t s_best[kThreads];
   __shared__ int s_group[kMostTop];
   __shared__ uint64_t s_floor;
-  __shared__ int s_n, s_first;
+  __shared__ int s_n, s_ids, s_first;
+  __shared__ uint32_t s_least;
   if (count > 0) {
     // all of this thread's maxima: f(order, index) of each
     auto piece = [&](const uint4& u, int i, auto&& f) {
@@ -330,13 +346,12 @@ template <class T> __global__ __launch_bounds__(kThreads, kFinish) void finish_k
     uint32_t top = 0;
     each([&](uint32_t o, int) { top = max(top, o); });
     s_best[t] = top;
-    if (t == 0) s_n = 0;
+    if (t == 0) s_n = s_ids = 0;
     __syncthreads();
     // The largest value that as many threads' best ones reach as there are places (0: fewer threads
-    // have any), one bit after the other, in every wave.
-    uint32_t least = 0;
-    {
-      uint32_t b[kThreads / 64];
+    // have any), one bit after the other, by the first wave.
+    if (t < 64) {
+      uint32_t b[kThreads / 64], least = 0;
 #pragma unroll
       for (int i = 0; i < kThreads / 64; ++i) b[i] = s_best[lane + 64 * i];
       for (int bit = 31; bit >= 0; --bit) {
@@ -347,7 +362,12 @@ template <class T> __global__ __launch_bounds__(kThreads, kFinish) void finish_k
         if (n >= of_groups) least = next;
         if (n == of_groups) break;  // (no more than needed: what is above is as good)
       }
+      s_least = least;
+    } else if (t < 128) {
+      join();
     }
+    __syncthreads();
+    const uint32_t least = s_least;
     each([&](uint32_t o, int g) {
       if (o < least) return;
       const int at = atomicAdd(&s_n, 1);
@@ -380,49 +400,51 @@ template <class T> __global__ __launch_bounds__(kThreads, kFinish) void finish_k
     __syncthreads();
     // ids below the last of as many groups as there are places are not among the first
     const uint32_t cut = of_groups == count ? (uint32_t)(s_floor >> 32) : 0u;
-    if (t == 0) s_n = 0;
-    __syncthreads();
-    for (int i0 = t; i0 < of_groups * kGroup; i0 += 4 * kThreads) {  // four loads in flight
+    const int n_ids = of_groups * kGroup;
+    for (int i0 = t; i0 < n_ids; i0 += 4 * kThreads) {  // four loads in flight
       float x[4];
       int id[4];
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int i = i0 + j * kThreads, g = s_group[min(i / kGroup, of_groups - 1)];
         const int64_t v = (int64_t)g * kGroup + i % kGroup - row.off;
-        id[j] = i < of_groups * kGroup && v >= 0 && v < A.V ? (int)v : -1;
+        id[j] = i < n_ids && v >= 0 && v < A.V ? (int)v : -1;
         x[j] = to_f32<T>(row.x[max(id[j], 0)]);
       }
 #pragma unroll
       for (int j = 0; j < 4; ++j)
         if (id[j] >= 0 && order_of(x[j]) >= cut)
-          s_list[atomicAdd(&s_n, 1)] = key_of(order_of(x[j]), id[j]);
+          s_list[atomicAdd(&s_ids, 1)] = key_of(order_of(x[j]), id[j]);
     }
     __syncthreads();
-    in_order(s_list, s_n, count, [&](int place, uint64_t key) {
+    in_order(s_list, s_ids, count, [&](int place, uint64_t key) {
       if (place == 0) s_first = index_of(key);
       if (place >= A.top) return;
       const float x = value_of((uint32_t)(key >> 32));
       A.top_ids[r * A.top + place] = index_of(key);
-      A.top_logprobs[r * A.top + place] = greedy && place == 0 && m > -INFINITY ? 0.f : logp(x);
+      A.top_logprobs[r * A.top + place] = greedy && place == 0 && s_sums[0] > -INFINITY ? 0.f : logp(x);
     });
     for (int k = count + t; k < A.top; k += kThreads) {
       A.top_ids[r * A.top + k] = -1;
       A.top_logprobs[r * A.top + k] = -INFINITY;
     }
     __syncthreads();
+  } else {
+    if (t >= 64 && t < 128) join();
+    __syncthreads();
   }
   if (t != 0) return;
   if (A.entropy) {
-    const bool none = greedy || m == -INFINITY;
-    A.entropy[r] = none ? 0.f : (float)(log_sum - zsum / sum * 0.69314718055994531);
+    const bool none = greedy || s_sums[0] == -INFINITY;
+    A.entropy[r] = none ? 0.f : (float)s_sums[2];
   }
   const bool inside = token < A.V;
-  if (A.token && A.rank) A.rank[r] = inside ? above : -1;
+  if (A.token && A.rank) A.rank[r] = inside ? s_above : -1;
   if (A.token && A.logprob) {
     float l = -INFINITY;
     if (inside) {
       if (greedy)
-        l = token == s_first && m > -INFINITY ? 0.f : -INFINITY;
+        l = token == s_first && s_sums[0] > -INFINITY ? 0.f : -INFINITY;
       else
         l = logp(given);
     }
