@@ -389,7 +389,8 @@ xpress_status xpress_cache_append_if(const xpress_cache* c, const int32_t* lacki
 
 /* Reads back K and V of one layer: token b of list entry i is position first[i] + b of row seq[i], for
  * b < B (first NULL: the row's last B tokens, as an append takes them); positions outside the row, and
- * rows outside the cache, give 0. From 4 bits the values are those that are held, exactly.
+ * rows outside the cache, give 0. From 4 bits the values are those that are held, exactly. The list may
+ * hold a row more than once.
  * first: [N] int32 on the device, nullable. k_out, v_out: token i*B + b at element (i*B + b)*ld_out,
  * [Hkv, D] dense, the cache's type, 16-byte aligned, ld_out a multiple of 8 and at least Hkv*D; they
  * do not overlap. N*B*Hkv < 2^26. */

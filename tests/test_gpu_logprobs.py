@@ -268,3 +268,60 @@ def test_streams_and_captured_calls():
         for name in mine:
             assert torch.equal(mine[name], other[name]), (rep, name)
         check(x.cpu(), token.cpu(), temps.cpu(), top, mine, f"replay {rep}")
+
+
+@pytest.mark.parametrize("dtype,bits", [(torch.bfloat16, 0x7f81), (torch.float16, 0x7c01),
+                                        (torch.float32, 0x7f800001)], ids=["bf16", "f16", "f32"])
+def test_signalling_nans(dtype, bits):
+    V, top = 20000, 20
+    x = logits(4, V, dtype, 11)
+    word = torch.int32 if dtype == torch.float32 else torch.int16
+    raw = x.view(word)
+    g = torch.Generator().manual_seed(3)
+    raw[0, torch.randint(V, (50,), generator=g)] = bits
+    raw[1, ::2] = bits
+    raw[2, 8192:] = bits | (-1 << (31 if dtype == torch.float32 else 15))
+    raw[3] = bits
+    token = torch.tensor([[5, 7], [9, 11]])
+    for temps in (None, [0.0, 0.7]):
+        for t in (0, top):
+            check(x, token, temps, t, run(x, token, temps, t, 1, 1), f"signalling {temps} {t}")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16, torch.float32],
+                         ids=["bf16", "f16", "f32"])
+def test_vocabularies_that_are_masked(dtype):
+    """A few allowed ids among -inf or the type's lowest value; chunks of nothing else."""
+    V, top = 151936, 20
+    x = logits(6, V, dtype, 12)
+    allowed = [range(0), range(7), range(100000, 100040), range(0, V, 9973), range(8192, 16384), range(V - 3, V)]
+    low = torch.finfo(dtype).min
+    for r, ids in enumerate(allowed):
+        keep = torch.zeros(V, dtype=torch.bool)
+        keep[list(ids)] = True
+        x[r] = torch.where(keep, x[r], low if r % 2 else -math.inf)
+    token = torch.tensor([[0, 3], [100002, 9973], [9000, V - 1]])
+    for temps in (None, [0.6, 0.0, 1.5]):
+        check(x, token, temps, top, run(x, token, temps, top), f"masked {temps}")
+
+
+def test_two_calls_at_once_and_rows_past_32_bits():
+    """Two streams with a workspace each; rows whose last element lies past 2^32 bytes."""
+    V, top, ld = 1000, 5, 1 << 29
+    hold = torch.empty(5 * ld, dtype=torch.bfloat16, device="cuda")
+    view = hold.view(5, ld)[:, :V]
+    x = logits(5, V, torch.bfloat16, 13)
+    view.copy_(x)
+    token = torch.tensor([[1], [2], [3], [4], [999]])
+    d = token.cuda()
+    outs = [outputs(5, top) for _ in range(2)]
+    streams = [torch.cuda.Stream() for _ in range(2)]
+    spaces = [xpress.logprobs_workspace(5, V, top) for _ in range(2)]
+    torch.cuda.synchronize()
+    for _ in range(3):
+        for s, o, ws in zip(streams, outs, spaces):
+            with torch.cuda.stream(s):
+                xpress.token_logprobs(view, d, ws=ws, **o)
+    torch.cuda.synchronize()
+    for o in outs:
+        check(x, token, None, top, o, "at once")

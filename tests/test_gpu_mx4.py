@@ -492,3 +492,69 @@ def test_long_row_in_a_big_pool():
         assert bool(((out.cpu().double().view(2 * B, 8, D) - want).abs() <= bound).all())
     del c
     torch.cuda.empty_cache()
+
+
+@pytest.mark.parametrize("B", [1, 2, 17])
+def test_more_rows_than_a_grid_has_in_its_second_direction(B):
+    """70,001 rows of one head: appended to and read."""
+    N, D, dtype = 70001, 64, torch.bfloat16
+    g = torch.Generator().manual_seed(B)
+    pool = torch.zeros(1, 2 * N, 1, 1, 17 * D // 2, dtype=torch.uint8, device="cuda")
+    length = torch.randint(1, 33, (N,), generator=g, dtype=torch.int32)
+    c = xpress.Cache(k=pool, v=pool.clone(), table=torch.randperm(2 * N, generator=g).int().view(N, 2).cuda(),
+                     length=length.cuda(), ref=torch.ones(2 * N, dtype=torch.int32, device="cuda"),
+                     dtype=dtype)
+    new = torch.randn(2, N * B, D, generator=g).to(dtype)
+    d, out = new.cuda(), torch.full((2, N * B, D), 7.0, dtype=dtype, device="cuda")
+    xpress.cache_append(c, 0, d[0], d[1], B=B)
+    xpress.cache_read(c, 0, out[0], out[1], B=B)
+    want = mx4.values(*mx4.quantise(new, dtype)).view(2, N, B, D)
+    held = torch.arange(B)[None] >= B - length[:, None]
+    assert torch.equal(out.cpu().view(2, N, B, D).double(), want * held[None, :, :, None])
+
+
+@pytest.mark.parametrize("bits", [4, 16])
+def test_a_row_read_twice_and_reads_at_once(bits):
+    """The same row several times in a list, two reads on streams of their own beside an append to other
+    rows, and replays of a captured read over rows that grow."""
+    Hkv, page, D, lengths, B, dtype = 3, 32, 128, [300, 200, 64], 50, torch.float16
+    width = Hkv * D
+    x = Held(Hkv, page, D, lengths, dtype, seed=8)
+    g = torch.Generator().manual_seed(2)
+    if bits == 16:
+        shape = (2, x.n_pages, Hkv, page, D)
+        k, v = (torch.randn(shape, generator=g).to(dtype).cuda() for _ in range(2))
+        x.c = xpress.Cache(k=k, v=v, table=x.c.table, length=x.c.length, ref=x.c.ref)
+    first = torch.randn(lengths[0], 2 * width, generator=g).to(dtype).cuda()
+    xpress.cache_append(x.c, 1, first[:, :width], first[:, width:], seq=i32([0]), B=lengths[0])
+    whole = torch.empty_like(first)
+    xpress.cache_read(x.c, 1, whole[:, :width], whole[:, width:], seq=i32([0]), B=lengths[0])
+    torch.cuda.synchronize()
+    starts = [250, 13, 250]
+    outs = [torch.zeros(3 * B, 2 * width, dtype=dtype, device="cuda") for _ in range(2)]
+    seq, at = i32([0] * 3), i32(starts)
+    streams = [torch.cuda.Stream() for _ in range(3)]
+    new = torch.randn(2 * B, 2 * width, generator=g).to(dtype).cuda()
+    torch.cuda.synchronize()
+    for s, o in zip(streams, outs):
+        with torch.cuda.stream(s):
+            xpress.cache_read(x.c, 1, o[:, :width], o[:, width:], seq=seq, first=at, B=B)
+    with torch.cuda.stream(streams[2]):
+        xpress.cache_append(x.c, 1, new[:, :width], new[:, width:], seq=i32([1, 2]), B=B)
+    torch.cuda.synchronize()
+    for o in outs:
+        for i, f in enumerate(starts):
+            assert torch.equal(o.view(3, B, -1)[i], whole[f:f + B])
+    graph, o = torch.cuda.CUDAGraph(), outs[0]
+    last = i32([1])
+    with torch.cuda.graph(graph):
+        xpress.cache_read(x.c, 1, o[:B, :width], o[:B, width:], seq=last, B=B)
+    for n in (200, 180, 49, 0, 200):
+        x.c.length[1] = n
+        o.fill_(3)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        xpress.cache_read(x.c, 1, outs[1][:B, :width], outs[1][:B, width:], seq=last, B=B)
+        assert torch.equal(o[:B].view(torch.int16), outs[1][:B].view(torch.int16)) and bool((o[B:] == 3).all())
+        assert bool((o[:max(0, B - n)] == 0).all())
