@@ -10,7 +10,8 @@
 //
 // To find the best K of n values without sorting them: of the threads' own best ones the K-th, by a
 // search over its bits; values that are not below it are a few more than K, and their places are
-// counted.
+// counted. Where they are very many, as in rows that are masked but for a few ids, values above it come
+// first, then the first by index of those that equal it.
 #include "serve.hpp"
 #include "logit_rows.hpp"
 #include "xpress_common.hpp"
@@ -129,11 +130,11 @@ template <> __device__ __forceinline__ _Float16 narrow(float x) { return (_Float
 template <> __device__ __forceinline__ float narrow(float x) { return x; }
 
 // One chunk of one row, 16 KiB of 16-bit logits; each wave leaves sums of its own. Bound by HBM, close to
-// the vector unit's 280 operations a wave (with 430, of which quieted maxima, a join of the waves and
-// bounds checks of every piece were the rest, 2048 rows of 151,936 ids took 158 us in all instead of 144). Six
-// workgroups a CU: with eight the careful path spills (222 us). Workgroups that go on from chunk to chunk
-// and ask for the next one's logits ahead were slower (224 us and more).
-template <class T> __global__ __launch_bounds__(kThreads, 6) void chunks_kernel(Args A) {
+// the vector unit's 290 operations a wave: 2048 rows of 151,936 ids 118 us, at the rate of a copy 130 (which
+// writes too). With quieted maxima, a join of the waves and bounds checks of every piece 430 operations,
+// and 14 us more. Workgroups that go on from chunk to chunk and ask for the next one's logits ahead
+// were slower by half.
+template <class T> __global__ __launch_bounds__(kThreads, 8) void chunks_kernel(Args A) {
   constexpr int E = Row<T>::E, K = kChunk / kThreads / E;  // K loads; as many lanes hold a group
   static_assert(K * E == kGroup, "a thread's ids are as many as a group's");
   const int c = blockIdx.x % A.chunks, t = threadIdx.x;
@@ -164,7 +165,7 @@ template <class T> __global__ __launch_bounds__(kThreads, 6) void chunks_kernel(
   int above;
   float m, sum, zsum;
   // What the chunk leaves, of x as it is: numbers.
-  auto maxima = [&] {
+  auto maxima = [&]() __attribute__((always_inline)) {
     above = 0;
     m = -INFINITY;
     float best = -INFINITY;
@@ -185,7 +186,7 @@ template <class T> __global__ __launch_bounds__(kThreads, 6) void chunks_kernel(
         narrow<T>(best);
     m = wave_max(m);
   };
-  auto sums = [&](auto exponent) {
+  auto sums = [&](auto exponent) __attribute__((always_inline)) {
     sum = zsum = 0.f;
 #pragma unroll
     for (int k = 0; k < K; ++k)
@@ -193,17 +194,20 @@ template <class T> __global__ __launch_bounds__(kThreads, 6) void chunks_kernel(
       for (int e = 0; e < E; ++e) {
         const float z = exponent(x[k][e]), w = __builtin_amdgcn_exp2f(z);
         sum += w;
-        zsum = fmaf(w, z, zsum);
+        zsum = fmaf(w, fmaxf(z, -1e30f), zsum);  // (-inf: no weight, and no NaN of it)
       }
   };
   maxima();
-  {
+  bool care = !scale.plain(m) || scale.t == 0.f;
+  if (!care) {
     const float unit = m * scale.c;
     sums([&](float v) { return fmaf(v, scale.c, -unit); });
+    // (a NaN is in the sum. Asked of both, or the second is formed behind the branch and its terms kept
+    // until then: twice the registers.)
+    care = __ballot(!(sum >= zsum)) != 0;
   }
-  // NaN, and infinities (products of 0 and -inf), make a sum NaN: then, and where the scale asks for it,
-  // once more with care.
-  if (__ballot(!(zsum <= 0.f)) || !scale.plain(m) || scale.t == 0.f) {
+  // Once more with care for NaN, an infinite maximum, and where the scale asks for it.
+  if (care) {
 #pragma unroll
     for (int k = 0; k < K; ++k)
 #pragma unroll
@@ -217,7 +221,7 @@ template <class T> __global__ __launch_bounds__(kThreads, 6) void chunks_kernel(
         for (int e = 0; e < E; ++e) sum += x[k][e] == m ? 1.f : 0.f;
     } else if (m > -INFINITY && scale.t != 0.f) {
       const float unit = m * scale.c;
-      // (the maximum with -1e30: no weight, and no NaN of it)
+      // (-1e30 for what an infinite temperature makes of -inf)
       if (scale.plain(m))
         sums([&](float v) { return fmaxf(fmaf(v, scale.c, -unit), -1e30f); });
       else
@@ -244,6 +248,39 @@ __device__ __forceinline__ void in_order(const uint64_t* list, int n, int count,
     place += __builtin_amdgcn_update_dpp(0, place, 0x4E, 0xf, 0xf, false);  // quad_perm 2 3 0 1
     if (part == 0 && place < count) take(place, key);
   }
+}
+
+// The best `count` of the n keys in `list` (all different, n >= count): take(place, key). Of many, the least
+// that counts is searched for first, by its bits: 256 keys are as quick without.
+template <class F>
+__device__ __forceinline__ void best_of(const uint64_t* list, int n, int count, F&& take) {
+  __shared__ uint64_t s_keep[kMostTop];
+  __shared__ int s_count[2][kWaves], s_kept;
+  if (n <= kThreads) return in_order(list, n, count, take);
+  const int t = threadIdx.x;
+  if (t == 0) s_kept = 0;
+  uint64_t mine[kList / kThreads], least = 0;
+#pragma unroll
+  for (int i = 0; i < kList / kThreads; ++i) mine[i] = t + i * kThreads < n ? list[t + i * kThreads] : 0;
+  for (int bit = 63; bit >= 0; --bit) {
+    const uint64_t next = least | 1ull << bit;
+    int above = 0;
+#pragma unroll
+    for (int i = 0; i < kList / kThreads; ++i) above += __popcll(__ballot(mine[i] >= next));
+    // (two sets: the last but one was read before the last meeting)
+    if (t % 64 == 0) s_count[bit & 1][t / 64] = above;
+    __syncthreads();
+    above = 0;
+#pragma unroll
+    for (int w = 0; w < kWaves; ++w) above += s_count[bit & 1][w];
+    if (above >= count) least = next;
+    if (above == count) break;
+  }
+#pragma unroll
+  for (int i = 0; i < kList / kThreads; ++i)
+    if (mine[i] >= least && mine[i]) s_keep[atomicAdd(&s_kept, 1)] = mine[i];
+  __syncthreads();
+  in_order(s_keep, count, count, take);
 }
 
 // A row's end: dependent loads and meetings of about 9 us, so few registers, for many rows at a time. The
@@ -325,6 +362,7 @@ template <class T> __global__ __launch_bounds__(kThreads, kFinish) void finish_k
   __shared__ uint64_t s_floor;
   __shared__ int s_n, s_ids, s_first;
   __shared__ uint32_t s_least;
+  __shared__ int s_part[kWaves];
   if (count > 0) {
     // all of this thread's maxima: f(order, index) of each
     auto piece = [&](const uint4& u, int i, auto&& f) {
@@ -374,13 +412,51 @@ template <class T> __global__ __launch_bounds__(kThreads, kFinish) void finish_k
       if (at < kList) s_list[at] = key_of(o, g);
     });
     __syncthreads();
-    if (s_n <= kList) {
-      in_order(s_list, s_n, of_groups, [&](int place, uint64_t key) {
+    int n = s_n;
+    if (n > kList) {
+      // once more without those that equal it, of which the first are then looked for in their order
+      __syncthreads();
+      if (t == 0) s_n = 0;
+      __syncthreads();
+      each([&](uint32_t o, int g) {
+        if (o <= least) return;
+        const int at = atomicAdd(&s_n, 1);
+        if (at < kList) s_list[at] = key_of(o, g);
+      });
+      __syncthreads();
+      n = s_n;
+      for (int i0 = 0; n < of_groups && i0 < pieces; i0 += kThreads) {
+        uint32_t equal = 0;
+        if (i0 + t < pieces)
+          piece(groups[i0 + t], i0 + t, [&](uint32_t o, int g) { equal |= (o == least) << g % E; });
+        int before = __popc(equal);
+#pragma unroll
+        for (int d = 1; d < 64; d *= 2) {
+          const int y = __shfl_up(before, d);
+          if (lane >= d) before += y;
+        }
+        if (lane == 63) s_part[t / 64] = before;
+        __syncthreads();
+        before -= __popc(equal);
+        int all = 0;
+#pragma unroll
+        for (int w = 0; w < kWaves; ++w) {
+          if (w < t / 64) before += s_part[w];
+          all += s_part[w];
+        }
+        for (; equal && n + before < of_groups; equal &= equal - 1, ++before)
+          s_list[n + before] = key_of(least, (i0 + t) * E + __ffs(equal) - 1);
+        n = min(n + all, of_groups);
+        __syncthreads();
+      }
+    }
+    if (n <= kList) {
+      best_of(s_list, n, of_groups, [&](int place, uint64_t key) {
         s_group[place] = index_of(key);
         if (place == of_groups - 1) s_floor = key;
       });
     } else {
-      // more than the list holds, as in a row of equal logits: one after the other
+      // more than the list holds: one after the other
       uint64_t last = ~0ull;
       for (int k = 0; k < of_groups; ++k) {
         uint64_t best = 0;
@@ -417,7 +493,7 @@ template <class T> __global__ __launch_bounds__(kThreads, kFinish) void finish_k
           s_list[atomicAdd(&s_ids, 1)] = key_of(order_of(x[j]), id[j]);
     }
     __syncthreads();
-    in_order(s_list, s_ids, count, [&](int place, uint64_t key) {
+    best_of(s_list, s_ids, count, [&](int place, uint64_t key) {
       if (place == 0) s_first = index_of(key);
       if (place >= A.top) return;
       const float x = value_of((uint32_t)(key >> 32));

@@ -325,3 +325,31 @@ def test_two_calls_at_once_and_rows_past_32_bits():
     torch.cuda.synchronize()
     for o in outs:
         check(x, token, None, top, o, "at once")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float32], ids=["bf16", "f32"])
+def test_very_many_equal_ids_behind_others(dtype):
+    """More groups whose best are equal than the selection's list holds, beginning far into the row, with
+    fewer better ones than there are places, as many, and more."""
+    V = 400000
+    g = torch.Generator().manual_seed(15)
+    x = (-5 - torch.rand(4, V, generator=g)).to(dtype)
+    x[:, 200000:] = 1.0
+    for r, better in enumerate((0, 10, 64, 200)):
+        at = torch.randperm(V, generator=g)[:better]
+        x[r, at] = (2 + torch.rand(better, generator=g)).to(dtype)
+    token = torch.tensor([[200000], [5], [V - 1], [399000]])
+    for top in (1, 64):
+        check(x, token, None, top, run(x, token, None, top, 5, 1), f"equal behind others {dtype} {top}")
+
+
+def test_best_ids_that_share_groups():
+    """All ids of a few groups before all others: more keys at the end than are counted without a search."""
+    V, top = 151936, 64
+    x = logits(2, V, torch.float32, 16) - 30
+    for group in range(60):
+        x[0, 32 * 70 * group:32 * 70 * group + 32] += 40
+    x[1, 1000:5000] += 40
+    token = torch.tensor([[0], [1234]])
+    for t in (top, 20, 1):
+        check(x, token, None, t, run(x, token, None, t), f"shared groups {t}")
