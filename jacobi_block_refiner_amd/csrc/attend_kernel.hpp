@@ -348,7 +348,8 @@ template <int D, int KT, int NW> struct Source {
 
 // The same for tiles of 4 bits. A thread loads 8 bytes of codes and their scales (U times), a tile
 // ahead of the one that it turns into 16-bit values: 16 channels of a key of K, two channels of four
-// keys of two groups of V. With LAG the values are those of the tile before the keys'.
+// keys of two groups of V. With LAG the values are those of the tile before the keys'. The conversions
+// lie beside the products: 2560 rows, 8192 keys, 8 heads of 128 take wide items 110 us (104 from 16 bits).
 template <bool F16, int D, int KT, int NW, bool LAG> struct Source4 {
   using C = Core<F16, D, KT, true>;
   static constexpr int U = KT / 16 * D / (NW * 64), SPAN = D / 16;  // units of 8 bytes; of a key

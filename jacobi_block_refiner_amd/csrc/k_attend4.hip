@@ -535,12 +535,16 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
   if (F.parts && !F.by_pair && lane == 0 && row0 == 0) F.cut[part] = cut;
 }
 
+// 64 requests decoding up to 32,768 tokens each (8 heads of 128, 5 queries each, 1.14 GB): 225 us, 5.1
+// TB/s (a copy reaches 4.8, reads alone 5.9). One of 1000 tokens: 8.8 us, of them 2.3 for the lengths and
+// 1.5 for the first tile of keys, and 4.1 of join_kernel.
 template <bool F16, int D, int RT>
 __global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
   few_part<F16, D, RT>(F, blockIdx.x);
 }
 
-// The shared part's narrow items beside them.
+// The shared part's narrow items beside them: 32 requests decoding behind 4096 tokens (32 heads of 128,
+// up to 1024 own) 18.5 us and 5.3 of the join, 23 in all; as two launches 31.
 template <bool F16, int D, int RT>
 __global__ __launch_bounds__(256, narrow_per_cu(D)) void beside_kernel(Few F) {
   const int items = F.a.Hkv * F.a.tiles_sh * F.a.s_sh;

@@ -285,7 +285,7 @@ __device__ __forceinline__ void best_of(const uint64_t* list, int n, int count, 
 
 // A row's end: dependent loads and meetings of about 9 us, so few registers, for many rows at a time. The
 // sums, in 64 bits, are one wave's work beside the search of another (in every wave, before the search:
-// 9.7 us instead of 9.3 for one row of 151,936 ids with 20 alternatives, 20 instead of 17.6 for 2048 rows
+// 9.7 us instead of 9.2 for one row of 151,936 ids with 20 alternatives, 20 instead of 17.2 for 2048 rows
 // with 5). The maxima held in registers between their two uses spill: 24 us for the 2048 rows.
 template <class T> __global__ __launch_bounds__(kThreads, kFinish) void finish_kernel(Args A) {
   constexpr int E = Row<T>::E;
