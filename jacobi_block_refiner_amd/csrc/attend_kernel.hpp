@@ -715,20 +715,20 @@ __device__ __forceinline__ void attend_item(const Args& A, int id) {
     while (t < nt) {
       enter();
       if constexpr (!MX4) {
-      bool wild = false;
-      for (int x = threadIdx.x; x < KT * C::CPR; x += NW * 64) {
-        uint4& v = s_tile[(at + C::SIDE) / 16 + x];
-        uint4 u = v;
-        if (tame<F16>(u.x) | tame<F16>(u.y) | tame<F16>(u.z) | tame<F16>(u.w)) {
-          v = u;
-          wild = true;
+        bool wild = false;
+        for (int x = threadIdx.x; x < KT * C::CPR; x += NW * 64) {
+          uint4& v = s_tile[(at + C::SIDE) / 16 + x];
+          uint4 u = v;
+          if (tame<F16>(u.x) | tame<F16>(u.y) | tame<F16>(u.z) | tame<F16>(u.w)) {
+            v = u;
+            wild = true;
+          }
         }
-      }
-      if (wild) {
-        atomicMin(&s_wild[0], t);
-        atomicMax(&s_wild[1], t);
-      }
-      meet_reads();
+        if (wild) {
+          atomicMin(&s_wild[0], t);
+          atomicMax(&s_wild[1], t);
+        }
+        meet_reads();
       }
       if (!idle) {
         w.scores(at);
@@ -893,7 +893,7 @@ hipError_t launch_t(Args A, bool wide, hipStream_t s) {
   const int64_t own = (int64_t)A.Hkv * A.s_own * A.tiles_own * A.N;
   int64_t shared = (int64_t)A.Hkv * A.tiles_sh * A.s_sh;
   A.slots_sh = A.s_sh;
-  A.step_own = narrow_step(D);
+  A.step_own = narrow_step(D, MX4);
   A.direct = A.s_own == 1 && (wide || A.s_sh == 0);
   if constexpr (D == 128) if (wide) {
     hipLaunchKernelGGL((attend_kernel<F16, D, kWide, kWideStep, MX4>), dim3((unsigned)shared),
@@ -906,10 +906,10 @@ hipError_t launch_t(Args A, bool wide, hipStream_t s) {
   if constexpr (D == 256) slim = shared == 0 && A.B * A.G <= kSlim * 32 && own > kCUs;
   if (slim) {
     if constexpr (D == 256)
-      hipLaunchKernelGGL((attend_kernel<F16, D, kSlim, narrow_step(D), MX4>), dim3((unsigned)own),
+      hipLaunchKernelGGL((attend_kernel<F16, D, kSlim, kSlimStep, MX4>), dim3((unsigned)own),
                          dim3(kSlim * 64), 0, s, A);
   } else {
-    hipLaunchKernelGGL((attend_kernel<F16, D, kNarrow, narrow_step(D), MX4>),
+    hipLaunchKernelGGL((attend_kernel<F16, D, kNarrow, narrow_step(D, MX4), MX4>),
                        dim3((unsigned)(shared + own)), dim3(kNarrow * 64), 0, s, A);
   }
   const hipError_t e = hipGetLastError();

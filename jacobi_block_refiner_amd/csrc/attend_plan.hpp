@@ -20,7 +20,12 @@ struct AttendPlan {
 };
 
 constexpr int kTile = 64;  // the shared part is a multiple of it
-constexpr int narrow_step(int D) { return D == 64 ? 64 : 32; }  // keys of a tile
+// Keys of a tile. From 4 bits two stages of 64 keys fit where 16 bits take four of 32, and a tile's codes
+// are asked for a tile ahead: us a call with 64 and 32, D 128: 128 requests decoding behind 16,384 tokens 65
+// and 73, 32 behind 32,768 41 and 45; D 256: 32 blocks of 16 behind 8192 266 and 328, 64 of up to 2000
+// tokens 217 and 248. (A slim item of 64 has no registers for it.)
+constexpr int kSlimStep = 32;
+constexpr int narrow_step(int D, bool mx4) { return D == 64 || mx4 ? 64 : 32; }
 constexpr int kWideStep = 64;
 constexpr int kCUs = 256;
 // Query rows a head from which the shared part goes to wide items, D 128 alone. Narrow against wide,
@@ -64,7 +69,7 @@ inline AttendPlan plan_of(const xpress_cache& c, int N, int B, int Hq, int share
   // (a request that does not see the whole shared part has less than shared + B keys, all its own)
   p.s_own = (int)std::max(s, ceil_div(std::max(own, std::min<int64_t>(cap, (int64_t)shared + B)), most));
   if (shared > 0) {
-    const int KT = p.wide ? kWideStep : narrow_step(c.D);
+    const int KT = p.wide ? kWideStep : narrow_step(c.D, c.dtype > 15u);
     p.tiles_sh = (int)ceil_div(rows, (p.wide ? kWide : kNarrow) * 32);
     const int64_t tiles = (int64_t)c.Hkv * p.tiles_sh;
     if (p.wide) {

@@ -549,7 +549,7 @@ template <bool F16, int D, int RT>
 __global__ __launch_bounds__(256, narrow_per_cu(D)) void beside_kernel(Few F) {
   const int items = F.a.Hkv * F.a.tiles_sh * F.a.s_sh;
   if ((int)blockIdx.x < items)
-    attend_item<F16, D, kNarrow, narrow_step(D), true>(F.a, blockIdx.x);
+    attend_item<F16, D, kNarrow, narrow_step(D, true), true>(F.a, blockIdx.x);
   else
     few_part<F16, D, RT>(F, blockIdx.x - items);
 }
@@ -625,7 +625,7 @@ template <bool F16, int D> hipError_t launch_few(Few F, bool wide, bool beside, 
   Args& A = F.a;
   const int64_t shared = (int64_t)A.Hkv * A.tiles_sh * A.s_sh;
   A.slots_sh = A.s_sh;
-  A.step_own = narrow_step(D);
+  A.step_own = narrow_step(D, true);
   A.direct = false;
   const int R = A.B * A.G;
   const int64_t own = ceil_div(F.parts ? F.parts : (int64_t)A.N * A.Hkv, 4 / F.waves);
@@ -645,7 +645,7 @@ template <bool F16, int D> hipError_t launch_few(Few F, bool wide, bool beside, 
           hipLaunchKernelGGL((attend_kernel<F16, D, kWide, kWideStep, true>), dim3((unsigned)shared),
                              dim3(kWide * 64), 0, s, A);
       if (!wide)
-        hipLaunchKernelGGL((attend_kernel<F16, D, kNarrow, narrow_step(D), true>),
+        hipLaunchKernelGGL((attend_kernel<F16, D, kNarrow, narrow_step(D, true), true>),
                            dim3((unsigned)shared), dim3(kNarrow * 64), 0, s, A);
       const hipError_t e = hipGetLastError();
       if (e != hipSuccess) return e;
