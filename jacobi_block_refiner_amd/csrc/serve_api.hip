@@ -1,6 +1,6 @@
 // C ABI of the target's side of a draft step: argument checks of the paged cache, the block
-// attention, the draft verification and the log probabilities of tokens. Every entry point validates on the host, then only
-// enqueues kernels on the caller's stream.
+// attention, the draft verification and the log probabilities of tokens. Every entry point validates
+// on the host, then only enqueues kernels on the caller's stream.
 #include "api_common.hpp"
 #include "serve.hpp"
 
