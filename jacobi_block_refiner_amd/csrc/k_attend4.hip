@@ -679,10 +679,10 @@ template <bool F16, int D> hipError_t launch_few(Few F, bool wide, bool beside, 
 // Whether few_kernel takes the own keys of N requests with R query rows a head. Up to 32: always, and up
 // to 64 over long contexts (by what the tables hold), where the items' meetings cost more than reading
 // codes in several waves: 16 tokens of 4 heads a head, us a call, few_kernel and items: D 128: 64
-// requests of up to 4000 own keys 93 and 130, of up to 300 37 and 34; 8 of up to 4000 31 and 34, of up
-// to 1000 23 and 20; one 21 and 18. D 64: 64 of up to 4000 56 and 67, of up to 1000 34 and 31. D 256:
-// 64 of up to 300 58 and 61, 8 of up to 1000 34 and 29. (65 to 128 rows, 64 requests of up to 4000: 154
-// and 146.)
+// requests of up to 4000 own keys 92 and 121, of up to 300 36 and 35; 8 of up to 4000 31 and 34, of up
+// to 1000 23 and 20; one of up to 4000 21 and 17. D 64: 64 of up to 4000 57 and 67, of up to 1000 34 and
+// 31. D 256: 64 of up to 300 57 and 63, 8 of up to 4000 44 and 61, of up to 1000 33 and 29. (65 to 128
+// rows, 64 requests of up to 4000: 154, and 146 by items of tiles of 32 keys still.)
 bool few_rows(const xpress_cache& c, int N, int R, int shared) {
   const int64_t keys = (int64_t)N * c.Hkv * ((int64_t)c.table_ld * c.page - shared);
   return R <= 32 || (R <= kFewRows4 && keys * c.D * c.D >= (int64_t)1 << 32);
