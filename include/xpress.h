@@ -429,7 +429,10 @@ xpress_status xpress_cache_compact(const xpress_cache* c, int32_t* live, void* w
  * 0 < scale <= 1e6; 0 <= shared <= table_ld*page. Products q.k below -1e30 - 90 / scale have no
  * weight: a row that sees nothing else is as one that sees no token.
  * Values in masked places (beyond a row's end, in later tokens of the block) do not reach the
- * result, whatever they are. */
+ * result, whatever they are.
+ * Weights are up to 2^8 each before they are divided by their sum. Sums of fp16 values, and of all that 4
+ * bits hold, stay in the range of 32 bits (of bf16 in 4 bits they are held to 2^-112, and lse to 2^-18);
+ * of bf16 in 16 bits they do while the values are below 2^90, whatever the scores. */
 xpress_status xpress_attention_workspace_size(const xpress_cache* c, int32_t n_max, int32_t B,
                                               int32_t Hq, size_t* bytes);
 xpress_status xpress_block_attention(const xpress_cache* c, int32_t layer, const void* q,

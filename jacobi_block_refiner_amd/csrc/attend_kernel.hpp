@@ -123,7 +123,10 @@ template <bool F16, int D, int KT, bool MX4 = false> struct Core {
   // of the maximum lost bits and one below 2^-25 vanished, and 60,000 of them 17 nats under one key
   // were off by 44%. With it steps are coarser from 2^-21 on and nothing is left from 2^-32 on: half a
   // step of 2^21 such keys is 2^-11 of the row, the result's own rounding.
-  static constexpr float kLift = F16 ? 7.f : 0.f;
+  // bf16 has the range of the 32-bit sums, and a cache of 4 bits makes 1.5 * 2^127 of an infinity: there
+  // the weights of all the 2^28 keys that a table can hold, up to 2^8 each, add up to 1/2, so that no sum
+  // leaves the range. The steps of a sum's subnormals are 2^-149 of such weights, 2^-112 of a result.
+  static constexpr float kLift = F16 ? 7.f : MX4 ? -37.f : 0.f;
 
   char* lds;
   int lane, h, col;

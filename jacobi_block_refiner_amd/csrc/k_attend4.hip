@@ -75,7 +75,7 @@ template <int N> __device__ __forceinline__ void load_words(const uint8_t* p, ui
 // instructions, 1000 cycles; at 5 TB/s a SIMD has 2000.
 template <bool F16, int D, int RT> struct FewCore {
   static constexpr int NG = D / 32;
-  static constexpr float kLift = F16 ? 7.f : 0.f;  // as in Core
+  static constexpr float kLift = F16 ? 7.f : -37.f;  // as in Core
   static constexpr float kHuge = 0x1p20f;
 
   int lane, i, q;
