@@ -111,6 +111,22 @@ inline int64_t most_row_slots(const xpress_cache& c, int n, int B, int Hq) {
   return std::max<int64_t>(own, n * ids) + std::max<int64_t>(sh, n * ids);
 }
 
+// A (request, head) pair whose keys lie in several parts of the sequence of all: it begins in this one.
+struct Cut {
+  int pair, slots;  // (0: it is whole, or none begins here)
+  int part, slot;   // where it begins, its slot there; then slots 2 (part + 1), 2 (part + 2), ..
+};
+// A record as the join uses it: inside the pairs and the 2 * parts slots, whatever it holds. (Where
+// another stream changes lengths during a call, a pair may begin in no part, and its record is an old one.)
+XP_HD Cut cut_inside(Cut c, int pairs, int parts) {
+  auto within = [](int x, int lo, int hi) { return x < lo ? lo : (x < hi ? x : hi); };
+  c.pair = within(c.pair, 0, pairs - 1);
+  c.part = within(c.part, 0, parts - 1);
+  c.slot = 2 * c.part + (c.slot & 1);
+  c.slots = within(c.slots, 0, parts - c.part);
+  return c;
+}
+
 // A wave holds the page ids of 64 tiles, from `from` on, and finds each tile's addresses while it works
 // on the one before. At tile t of those up to t1: whether the next tile's ids have to be read first, and
 // up to where it can then go on (past t, always).

@@ -24,12 +24,6 @@ constexpr int kFewRequests = 4096;  // more are not cut: a part a pair
 // Workgroups of few_kernel on a CU, by its registers.
 constexpr int few_per_cu(int D, int RT) { return D == 64 ? 3 : 2; }
 
-// A pair whose keys lie in several parts: it begins in this one.
-struct Cut {
-  int pair, slots;  // (0: it is whole, or none begins here)
-  int part, slot;   // where it begins, its slot there; then slots 2 (part + 1), 2 (part + 2), ..
-};
-
 struct Few {
   Args a;
   int parts;  // of the sequence, where it is cut; else 0
@@ -563,7 +557,10 @@ __global__ __launch_bounds__(J * D > 1024 ? 1024 : 256) void join_kernel(Few F) 
   constexpr int LPR = D / 4, RPB = J * D > 1024 ? 1 : 256 / (LPR * J);
   const Args& A = F.a;
   Cut cut{(int)blockIdx.x, 0, 0, 0};
-  if (F.parts) cut = F.cut[blockIdx.x];
+  if (F.parts) {
+    cut = cut_inside(F.cut[blockIdx.x], A.N * A.Hkv, F.parts);
+    if (F.by_pair) cut.pair = blockIdx.x;
+  }
   if (cut.slots == 0 && A.slots_sh == 0) return;
   const int R = A.B * A.G, d = threadIdx.x % LPR * 4;
   const int group = threadIdx.x / LPR % J, r = blockIdx.y * RPB + threadIdx.x / (LPR * J);
