@@ -485,7 +485,8 @@ xpress_status xpress_verify_draft(const void* logits, uint32_t logits_dtype, int
  * temperature: [N] fp32, nullable (1). At 0, a negative value or NaN all of p is on the first of the
  * alternatives: its log probability is 0, the others' -inf, the entropy 0.
  * A logit of -inf or NaN has no weight and is ordered last (by id); at +inf the ids that hold it share
- * all. In a row without any weight the log probabilities are -inf and the entropy is 0.
+ * all. In a row without any weight the log probabilities are -inf and the entropy is 0. No log
+ * probability is above 0, and no entropy below it.
  * token: [N, B] int64. logprob, entropy: [N*B] fp32, rank: [N*B] int32, each nullable. top_ids: [N*B,
  * top] int64, top_logprobs: [N*B, top] fp32 (top 0: not used). logits: XPRESS_BF16, _F16 or _F32 with
  * row stride ld >= V in elements, any alignment of the rows to their own elements. 0 <= top <= 64;

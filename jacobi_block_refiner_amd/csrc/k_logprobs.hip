@@ -349,11 +349,12 @@ template <class T> __global__ __launch_bounds__(kThreads, kFinish) void finish_k
     s_sums[2] = log_sum - zsum / sum * 0.69314718055994531;
     s_above = above;
   };
-  // log p of a logit (greedy: of one that is not the first best)
+  // log p of a logit (greedy: of one that is not the first best). Where one id has nearly all, the rounding
+  // of its 32-bit weight is all that is left of the sum's logarithm, of either sign: no p is above 1.
   auto logp = [&](float x) {
     const float m = (float)s_sums[0];
     if (greedy || m == -INFINITY || x == -INFINITY || (m == INFINITY && x != m)) return -INFINITY;
-    return (float)((x == m ? 0.0 : ((double)x - (double)m) / scale.t) - s_sums[1]);
+    return fminf((float)((x == m ? 0.0 : ((double)x - (double)m) / scale.t) - s_sums[1]), 0.f);
   };
 
   __shared__ uint64_t s_list[kList];
@@ -512,7 +513,7 @@ template <class T> __global__ __launch_bounds__(kThreads, kFinish) void finish_k
   if (t != 0) return;
   if (A.entropy) {
     const bool none = greedy || s_sums[0] == -INFINITY;
-    A.entropy[r] = none ? 0.f : (float)s_sums[2];
+    A.entropy[r] = none ? 0.f : fmaxf((float)s_sums[2], 0.f);  // (as a log p's end at 0)
   }
   const bool inside = token < A.V;
   if (A.token && A.rank) A.rank[r] = inside ? s_above : -1;
