@@ -520,7 +520,7 @@ class Cache:
         if bits == 4:
             shape, pool = (n_layers, n_pages, Hkv, page // 16, 17 * D // 2), torch.uint8
         return cls(k=torch.empty(shape, dtype=pool, device=device),
-                   v=torch.empty(shape, dtype=pool, device=device), dtype=dtype,
+                   v=torch.empty(shape, dtype=pool, device=device), dtype=dtype if bits == 4 else None,
                    table=torch.full((rows, table_ld), -1, dtype=torch.int32, device=device),
                    length=torch.zeros(rows, dtype=torch.int32, device=device),
                    ref=torch.zeros(n_pages, dtype=torch.int32, device=device))
