@@ -81,11 +81,12 @@ class Turn:
 
 class Decoder:
     """The samples of one prompt: their cache (of 16 or 4 bits), the refiner's inputs and the buffers of
-    a turn. top: with each turn's tokens come their log probabilities and as many alternatives."""
+    a turn. top: with each turn's tokens come their log probabilities and as many alternatives, under
+    the temperature ``report`` (None: the one that they are drawn at; at 0 each token has all)."""
 
     def __init__(self, target: Target, refiner: xpress.Weights, samples: int, *, page: int = 16,
                  most: int = 512, temperature: float = 1.0, seed: int = 0, bits: int = 16,
-                 top: int | None = None):
+                 top: int | None = None, report: float | None = None):
         d = refiner.dims
         if (d["H"], d["V"]) != (target.H, target.V):
             raise ValueError("the refiner and the target differ in hidden size or vocabulary")
@@ -104,6 +105,7 @@ class Decoder:
         self.blk, self.out = empty(N, B, dtype=torch.int64), empty(N, B, dtype=torch.int64)
         self.accepted, self.drop, self.lacking, self.live = empty(N), empty(N), empty(1), empty(1)
         self.temperature = torch.full((N,), temperature, device=dev)
+        self.report = self.temperature if report is None else torch.full((N,), report, device=dev)
         self.rng = torch.Generator(device=dev).manual_seed(seed)
         self.step_ws = xpress.alloc_workspace(N, B, d["r"], V, 0, B, dev)
         self.cache_ws = xpress.cache_workspace(self.cache, N)
@@ -164,7 +166,7 @@ class Decoder:
             if self.top:
                 said["top_ids"] = torch.empty(N * B, self.top, dtype=torch.int64, device=h.device)
                 said["top_logprobs"] = torch.empty(N * B, self.top, device=h.device)
-            xpress.token_logprobs(logits, self.out, temperature=self.temperature,
+            xpress.token_logprobs(logits, self.out, temperature=self.report,
                                   ws=self.logprobs_ws, **said)
             said = {name: t.view(N, B, *t.shape[1:]) for name, t in said.items()}
         # tokens of the longest row at most: the host waits for the card only where they might not fit
@@ -202,14 +204,14 @@ def main(argv=None) -> None:
     p.add_argument("--prompt", type=int, default=200)
     p.add_argument("--greedy", action="store_true")
     p.add_argument("--bits", type=int, default=16, choices=(4, 16), help="of a value in the cache")
-    p.add_argument("--logprobs", action="store_true", help="of the tokens, summed up a sample")
+    p.add_argument("--logprobs", action="store_true", help="of the tokens at temperature 1, summed up a sample")
     a = p.parse_args(argv)
     inp = synth.make_inputs(1).rounded_bf16()
     most = a.prompt + a.turns * inp.wl.B
     target = Target(inp.wl.V, inp.wl.H, most=most + inp.wl.B)
     dec = Decoder(target, upload.weights(inp), a.samples, most=most,
                   temperature=0.0 if a.greedy else 1.0, bits=a.bits,
-                  top=0 if a.logprobs else None)
+                  top=0 if a.logprobs else None, report=1.0)
     ids = torch.randint(inp.wl.V, (a.prompt,), generator=torch.Generator().manual_seed(1))
     dec.prompt(ids.cuda())
     text, logprob = [[] for _ in range(a.samples)], torch.zeros(a.samples, device="cuda")
