@@ -111,6 +111,41 @@ inline int64_t most_row_slots(const xpress_cache& c, int n, int B, int Hq) {
   return std::max<int64_t>(own, n * ids) + std::max<int64_t>(sh, n * ids);
 }
 
+// The register path over 4 bits (few_kernel).
+constexpr int kFewTile = 32;   // keys of a step of a wave
+constexpr int kFewRequests = 4096;  // more are not cut: a part a pair
+constexpr int kFewRows4 = 64;  // query rows of a request and head at most
+
+// Workgroups on a CU, by the registers.
+constexpr int few_per_cu(int D) { return D == 64 ? 3 : 2; }
+// Row tiles of a wave, waves of a part, and parts of the sequence. At D 256 two row tiles would have a
+// SIMD to themselves and no registers left.
+constexpr int few_row_tiles(int D, int R) { return R <= 16 || D == 256 ? 1 : 2; }
+constexpr int few_waves(int D, int R) {
+  const int n = (R - 1) / (16 * few_row_tiles(D, R));
+  return n == 0 ? 1 : n == 1 ? 2 : 4;
+}
+constexpr int few_parts(int D, int R) { return kCUs * few_per_cu(D) * 4 / few_waves(D, R); }
+
+// Whether it takes the own keys of N requests with R query rows a head. Up to 32 rows: always, and up to 64
+// from so many keys of all heads on (by what the tables hold), where the items' meetings cost more than
+// reading codes in several waves. 16 tokens of 4 heads a head, 8 heads, tables of up to so many own
+// tokens, us a call, few_kernel and items:
+//   D 64: 64 x 4000 57 and 67, 64 x 2000 41 and 43, 8 x 16,000 37 and 41; 64 x 1000 34 and 31, 32 x 2000
+//   33 and 32, 4 x 16,000 31 and 28, 1 x 16,000 25 and 19.
+//   D 128: 64 x 4000 93 and 120, 64 x 1000 48 and 50, 8 x 4000 31 and 34, 2 x 16,000 32 and 38; 64 x 300
+//   36 and 35, 16 x 1000 28 and 27, 4 x 4000 28 and 28, 1 x 16,000 27 and 25. Not taken where it wins: 8 x
+//   2000 27 and 29; taken where it loses: 32 x 1000 37 and 36.
+//   D 256: 64 x 4000 182 and 275, 64 x 300 58 and 64, 8 x 2000 37 and 47, 1 x 16,000 38 and 43; 16 x 300 31
+//   and 27, 8 x 1000 34 and 30, 2 x 4000 31 and 30, 1 x 4000 29 and 24. Not taken where it wins: 4 x 1000 26
+//   and 29, 1 x 300 15 and 19.
+// (More rows, 80 and 128: 64 x 4000 at D 128 137 and 123, 154 and 135; at D 64 87 and 77, 95 and 83.)
+constexpr int64_t few_keys(int D) { return D == 64 ? 3 << 18 : D == 128 ? 7 << 15 : 7 << 14; }
+inline bool few_rows(const xpress_cache& c, int N, int R, int shared) {
+  const int64_t keys = (int64_t)N * c.Hkv * ((int64_t)c.table_ld * c.page - shared);
+  return R <= 32 || (R <= kFewRows4 && keys >= few_keys(c.D));
+}
+
 // A (request, head) pair whose keys lie in several parts of the sequence of all: it begins in this one.
 struct Cut {
   int pair, slots;  // (0: it is whole, or none begins here)

@@ -18,12 +18,6 @@ namespace xpress {
 
 namespace {
 
-constexpr int kFewTile = 32;   // keys of a step of a wave
-constexpr int kFewRequests = 4096;  // more are not cut: a part a pair
-
-// Workgroups of few_kernel on a CU, by its registers.
-constexpr int few_per_cu(int D, int RT) { return D == 64 ? 3 : 2; }
-
 struct Few {
   Args a;
   int parts;  // of the sequence, where it is cut; else 0
@@ -533,7 +527,7 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
 // TB/s (a copy reaches 4.8, reads alone 5.9). One of 1000 tokens: 8.8 us, of them 2.3 for the lengths and
 // 1.5 for the first tile of keys, and 4.1 of join_kernel.
 template <bool F16, int D, int RT>
-__global__ __launch_bounds__(256, few_per_cu(D, RT)) void few_kernel(Few F) {
+__global__ __launch_bounds__(256, few_per_cu(D)) void few_kernel(Few F) {
   few_part<F16, D, RT>(F, blockIdx.x);
 }
 
@@ -607,17 +601,6 @@ __global__ __launch_bounds__(J * D > 1024 ? 1024 : 256) void join_kernel(Few F) 
     A.lse[row] = all.l == 0.f ? -INFINITY : (all.m + log2f(all.l)) * 0.69314718056f;
 }
 
-// Row tiles of a wave, waves of a part, and parts of the sequence. At D 256 two row tiles would have a
-// SIMD to themselves and no registers left.
-int few_row_tiles(int D, int R) { return R <= 16 || D == 256 ? 1 : 2; }
-int few_waves(int D, int R) {
-  const int n = (R - 1) / (16 * few_row_tiles(D, R));
-  return n == 0 ? 1 : n == 1 ? 2 : 4;
-}
-int few_parts(int D, int R) {
-  return kCUs * few_per_cu(D, few_row_tiles(D, R)) * 4 / few_waves(D, R);
-}
-
 template <bool F16, int D> hipError_t launch_few(Few F, bool wide, bool beside, hipStream_t s) {
   Args& A = F.a;
   const int64_t shared = (int64_t)A.Hkv * A.tiles_sh * A.s_sh;
@@ -672,18 +655,6 @@ template <bool F16, int D> hipError_t launch_few(Few F, bool wide, bool beside, 
 }
 
 }  // namespace
-
-// Whether few_kernel takes the own keys of N requests with R query rows a head. Up to 32: always, and up
-// to 64 over long contexts (by what the tables hold), where the items' meetings cost more than reading
-// codes in several waves: 16 tokens of 4 heads a head, us a call, few_kernel and items: D 128: 64
-// requests of up to 4000 own keys 92 and 121, of up to 300 36 and 35; 8 of up to 4000 31 and 34, of up
-// to 1000 23 and 20; one of up to 4000 21 and 17. D 64: 64 of up to 4000 57 and 67, of up to 1000 34 and
-// 31. D 256: 64 of up to 300 57 and 63, 8 of up to 4000 44 and 61, of up to 1000 33 and 29. (65 to 128
-// rows, 64 requests of up to 4000: 154, and 146 by items of tiles of 32 keys still.)
-bool few_rows(const xpress_cache& c, int N, int R, int shared) {
-  const int64_t keys = (int64_t)N * c.Hkv * ((int64_t)c.table_ld * c.page - shared);
-  return R <= 32 || (R <= kFewRows4 && keys * c.D * c.D >= (int64_t)1 << 32);
-}
 
 size_t few_scratch_bytes(const xpress_cache& c, int N, int B, int Hq) {
   const int R = B * (Hq / c.Hkv);

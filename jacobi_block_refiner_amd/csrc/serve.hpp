@@ -46,7 +46,6 @@ hipError_t launch_block_attention(const xpress_cache& c, int layer, const void* 
                                   int shared, void* out, int64_t out_ld, float* lse, void* ws,
                                   hipStream_t s);
 
-constexpr int kFewRows4 = 64;  // query rows of a request and head that few_kernel takes at most
 size_t few_scratch_bytes(const xpress_cache& c, int N, int B, int Hq);
 hipError_t launch_block_attention4(const xpress_cache& c, int layer, const void* q, int64_t q_ld,
                                    const int32_t* seq, int N, int B, int Hq, float scale, int shared,
