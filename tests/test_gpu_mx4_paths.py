@@ -167,3 +167,46 @@ def test_own_parts_of_two_waves_beside_a_shared_part(D, ld, B, G, shared):
     c = x.cache()
     x.check(x.run(c), what=f"D {D}, {R} rows")
     x.check(x.run(c, seq=i32(order), rows=order), rows=order, what="a list")
+
+
+@pytest.mark.parametrize("dtype", [torch.bfloat16, torch.float16], ids=["bf16", "f16"])
+@pytest.mark.parametrize("N,Hkv,G,B,table", [(400, 2, 4, 1, 0), (110, 2, 5, 3, 0), (100, 1, 4, 8, 0),
+                                             (40, 2, 4, 16, 4096)])
+def test_own_parts_behind_wide_items(N, Hkv, G, B, table, dtype):
+    """So many query rows that the shared part is a launch of its own, in wide items."""
+    D, page, shared, R = 128, 16, 200, B * G
+    log(f"own parts behind wide items: {N} x {Hkv} pairs, {R} rows {dtype}")
+    lengths, picked = uneven(N, [600, 601, 64, 1, 65, 330], shared)
+    lengths[5], lengths[7] = 0, 100  # a row that does not hold the prefix
+    x = Rows(lengths, Hkv, D, dtype, shared=shared, page=page, table=table // page, seed=R)
+    assert N * R >= 1536 and few_plan.taken(D, R, N, Hkv, x.table.shape[1] * page - 192)
+    x.check(B, G, picked, f"{R} rows")
+
+
+def test_two_captured_calls_share_a_workspace():
+    """Decoding and blocks, cut in different ways, replayed in turn with eager calls between them."""
+    Hkv, D, G, dtype = 4, 128, 4, torch.bfloat16
+    lengths, _ = uneven(520, [900, 901, 640, 1, 513, 880])
+    x = Rows(lengths, Hkv, D, dtype)
+    Hq = Hkv * G
+    calls = []
+    for N, B in ((520, 1), (300, 4)):
+        assert (N * Hkv > few_plan.parts(D, B * G)) == (B == 1)
+        q = torch.randn(N * B, Hq * D, generator=torch.Generator().manual_seed(B)).to(dtype).cuda()
+        calls.append((N, B, q, torch.zeros(N * B, Hq * D, dtype=dtype, device="cuda")))
+    ws = max((xpress.attention_workspace(x.c, N, B, Hq) for N, B, _, _ in calls), key=torch.Tensor.numel)
+    want = [x.run(q, B, Hq, list(range(N)))[0] for N, B, q, _ in calls]
+    graphs = []
+    for N, B, q, out in calls:
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            xpress.block_attention(x.c, 0, q, B=B, Hq=Hq, N=N, out=out, ws=ws)
+    for turn in (0, 1, 1, 0, 1, 0):
+        out = calls[turn][3].fill_(3.0)
+        torch.cuda.synchronize()
+        graphs[turn].replay()
+        torch.cuda.synchronize()
+        assert torch.equal(out.cpu().double().view(want[turn].shape), want[turn]), turn
+        other = x.run(calls[turn][2], calls[turn][1], Hq, list(range(calls[turn][0])))[0]
+        assert torch.equal(other, want[turn])
+        ws.fill_(0xFF if turn else 0x01)
