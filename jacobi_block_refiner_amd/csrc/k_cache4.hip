@@ -206,7 +206,8 @@ __global__ __launch_bounds__(256) void read4_kernel(Lines L, const uint8_t* k, c
   }
 }
 
-// Of a cache of 16 bits: copies.
+// Of a cache of 16 bits: copies, at the rate of one (8 x 8192 tokens of 8 heads of 128, 537 MB, 102 us, 5.2
+// TB/s; 8191 tokens 11.8 us; 16 tokens 2.5).
 template <int D>
 __global__ __launch_bounds__(256) void read16_kernel(Lines L, const uint8_t* k, const uint8_t* v,
                                                      const int32_t* first, uint16_t* k_out,
