@@ -523,9 +523,9 @@ __device__ __forceinline__ void few_part(const Few& F, int block) {
   if (F.parts && !F.by_pair && lane == 0 && row0 == 0) F.cut[part] = cut;
 }
 
-// 64 requests decoding up to 32,768 tokens each (8 heads of 128, 5 queries each, 1.14 GB): 225 us, 5.1
-// TB/s (a copy reaches 4.8, reads alone 5.9). One of 1000 tokens: 8.8 us, of them 2.3 for the lengths and
-// 1.5 for the first tile of keys, and 4.1 of join_kernel.
+// 64 requests decoding up to 32,768 tokens each (8 heads of 128, 5 queries each, 1.14 GB): 220 us, 5.2
+// TB/s (a copy reaches 4.7 to 5.2, reads alone 5.9). One of 1000 tokens: 8.8 us, of them 2.3 for the lengths
+// and 1.5 for the first tile of keys, and 4.1 of join_kernel.
 template <bool F16, int D, int RT>
 __global__ __launch_bounds__(256, few_per_cu(D)) void few_kernel(Few F) {
   few_part<F16, D, RT>(F, blockIdx.x);

@@ -5,7 +5,7 @@
 // the pieces do. V's lie by pairs of channels and four tokens: between a piece (a token's four pairs) and
 // a word (a pair's four tokens) the bytes pass through LDS, so that both sides are read and written in
 // whole lines. (A thread with a piece of its own and V's bytes one by one took 128 us instead of 77 for
-// 8 x 8192 tokens of 8 heads of 128 read, whose bytes a copy passes in 71.)
+// 8 x 8192 tokens of 8 heads of 128 read, whose bytes a copy passes in 65 to 71.)
 #include "serve.hpp"
 #include "cache_mx4.hpp"
 #include "xpress_common.hpp"

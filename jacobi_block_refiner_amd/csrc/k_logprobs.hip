@@ -130,10 +130,10 @@ template <> __device__ __forceinline__ _Float16 narrow(float x) { return (_Float
 template <> __device__ __forceinline__ float narrow(float x) { return x; }
 
 // One chunk of one row, 16 KiB of 16-bit logits; each wave leaves sums of its own. Bound by HBM, close to
-// the vector unit's 290 operations a wave: 2048 rows of 151,936 ids 118 us, at the rate of a copy 130 (which
-// writes too). With quieted maxima, a join of the waves and bounds checks of every piece 430 operations,
-// and 14 us more. Workgroups that go on from chunk to chunk and ask for the next one's logits ahead
-// were slower by half.
+// the vector unit's 290 operations a wave: 2048 rows of 151,936 ids 118 us, at the rate of a copy 120 to
+// 130 (which writes too). With quieted maxima, a join of the waves and bounds checks of every piece 430
+// operations, and 14 us more. Workgroups that go on from chunk to chunk and ask for the next one's logits
+// ahead were slower by half.
 template <class T> __global__ __launch_bounds__(kThreads, 8) void chunks_kernel(Args A) {
   constexpr int E = Row<T>::E, K = kChunk / kThreads / E;  // K loads; as many lanes hold a group
   static_assert(K * E == kGroup, "a thread's ids are as many as a group's");
