@@ -23,7 +23,7 @@ int main() {
   std::mt19937 rng(1);
   const int odd[] = {INT_MIN, INT_MIN + 1, -1, 0, 1, 2, 7, 511, 512, 1 << 30, INT_MAX - 1, INT_MAX};
   for (int pairs : {1, 5, 290, 1 << 23})
-    for (int parts : {1, 2, 512, 3072}) {
+    for (int parts : {1, 2, 512, 2048}) {
       for (int a : odd)
         for (int b : odd)
           for (int c : odd)
